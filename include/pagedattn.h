@@ -15,6 +15,9 @@
  *     ("A vLLM engine small enough to read in one sitting", What it does /
  *     Key highlights: paged attention for decoding).
  *
+ * pagedattn/blocks.h declares the operations on the pools' blocks (copy, fork,
+ * free, compact).
+ *
  * Layouts (all row-major, contiguous, bf16 = IEEE bfloat16):
  *   q            [num_seqs, num_q_heads, head_dim]                 bf16
  *   k, v         [num_tokens, num_kv_heads, head_dim]              bf16
@@ -358,7 +361,11 @@ PA_API pa_status_t pa_prefill_layout(const void *q, const void *k_cache, const v
  *      skipped; nothing is written for that row;
  *   4  pa_decode / pa_decode_multi / pa_prefill: a block-table entry that
  *      covers context tokens lies outside [0, num_blocks); its rows are read
- *      as zeros, so each of those keys scores 0 and adds a zero value.
+ *      as zeros, so each of those keys scores 0 and adds a zero value;
+ *   5  a block operation: a row or block id out of range, or an owned entry
+ *      whose block had count 0; that item was skipped (fork: passed on);
+ *   6  pa_fork_blocks: a fork was refused (its child row was not empty or was
+ *      listed before, or no block was free).
  * Entries past a sequence's last block are never read and never reported.
  */
 PA_API pa_status_t pa_take_device_error(int32_t *code, void *stream);

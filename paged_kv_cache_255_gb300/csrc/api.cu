@@ -1,5 +1,5 @@
 // C ABI of libpagedattn: argument checks on the host, then kernel launches.
-// The public contract is in include/pagedattn.h.
+// The public contract is in include/pagedattn.h and include/pagedattn/.
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -7,6 +7,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/pagedattn.h"
+#include "../../include/pagedattn/blocks.h"
 #include "kernels.h"
 
 namespace {
@@ -222,6 +223,29 @@ pa_status_t prefill_impl(const void *q, const void *k_cache, const void *v_cache
     const cudaError_t e = mma ? pa::launch_prefill(a, gp, mql, st)
                               : pa::launch_prefill_tc(a, gp, mql, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// The shape of the pools a block operation works on, and their addresses.
+pa_status_t check_pools(void *const *caches, int num_caches, int num_kv_heads, int head_dim,
+                        int block_size, int64_t num_blocks) {
+    if (num_caches < 0 || num_kv_heads <= 0 || num_blocks <= 0) return PA_ERR_INVALID_ARG;
+    if (head_dim != pa::kHeadDimPublic || !block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+    if (num_kv_heads > 65535 || num_blocks > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (num_caches > 0 && !caches) return PA_ERR_INVALID_ARG;
+    for (int i = 0; i < num_caches; ++i)
+        if (!caches[i] || !aligned16(caches[i])) return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+int block_chunks_of(int num_kv_heads, int head_dim, int block_size) {
+    return block_size * num_kv_heads * (head_dim / 8);
+}
+
+pa_status_t check_workspace(const void *workspace, size_t workspace_bytes, int num_rows,
+                            int64_t num_blocks) {
+    const bool ok = workspace && aligned16(workspace) &&
+                    workspace_bytes >= pa::blocks_workspace_bytes(num_rows, num_blocks);
+    return ok ? PA_OK : PA_ERR_WORKSPACE;
 }
 
 }  // namespace
@@ -461,6 +485,115 @@ pa_status_t pa_prefill_layout(const void *q, const void *k_cache, const void *v_
                         stream);
 }
 
+pa_status_t pa_copy_blocks(void *const *caches, int num_caches, const int32_t *block_pairs,
+                           int64_t num_pairs, int num_kv_heads, int head_dim, int block_size,
+                           int64_t num_blocks, void *stream) {
+    TraceRange r("pa_copy_blocks");
+    if (num_pairs < 0) return PA_ERR_INVALID_ARG;
+    const pa_status_t chk = check_pools(caches, num_caches, num_kv_heads, head_dim, block_size, num_blocks);
+    if (chk != PA_OK) return chk;
+    if (num_pairs == 0 || num_caches == 0) return PA_OK;
+    if (!block_pairs || (reinterpret_cast<uintptr_t>(block_pairs) & 7u)) return PA_ERR_INVALID_ARG;
+    const int sms = current_sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    const cudaError_t e = pa::launch_copy_blocks(
+        caches, num_caches, block_pairs, num_pairs, num_blocks,
+        block_chunks_of(num_kv_heads, head_dim, block_size), sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+size_t pa_blocks_workspace_size(int num_rows, int64_t num_blocks) {
+    if (num_rows < 0 || num_blocks <= 0 || num_blocks > INT32_MAX) return 0;
+    return pa::blocks_workspace_bytes(num_rows, num_blocks);
+}
+
+pa_status_t pa_fork_blocks(void *const *caches, int num_caches, int32_t *block_tables,
+                           int max_blocks_per_seq, int32_t *context_lens, int num_rows,
+                           int32_t *ref_counts, const int32_t *parents, const int32_t *children,
+                           int num_forks, int num_kv_heads, int head_dim, int block_size,
+                           int64_t num_blocks, pa_layout_t layout, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    TraceRange r("pa_fork_blocks");
+    if (num_forks < 0 || num_rows < 0 || max_blocks_per_seq < 0 || num_forks > num_rows)
+        return PA_ERR_INVALID_ARG;
+    if (layout != PA_LAYOUT_TOKEN_MAJOR && layout != PA_LAYOUT_HEAD_MAJOR) return PA_ERR_INVALID_ARG;
+    pa_status_t chk = check_pools(caches, num_caches, num_kv_heads, head_dim, block_size, num_blocks);
+    if (chk != PA_OK) return chk;
+    if (num_forks == 0) return PA_OK;
+    if (!block_tables || !context_lens || !ref_counts || !parents || !children ||
+        max_blocks_per_seq == 0)
+        return PA_ERR_INVALID_ARG;
+    chk = check_workspace(workspace, workspace_bytes, num_rows, num_blocks);
+    if (chk != PA_OK) return chk;
+    const int sms = current_sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    pa::ForkArgs a{};
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.ref_counts = ref_counts;
+    a.parents = parents;
+    a.children = children;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_rows = num_rows;
+    a.num_forks = num_forks;
+    a.block_size_log2 = log2_exact(block_size);
+    a.num_kv_heads = num_kv_heads;
+    a.head_major = layout == PA_LAYOUT_HEAD_MAJOR ? 1 : 0;
+    a.block_chunks = block_chunks_of(num_kv_heads, head_dim, block_size);
+    a.num_blocks = num_blocks;
+    const cudaError_t e = pa::launch_fork_blocks(caches, num_caches, a, workspace, sms,
+                                                 static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status_t pa_free_blocks(int32_t *block_tables, int max_blocks_per_seq, int32_t *context_lens,
+                           int num_rows, int32_t *ref_counts, const int32_t *rows, int num_freed,
+                           int block_size, int64_t num_blocks, void *stream) {
+    TraceRange r("pa_free_blocks");
+    if (num_freed < 0 || num_rows < 0 || max_blocks_per_seq < 0 || num_blocks <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (!block_size_ok(block_size) || num_blocks > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (num_freed == 0) return PA_OK;
+    if (!block_tables || !context_lens || !ref_counts || !rows || max_blocks_per_seq == 0)
+        return PA_ERR_INVALID_ARG;
+    const cudaError_t e = pa::launch_free_blocks(
+        block_tables, max_blocks_per_seq, context_lens, num_rows, ref_counts, rows, num_freed,
+        log2_exact(block_size), num_blocks, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status_t pa_compact_blocks(void *const *caches, int num_caches, int32_t *block_tables,
+                              int max_blocks_per_seq, const int32_t *context_lens, int num_rows,
+                              int32_t *ref_counts, int32_t *remap, int32_t *num_live,
+                              int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                              void *workspace, size_t workspace_bytes, void *stream) {
+    TraceRange r("pa_compact_blocks");
+    if (num_rows < 0 || max_blocks_per_seq < 0) return PA_ERR_INVALID_ARG;
+    pa_status_t chk = check_pools(caches, num_caches, num_kv_heads, head_dim, block_size, num_blocks);
+    if (chk != PA_OK) return chk;
+    if (!ref_counts || !remap || !num_live) return PA_ERR_INVALID_ARG;
+    if (num_rows > 0 && (!block_tables || !context_lens || max_blocks_per_seq == 0))
+        return PA_ERR_INVALID_ARG;
+    chk = check_workspace(workspace, workspace_bytes, num_rows, num_blocks);
+    if (chk != PA_OK) return chk;
+    const int sms = current_sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    pa::CompactArgs a{};
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.ref_counts = ref_counts;
+    a.remap = remap;
+    a.num_live = num_live;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_rows = num_rows;
+    a.block_size_log2 = log2_exact(block_size);
+    a.block_chunks = block_chunks_of(num_kv_heads, head_dim, block_size);
+    a.num_blocks = num_blocks;
+    const cudaError_t e = pa::launch_compact_blocks(caches, num_caches, a, workspace, sms,
+                                                    static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 pa_status_t pa_debug_kernel_variant(int flags) {
     if (flags & ~(PA_VARIANT_DECODE_SIMT | PA_VARIANT_PREFILL_MMA)) return PA_ERR_INVALID_ARG;
     g_kernel_variant.store(flags, std::memory_order_relaxed);
@@ -479,7 +612,7 @@ pa_status_t pa_take_device_error(int32_t *code, void *stream) {
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t (*const take[])(cudaStream_t, int *) = {
         pa::take_prefill_error, pa::take_prefill_mma_error, pa::take_decode_error,
-        pa::take_store_error};
+        pa::take_store_error,      pa::take_blocks_error};
     int first = 0;
     for (auto f : take) {   // every word is read and cleared; the smallest code is reported
         int v = 0;

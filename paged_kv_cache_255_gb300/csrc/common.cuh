@@ -20,6 +20,8 @@ enum DeviceError : int {
     kErrTimeout = 2,     // prefill or decode: a bounded mbarrier wait ran out; the launch gave up
     kErrBadSlot = 3,     // store: a slot outside [-1, num_blocks * block_size) was skipped
     kErrBadBlock = 4,    // decode / prefill: a block id outside [0, num_blocks) read as zeros
+    kErrBadEntry = 5,    // block operations: a row or block id out of range, or a block with no reference
+    kErrForkRefused = 6, // fork: the child row was not empty or listed before, or no block was free
 };
 
 // Read the __device__ int `word` (of the calling file) on `stream`, wait for

@@ -136,6 +136,63 @@ bool make_pool_map(CUtensorMap *m, const void *pool, int64_t num_blocks, int blo
 bool make_tile_map(CUtensorMap *m, const void *pool, int64_t num_blocks, int block_size,
                    int num_kv_heads, bool head_major);
 
+// Pools one launch of a block operation works on (a kernel parameter).
+constexpr int kPoolsPerLaunch = 64;
+struct PoolSet {
+    uint4 *p[kPoolsPerLaunch];
+    int n;
+};
+
+// One fork (pointers are device memory; the last three lie in the workspace).
+struct ForkArgs {
+    int32_t *block_tables;      // [num_rows, max_blocks]
+    int32_t *context_lens;      // [num_rows]
+    int32_t *ref_counts;        // [num_blocks]
+    const int32_t *parents;     // [num_forks]
+    const int32_t *children;    // [num_forks]
+    int max_blocks;
+    int num_rows;
+    int num_forks;
+    int block_size_log2;
+    int num_kv_heads;
+    int head_major;
+    int block_chunks;           // 16-byte chunks of a block
+    int64_t num_blocks;
+    int4 *forks;                // [num_forks] what the plan decided
+    int32_t *claim;             // [num_rows] first fork that lists the row as its child
+    int32_t *free_ids;          // [num_forks] lowest free blocks, ascending
+};
+
+struct CompactArgs {
+    int32_t *block_tables;      // [num_rows, max_blocks]
+    const int32_t *context_lens;
+    int32_t *ref_counts;        // [num_blocks]
+    int32_t *remap;             // [num_blocks] new id of every live block, 0 for the others
+    int32_t *num_live;          // [1]
+    int max_blocks;
+    int num_rows;
+    int block_size_log2;
+    int block_chunks;
+    int64_t num_blocks;
+    int32_t *num_moves;         // workspace: [1]
+    int2 *moves;                // workspace: [num_blocks / 2] (from, to)
+};
+
+// Bytes of workspace a fork or a compaction needs.
+size_t blocks_workspace_bytes(int num_rows, int64_t num_blocks);
+
+cudaError_t launch_copy_blocks(void *const *caches, int num_caches, const int32_t *pairs,
+                               int64_t num_pairs, int64_t num_blocks, int block_chunks,
+                               int sm_count, cudaStream_t stream);
+cudaError_t launch_fork_blocks(void *const *caches, int num_caches, ForkArgs a, void *workspace,
+                               int sm_count, cudaStream_t stream);
+cudaError_t launch_free_blocks(int32_t *block_tables, int max_blocks, int32_t *context_lens,
+                               int num_rows, int32_t *ref_counts, const int32_t *rows, int num_freed,
+                               int block_size_log2, int64_t num_blocks, cudaStream_t stream);
+cudaError_t launch_compact_blocks(void *const *caches, int num_caches, CompactArgs a,
+                                  void *workspace, int sm_count, cudaStream_t stream);
+cudaError_t take_blocks_error(cudaStream_t stream, int *code);
+
 cudaError_t launch_store_kvcache(const void *k, const void *v, void *k_cache, void *v_cache,
                                  const int64_t *slot_mapping, int64_t num_tokens,
                                  int num_kv_heads, int head_dim, int block_size_log2,

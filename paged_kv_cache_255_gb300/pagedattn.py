@@ -1,8 +1,8 @@
 """Python binding of libpagedattn (ctypes): argument marshalling only.
 
 Every function here checks tensor devices, dtypes and shapes, then calls the
-C ABI declared in ``include/pagedattn.h`` with raw device pointers and the
-current torch CUDA stream. All computation happens in the library's CUDA
+C ABI declared in ``include/pagedattn.h`` and ``include/pagedattn/`` with raw
+device pointers and the current torch CUDA stream. All computation happens in the library's CUDA
 kernels; there is no fallback. If the shared library has not been built, the
 first call raises.
 """
@@ -18,7 +18,7 @@ from . import build as _build
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = range(5)
 
-# every entry point include/pagedattn.h declares, with its ctypes signature
+# every entry point the headers declare, with its ctypes signature
 _P, _I32, _I64, _F32, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
                              ctypes.c_size_t)
 SIGNATURES = {
@@ -47,6 +47,13 @@ SIGNATURES = {
                          _I64, _P, _SZ, _P], _I32),
     "pa_decode_step": ([_P, _P, _P, _I64, _P, _P, _P, _P, _I32, _P, _F32, _P, _I32, _I32, _I32,
                         _I32, _I32, _I64, _I32, _P, _SZ, _P], _I32),
+    "pa_copy_blocks": ([_P, _I32, _P, _I64, _I32, _I32, _I32, _I64, _P], _I32),
+    "pa_blocks_workspace_size": ([_I32, _I64], _SZ),
+    "pa_fork_blocks": ([_P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _I64,
+                        _I32, _P, _SZ, _P], _I32),
+    "pa_free_blocks": ([_P, _I32, _P, _I32, _P, _P, _I32, _I32, _I64, _P], _I32),
+    "pa_compact_blocks": ([_P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I64, _P,
+                           _SZ, _P], _I32),
     "pa_decode_multi_layout": ([_P, _P, _P, _P, _I32, _P, _I32, _F32, _P, _I32, _I32, _I32, _I32,
                                 _I32, _I64, _I32, _P, _SZ, _P], _I32),
 }
@@ -345,10 +352,150 @@ def prefill(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, sc
     return out
 
 
+class CachePools:
+    """The pools that share one set of block ids, normally the K and the V pool
+    of every layer: bf16 [NB, bs, Hkv, 128], or [NB, Hkv, bs, 128] with
+    ``head_major``, all of one shape on one device. Made once for the life of
+    the pools (checked here, not at every call); keeps them alive."""
+
+    def __init__(self, caches, head_major=False):
+        caches = list(caches)
+        if not caches:
+            raise ValueError("no pools")
+        dev, shape = caches[0].device, caches[0].shape
+        for c in caches:
+            _cuda(c, "cache", torch.bfloat16, dev)
+            if c.shape != shape or c.dim() != 4:
+                raise ValueError("the pools must be 4-D tensors of one shape")
+        if len({c.data_ptr() for c in caches}) != len(caches):
+            raise ValueError("a pool is listed twice")
+        self.caches, self.device, self.head_major = caches, dev, bool(head_major)
+        self.num_blocks = shape[0]
+        self.num_kv_heads, self.block_size = (shape[1], shape[2]) if head_major else (shape[2], shape[1])
+        self.head_dim = shape[3]
+        self._ptrs = (ctypes.c_void_p * len(caches))(*(c.data_ptr() for c in caches))
+        self._args = (ctypes.addressof(self._ptrs), len(caches))
+        self._shape = (self.num_kv_heads, self.head_dim, self.block_size, self.num_blocks)
+
+
+def _check_tables(block_tables, context_lens, ref_counts, dev):
+    for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"),
+                 (ref_counts, "ref_counts")):
+        _cuda(t, n, torch.int32, dev)
+    if block_tables.dim() != 2 or context_lens.shape != block_tables.shape[:1] or ref_counts.dim() != 1:
+        raise ValueError("shape mismatch between block_tables, context_lens and ref_counts")
+
+
+def _call(fn, dev, stream, *args):
+    """One library call on ``dev`` and ``stream`` (None: the current one)."""
+    st = _stream_ptr(stream, dev)
+    if torch.cuda.current_device() == dev.index:
+        _check(fn, getattr(lib(), fn)(*args, st))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, getattr(lib(), fn)(*args, st))
+
+
+def _scratch(nbytes, dev, stream):
+    """Workspace of one call from torch's allocator: calls on several streams,
+    and graphs captured apart, never share it."""
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def copy_blocks(pools: CachePools, block_pairs, stream=None):
+    """Block ``block_pairs[i, 1]`` becomes a copy of block ``block_pairs[i, 0]``
+    in every pool (int32 [n, 2]; pairs holding -1 are skipped). A block one
+    pair writes must not stand in another pair."""
+    dev = pools.device
+    _cuda(block_pairs, "block_pairs", torch.int32, dev)
+    if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
+        raise ValueError("block_pairs must be [n, 2]")
+    _call("pa_copy_blocks", dev, stream, *pools._args, block_pairs.data_ptr(),
+          block_pairs.shape[0], *pools._shape)
+
+
+def fork_blocks(pools: CachePools, block_tables, context_lens, ref_counts, parents, children,
+                workspace=None, stream=None):
+    """Row ``children[i]`` becomes a second sequence with the tokens of row
+    ``parents[i]`` (int32 [n]): full blocks are shared (their counts go up), a
+    partly filled last block is copied into the lowest free block. Changes
+    block_tables, context_lens, ref_counts and the pools in place. The child
+    rows must be empty; forks that cannot be made change nothing and are
+    recorded (take_device_error: 6)."""
+    dev = pools.device
+    _check_tables(block_tables, context_lens, ref_counts, dev)
+    _cuda(parents, "parents", torch.int32, dev)
+    _cuda(children, "children", torch.int32, dev)
+    n, (rows, width) = parents.shape[0], block_tables.shape
+    if parents.dim() != 1 or children.shape != parents.shape:
+        raise ValueError("parents and children must be [n]")
+    if ref_counts.shape[0] != pools.num_blocks:
+        raise ValueError("ref_counts must have one entry per block")
+    if n > rows:
+        raise ValueError("more forks than rows")
+    if workspace is None:
+        workspace = _scratch(lib().pa_blocks_workspace_size(rows, pools.num_blocks), dev, stream)
+    else:
+        _cuda(workspace, "workspace", workspace.dtype, dev)
+    _call("pa_fork_blocks", dev, stream, *pools._args, block_tables.data_ptr(), width,
+          context_lens.data_ptr(), rows, ref_counts.data_ptr(), parents.data_ptr(),
+          children.data_ptr(), n, *pools._shape, 1 if pools.head_major else 0,
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def free_blocks(block_tables, context_lens, ref_counts, rows, block_size: int, stream=None):
+    """The listed rows (int32 [n]; -1 is skipped) give up their blocks: counts
+    go down by one per entry, entries and lengths become 0."""
+    dev = block_tables.device
+    _check_tables(block_tables, context_lens, ref_counts, dev)
+    _cuda(rows, "rows", torch.int32, dev)
+    if rows.dim() != 1:
+        raise ValueError("rows must be [n]")
+    _call("pa_free_blocks", dev, stream, block_tables.data_ptr(), block_tables.shape[1],
+          context_lens.data_ptr(), block_tables.shape[0], ref_counts.data_ptr(), rows.data_ptr(),
+          rows.shape[0], int(block_size), ref_counts.shape[0])
+
+
+def compact_blocks(pools: CachePools, block_tables, context_lens, ref_counts, remap=None,
+                   num_live=None, workspace=None, stream=None):
+    """The live blocks move to ids 1 .. n in every pool with the fewest moves;
+    block_tables and ref_counts follow. Returns (remap, num_live): int32 [NB],
+    the new id of every live block and 0 for the others, and int32 [1], n."""
+    dev = pools.device
+    _check_tables(block_tables, context_lens, ref_counts, dev)
+    NB, (rows, width) = pools.num_blocks, block_tables.shape
+    if ref_counts.shape[0] != NB:
+        raise ValueError("ref_counts must have one entry per block")
+    outs = []
+    for t, n, size in ((remap, "remap", NB), (num_live, "num_live", 1)):
+        if t is None:
+            t = torch.empty(size, dtype=torch.int32, device=dev)
+            if stream is not None:
+                t.record_stream(stream)
+        else:
+            _cuda(t, n, torch.int32, dev)
+            if t.shape != (size,):
+                raise ValueError(f"{n} must be [{size}]")
+        outs.append(t)
+    if workspace is None:
+        workspace = _scratch(lib().pa_blocks_workspace_size(rows, NB), dev, stream)
+    else:
+        _cuda(workspace, "workspace", workspace.dtype, dev)
+    _call("pa_compact_blocks", dev, stream, *pools._args, block_tables.data_ptr(), width,
+          context_lens.data_ptr(), rows, ref_counts.data_ptr(), outs[0].data_ptr(),
+          outs[1].data_ptr(), *pools._shape, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return outs[0], outs[1]
+
+
 def take_device_error(stream=None, device=None) -> int:
-    """Synchronize the stream and return (and clear) the first device-side
-    error code a prefill launch recorded: 0 none, 1 shared memory misaligned,
-    2 a tensor-core wait ran out."""
+    """Synchronize the stream and return (and clear) the smallest device-side
+    error code recorded so far: 0 none, 1 shared memory misaligned, 2 a wait
+    ran out, 3 a bad slot, 4 a bad block id, 5 a bad row or block in a block
+    operation, 6 a fork refused."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     code = ctypes.c_int32(0)
     with torch.cuda.device(dev):
