@@ -16,7 +16,7 @@
  *     Key highlights: paged attention for decoding).
  *
  * pagedattn/blocks.h declares the operations on the pools' blocks (copy, fork,
- * free, compact).
+ * free, compact), pagedattn/decode_shared.h decode over shared prefixes.
  *
  * Layouts (all row-major, contiguous, bf16 = IEEE bfloat16):
  *   q            [num_seqs, num_q_heads, head_dim]                 bf16

@@ -8,7 +8,9 @@
 
 #include "../../include/pagedattn.h"
 #include "../../include/pagedattn/blocks.h"
+#include "../../include/pagedattn/decode_shared.h"
 #include "kernels.h"
+#include "shared.h"
 
 namespace {
 
@@ -109,6 +111,33 @@ int plan_workers(int group_pad, pa::DecodeKernel k, int num_partitions) {
     return P;
 }
 
+// The arguments of a decode launch, but for the split and the workspace.
+pa::DecodeArgs decode_args(const void *q, const void *k_cache, const void *v_cache,
+                           const int32_t *block_tables, int max_blocks_per_seq,
+                           const int32_t *context_lens, int q_len, float scale, void *out,
+                           int num_seqs, int num_q_heads, int num_kv_heads, int block_size,
+                           int64_t num_blocks, int layout) {
+    pa::DecodeArgs a{};
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.out = out;
+    a.num_seqs = num_seqs;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.group = num_q_heads / num_kv_heads;
+    a.q_len = q_len;
+    a.cols = a.group * q_len;
+    a.block_size_log2 = log2_exact(block_size);
+    a.head_major = layout == PA_LAYOUT_HEAD_MAJOR ? 1 : 0;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634);   // scale * log2(e)
+    return a;
+}
+
 pa_status_t decode_impl(const void *q, const void *k_cache, const void *v_cache,
                         const int32_t *block_tables, int max_blocks_per_seq,
                         const int32_t *context_lens, int q_len, float scale, void *out,
@@ -122,8 +151,7 @@ pa_status_t decode_impl(const void *q, const void *k_cache, const void *v_cache,
         num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, layout,
         num_partitions, &nothing_to_do);
     if (chk != PA_OK || nothing_to_do) return chk;
-    const int group = num_q_heads / num_kv_heads;
-    const int gp = pa::decode_group_pad(group * q_len);
+    const int gp = pa::decode_group_pad(num_q_heads / num_kv_heads * q_len);
 
     const pa::DecodeKernel kind = decode_kernel_choice(gp, q_len);
     const int P = plan_workers(gp, kind, num_partitions);
@@ -131,24 +159,9 @@ pa_status_t decode_impl(const void *q, const void *k_cache, const void *v_cache,
     if (!workspace || !aligned16(workspace) || workspace_bytes < pa::decode_workspace_bytes(gp, P))
         return PA_ERR_WORKSPACE;
 
-    pa::DecodeArgs a{};
-    a.q = q;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.block_tables = block_tables;
-    a.context_lens = context_lens;
-    a.out = out;
-    a.num_seqs = num_seqs;
-    a.num_q_heads = num_q_heads;
-    a.num_kv_heads = num_kv_heads;
-    a.group = group;
-    a.q_len = q_len;
-    a.cols = group * q_len;
-    a.block_size_log2 = log2_exact(block_size);
-    a.head_major = layout == PA_LAYOUT_HEAD_MAJOR ? 1 : 0;
-    a.max_blocks_per_seq = max_blocks_per_seq;
-    a.num_blocks = num_blocks;
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634);   // scale * log2(e)
+    pa::DecodeArgs a = decode_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                                   context_lens, q_len, scale, out, num_seqs, num_q_heads,
+                                   num_kv_heads, block_size, num_blocks, layout);
     a.num_workers = P;
     a.min_tiles = num_partitions > 0 ? 1 : pa::kDefaultMinTiles;
     a.plan_early = plan_early ? 1 : 0;
@@ -224,6 +237,8 @@ pa_status_t prefill_impl(const void *q, const void *k_cache, const void *v_cache
                               : pa::launch_prefill_tc(a, gp, mql, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // The shape of the pools a block operation works on, and their addresses.
 pa_status_t check_pools(void *const *caches, int num_caches, int num_kv_heads, int head_dim,
@@ -458,6 +473,60 @@ pa_status_t pa_decode_step(const void *k, const void *v, const int64_t *slot_map
                        num_blocks, layout, workspace, workspace_bytes, 0, stream, !no_store);
 }
 
+size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_heads,
+                                       int num_kv_heads, int head_dim) {
+    if (num_seqs < 0 || num_groups < 0 || num_groups > pa::kSharedMaxGroups) return 0;
+    const size_t dec = pa_decode_workspace_size(num_q_heads, num_kv_heads, head_dim, 0);
+    const int sms = current_sm_count();
+    if (dec == 0 || sms <= 0) return 0;
+    return round256(dec) + pa::shared_workspace_bytes(num_seqs, num_groups, num_kv_heads,
+                                                      pa::decode_group_pad(num_q_heads / num_kv_heads), sms);
+}
+
+pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_cache,
+                             const int32_t *block_tables, int max_blocks_per_seq,
+                             const int32_t *context_lens, const int32_t *group_starts,
+                             const int32_t *prefix_blocks, int num_groups, float scale, void *out,
+                             int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                             int block_size, int64_t num_blocks, pa_layout_t layout,
+                             void *workspace, size_t workspace_bytes, void *stream) {
+    TraceRange r("pa_decode_shared");
+    if (num_groups < 0) return PA_ERR_INVALID_ARG;
+    bool nothing_to_do = false;
+    const pa_status_t chk = pa::decode_check_args(
+        q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, 1, scale, out, num_seqs,
+        num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, layout, 0, &nothing_to_do);
+    if (chk != PA_OK) return chk;
+    if (num_groups > pa::kSharedMaxGroups) return PA_ERR_UNSUPPORTED;
+    if (nothing_to_do || num_groups == 0) return PA_OK;
+    if (!group_starts || !prefix_blocks) return PA_ERR_INVALID_ARG;
+    const int gp = pa::decode_group_pad(num_q_heads / num_kv_heads);
+    const int P = plan_workers(gp, pa::DecodeKernel::kMma, 0);
+    const int sms = current_sm_count();
+    if (P <= 0 || sms <= 0) return PA_ERR_CUDA;
+    const size_t dec = round256(pa::decode_workspace_bytes(gp, P));
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < dec + pa::shared_workspace_bytes(num_seqs, num_groups, num_kv_heads, gp, sms))
+        return PA_ERR_WORKSPACE;
+    pa::DecodeArgs a = decode_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                                   context_lens, 1, scale, out, num_seqs, num_q_heads, num_kv_heads,
+                                   block_size, num_blocks, layout);
+    a.num_workers = P;
+    a.min_tiles = pa::kDefaultMinTiles;
+    pa::decode_carve_workspace(a, workspace, gp);
+    pa::SharedArgs sh{};
+    sh.group_starts = group_starts;
+    sh.prefix_blocks = prefix_blocks;
+    sh.num_groups = num_groups;
+    sh.group_pad = gp;
+    sh.max_workers = sms;
+    pa::shared_carve_workspace(sh, static_cast<char *>(workspace) + dec, num_seqs, num_kv_heads);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = pa::launch_shared_prefix(a, sh, st);
+    if (e == cudaSuccess) e = pa::launch_decode_shared(a, sh, gp, st);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 pa_status_t pa_prefill(const void *q, const void *k_cache, const void *v_cache,
                        const int32_t *block_tables, int max_blocks_per_seq,
                        const int32_t *context_lens, const int32_t *query_start_loc,
@@ -612,7 +681,8 @@ pa_status_t pa_take_device_error(int32_t *code, void *stream) {
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t (*const take[])(cudaStream_t, int *) = {
         pa::take_prefill_error, pa::take_prefill_mma_error, pa::take_decode_error,
-        pa::take_store_error,      pa::take_blocks_error};
+        pa::take_store_error,      pa::take_blocks_error,
+        pa::take_shared_error};
     int first = 0;
     for (auto f : take) {   // every word is read and cleared; the smallest code is reported
         int v = 0;

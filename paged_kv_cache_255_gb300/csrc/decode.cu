@@ -33,13 +33,19 @@
 //   * SimtTile: the same on the CUDA cores, lane l owning dims [4l, 4l + 4);
 //     kept as the comparison and a second parity path, selected only by the
 //     test hook pa_debug_kernel_variant.
+// With shared prefixes (decode_shared_kernel) a unit is only what follows the
+// tokens its group's prefix covers, and the share that holds the unit's first
+// tile folds the prefix's (m, l, o), left by shared.cu, into its own at the
+// end. The tiles do not need the prefix, so they stream while its kernel ends.
 // The kernels never wait on one another inside a launch; a warp waits only on
 // its own copies, and every such wait is bounded (1 s, then the launch records
 // code 2 and the warp exits).
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "shared.h"
 #include "tcgen05.cuh"
 
 namespace pa {
@@ -116,6 +122,27 @@ __device__ __forceinline__ int unit_tiles(int L) { return L > 0 ? (L + 15) >> 4 
 struct Cursor {
     int s, kvh, j, nt, L;
 };
+// With shared prefixes the unit's tiles begin at token `start`, a multiple of 16.
+struct SharedCursor : Cursor {
+    int start;
+};
+__device__ __forceinline__ int first_token(const Cursor &c) { return c.j << 4; }
+__device__ __forceinline__ int first_token(const SharedCursor &c) { return c.start + (c.j << 4); }
+
+__device__ __forceinline__ void cursor_advance(SharedCursor &c, const DecodeArgs &a,
+                                               const SharedArgs &sh, int s_hi, int max_len) {
+    if (++c.j == c.nt) {
+        c.j = 0;
+        if (++c.kvh == a.num_kv_heads) {
+            c.kvh = 0;
+            if (++c.s < s_hi) {
+                c.L = clamp_len(a.context_lens, c.s, max_len);
+                c.start = __ldcg(&sh.seq[c.s].x);
+                c.nt = unit_tiles(c.L - c.start);
+            }
+        }
+    }
+}
 
 __device__ __forceinline__ void cursor_advance(Cursor &c, const DecodeArgs &a, int max_len) {
     if (++c.j == c.nt) {
@@ -130,16 +157,18 @@ __device__ __forceinline__ void cursor_advance(Cursor &c, const DecodeArgs &a, i
     }
 }
 
-__device__ __forceinline__ int tile_valid(const Cursor &c) {
-    int v = c.L - (c.j << 4);
+template <class C>
+__device__ __forceinline__ int tile_valid(const C &c) {
+    int v = c.L - first_token(c);
     return v < 0 ? 0 : (v > 16 ? 16 : v);
 }
 
 // Physical block of the tile under the cursor (0 when the tile has no tokens).
-__device__ __forceinline__ int tile_block(const Cursor &c, const DecodeArgs &a) {
+template <class C>
+__device__ __forceinline__ int tile_block(const C &c, const DecodeArgs &a) {
     if (tile_valid(c) == 0) return 0;
     return __ldg(a.block_tables + (int64_t)c.s * a.max_blocks_per_seq +
-                 ((c.j << 4) >> a.block_size_log2));
+                 (first_token(c) >> a.block_size_log2));
 }
 
 // Fill `stage` with the K tile and the V tile under cursor c (physical block
@@ -148,7 +177,8 @@ __device__ __forceinline__ int tile_block(const Cursor &c, const DecodeArgs &a) 
 // with zeros by the warp instead (each of its keys then scores 0 and adds a
 // zero value) and `bar` gets a plain arrival. The stage's previous contents
 // must have been read by every lane (the __syncwarp below orders that).
-__device__ __forceinline__ void issue_tile(const Cursor &c, int bid, uint8_t *stage, uint32_t bar,
+template <class C>
+__device__ __forceinline__ void issue_tile(const C &c, int bid, uint8_t *stage, uint32_t bar,
                                            const DecodeArgs &a, const CUtensorMap *mk,
                                            const CUtensorMap *mv, int lane) {
     const int valid = tile_valid(c);
@@ -162,7 +192,7 @@ __device__ __forceinline__ void issue_tile(const Cursor &c, int bid, uint8_t *st
         if (tc::elect_one()) {
             // token-major pool: (0, block * bs + offset, 0, KV head);
             // head-major pool: (0, offset, 0, block * Hkv + KV head)
-            const int off = (c.j << 4) & ((1 << a.block_size_log2) - 1);
+            const int off = first_token(c) & ((1 << a.block_size_log2) - 1);
             const int row = a.head_major ? off : (bid << a.block_size_log2) + off;
             const int outer = a.head_major ? bid * a.num_kv_heads + c.kvh : c.kvh;
             const uint32_t dst = smem_u32(stage);
@@ -337,6 +367,12 @@ struct MmaTile {
     // running max and total sum in sm_m / sm_l. `scr` is a free 8 KB stage.
     __device__ __forceinline__ void finish(float *scr, float *sm_m, float *sm_l, float (&oc)[GP][4],
                                            int lane) {
+        put(scr, sm_m, sm_l, lane);
+        take(scr, oc, lane);
+    }
+
+    // The two halves of finish: o[h][0 .. 127] in scr[h], and back.
+    __device__ __forceinline__ void put(float *scr, float *sm_m, float *sm_l, int lane) {
         const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -371,6 +407,8 @@ struct MmaTile {
             }
         }
         __syncwarp();
+    }
+    __device__ __forceinline__ void take(const float *scr, float (&oc)[GP][4], int lane) {
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
             const float4 v = reinterpret_cast<const float4 *>(scr + h * kHeadDim)[lane];
@@ -535,17 +573,19 @@ struct Layout {
 
 // CTA prologue: the total tile count W, the share count actually used, and
 // the position (sequence, KV head, tile) of this warp's first tile.
-__device__ __forceinline__ void plan_share(const DecodeArgs &a, int max_len, int64_t &W,
-                                           int &p_eff, int64_t &T0, int64_t &T1, Cursor &c) {
+// `lo`, `hi`: the sequences the call covers; `tiles(s)`: those of one unit of s.
+template <class Tiles>
+__device__ __forceinline__ void plan_share(const DecodeArgs &a, int max_len, int lo, int hi,
+                                           Tiles tiles, int64_t &W, int &p_eff, int64_t &T0,
+                                           int64_t &T1, Cursor &c) {
     __shared__ long long s_wsum[kWarps];
     __shared__ long long s_scan[kWarps * 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = a.num_seqs, Hkv = a.num_kv_heads;
+    const int Hkv = a.num_kv_heads;
 
     // pass 1: total tiles
     long long local = 0;
-    for (int s = threadIdx.x; s < S; s += kWarps * 32)
-        local += unit_tiles(clamp_len(a.context_lens, s, max_len));
+    for (int s = lo + threadIdx.x; s < hi; s += kWarps * 32) local += tiles(s);
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) local += __shfl_xor_sync(0xffffffffu, local, m);
     if (lane == 0) s_wsum[warp] = local;
@@ -572,9 +612,9 @@ __device__ __forceinline__ void plan_share(const DecodeArgs &a, int max_len, int
     // the sequence holding tile T0
     bool found = T0 >= T1;
     long long base = 0;
-    for (int c0 = 0; c0 < S; c0 += kWarps * 32) {
+    for (int c0 = lo; c0 < hi; c0 += kWarps * 32) {
         const int s = c0 + threadIdx.x;
-        long long v = s < S ? unit_tiles(clamp_len(a.context_lens, s, max_len)) : 0;
+        long long v = s < hi ? tiles(s) : 0;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const long long n = __shfl_up_sync(0xffffffffu, v, off);
@@ -625,10 +665,95 @@ __device__ __forceinline__ void prefetch_inputs(const DecodeArgs &a) {
     }
 }
 
-template <class Tile, int GP>
-__global__ void __launch_bounds__(kWarps * 32)
-decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmap_k,
-              const __grid_constant__ CUtensorMap tmap_v) {
+// Fold the prefix of unit (s, kvh) into the unit's own part: o[h] in scr[h],
+// the columns' running max and sum in sm_m / sm_l; lane l handles dims
+// [4l, 4l + 4). The prefix is one row of unit_o or, when several CTAs shared
+// its keys, one row per CTA in part_o. Up to eight 16-byte loads are in flight
+// per lane, and the sources are merged in the order of their keys. Not inlined:
+// it runs once per unit, and inlined it took the tile loop's registers
+// (254 instead of 152 for groups of 8, two CTAs on an SM instead of three).
+template <int GP>
+__device__ __noinline__ void merge_prefix(const DecodeArgs &a, const SharedArgs &sh, int s, int kvh,
+                                          float *scr, float *sm_m, float *sm_l) {
+    constexpr int kPairSeqs = kPairRows / GP;
+    constexpr int kCols = GP < 4 ? GP : 4;          // columns merged together
+    constexpr int kBatch = 8 / kCols < 4 ? 8 / kCols : 4;   // sources loaded together
+    const int lane = threadIdx.x & 31;
+    const int act = __ldcg(&sh.seq[s].y);
+    if (act < 0) return;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");    // the prefix kernel is complete
+    const SharedHeader hdr = *sh.hdr;
+    const SharedGroup gr = sh.groups[act];
+    const int tok = s - gr.s0, pair = tok / kPairSeqs;
+    const int64_t U0 = gr.base + ((int64_t)kvh * gr.pairs + pair) * gr.nt;
+    // share w of the tile space is [w tiles / workers, (w + 1) tiles / workers)
+    const int w0 = (int)(((U0 + 1) * hdr.workers - 1) / hdr.tiles);
+    const int w1 = (int)(((U0 + gr.nt) * hdr.workers - 1) / hdr.tiles);
+    const bool whole = w0 == w1;
+    const int64_t unit_rows = (int64_t)a.num_seqs * GP;
+    const int64_t stride = whole ? unit_rows : kPairRows;
+    const int64_t row = whole ? (int64_t)s * GP : (tok - pair * kPairSeqs) * GP;
+    // part_o: share w's slot 2 w holds its first piece, 2 w + 1 its last; only
+    // share w0 may have begun before the unit
+    const int64_t slot0 = 2 * (int64_t)w0 + ((int64_t)w0 * hdr.tiles / hdr.workers < U0 ? 1 : 0);
+    const float4 *po = (whole ? sh.unit_o + (int64_t)kvh * 32 * unit_rows : sh.part_o) + lane * stride + row;
+    const float2 *pml = (whole ? sh.unit_ml + kvh * unit_rows : sh.part_ml) + row;
+    const int n = 1 + w1 - w0;
+    for (int h0 = 0; h0 < a.cols; h0 += kCols) {
+        float m[kCols], l[kCols];
+        float4 x[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+            m[c] = sm_m[h0 + c];
+            l[c] = sm_l[h0 + c];
+            x[c] = reinterpret_cast<const float4 *>(scr + (h0 + c) * kHeadDim)[lane];
+        }
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+            float4 o[kBatch][kCols];
+            float2 e[kBatch][kCols];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int64_t at = whole ? 0 : (i0 + k == 0 ? slot0 : 2 * (int64_t)(w0 + i0 + k)) * kPairRows;
+#pragma unroll
+                for (int c = 0; c < kCols; ++c)
+                    if (i0 + k < n && h0 + c < a.cols) {
+                        o[k][c] = po[at * 32 + h0 + c];
+                        e[k][c] = pml[at + h0 + c];
+                    }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                for (int c = 0; c < kCols; ++c)
+                    if (i0 + k < n && h0 + c < a.cols) {
+                        const float mn = fmaxf(m[c], e[k][c].x);
+                        const float ms = mn == kNegInf ? 0.f : mn;
+                        const float al = ex2(m[c] - ms), be = ex2(e[k][c].x - ms);
+                        l[c] = l[c] * al + e[k][c].y * be;
+                        x[c].x = x[c].x * al + o[k][c].x * be;
+                        x[c].y = x[c].y * al + o[k][c].y * be;
+                        x[c].z = x[c].z * al + o[k][c].z * be;
+                        x[c].w = x[c].w * al + o[k][c].w * be;
+                        m[c] = mn;
+                    }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+            reinterpret_cast<float4 *>(scr + (h0 + c) * kHeadDim)[lane] = x[c];
+            if (lane == 0) {
+                sm_m[h0 + c] = m[c];
+                sm_l[h0 + c] = l[c];
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// What the two kernels have in common; SHARED takes `sh` into account.
+template <class Tile, int GP, bool SHARED>
+__device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArgs &sh,
+                                            const CUtensorMap &tmap_k, const CUtensorMap &tmap_v) {
     using Lay = Layout<Tile, GP>;
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -655,8 +780,14 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmap_k,
     // let the combine launch queue up behind this grid. When the previous
     // kernel is known to be this step's store (plan_early), which writes the
     // caches only, the split of the work is planned from the lengths first.
+    // With shared prefixes the previous kernel is the prefixes', whose CTAs have
+    // all waited for everything before them: only its results are waited for,
+    // where they are merged, and by every thread before it ends, so that what
+    // follows this grid follows that one too.
     prefetch_inputs(a);
-    if (!a.plan_early) {
+    if (SHARED) {
+        asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    } else if (!a.plan_early) {
         asm volatile("griddepcontrol.wait;\n" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     }
@@ -665,25 +796,42 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmap_k,
                                  (int64_t)0x7fffffff);
     int64_t W, T0, T1;
     int p_eff;
-    Cursor cc{0, 0, 0, 1, 0};
-    plan_share(a, max_len, W, p_eff, T0, T1, cc);
-    if (a.plan_early) {
+    typename std::conditional<SHARED, SharedCursor, Cursor>::type cc{};
+    cc.nt = 1;
+    int s_hi = a.num_seqs;
+    if constexpr (SHARED) {
+        const int s_lo = __ldcg(&sh.hdr->s_lo);
+        s_hi = __ldcg(&sh.hdr->s_hi);
+        plan_share(a, max_len, s_lo, s_hi, [&](int s) {
+            return unit_tiles(clamp_len(a.context_lens, s, max_len) - __ldcg(&sh.seq[s].x));
+        }, W, p_eff, T0, T1, cc);
+        if (T0 < T1) cc.start = __ldcg(&sh.seq[cc.s].x);
+    } else {
+        plan_share(a, max_len, 0, s_hi, [&](int s) {
+            return unit_tiles(clamp_len(a.context_lens, s, max_len));
+        }, W, p_eff, T0, T1, cc);
+    }
+    if (!SHARED && a.plan_early) {
         asm volatile("griddepcontrol.wait;\n" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     }
     const int w = blockIdx.x * kWarps + warp;
-    if (w >= a.num_workers) return;
-    if (T0 >= T1) {
-        if (lane == 0) a.tasks[w] = make_int4(-1, 0, 0, 0);
+    if (w >= a.num_workers || T0 >= T1) {
+        if (w < a.num_workers && lane == 0) a.tasks[w] = make_int4(-1, 0, 0, 0);
+        if (SHARED) asm volatile("griddepcontrol.wait;\n" ::: "memory");
         return;
     }
+    auto advance = [&](auto &c) {
+        if constexpr (SHARED) cursor_advance(c, a, sh, s_hi, max_len);
+        else cursor_advance(c, a, max_len);
+    };
 
     uint32_t *outg = static_cast<uint32_t *>(a.out);
     uint32_t phase = 0;      // bit i: parity of stage i's next barrier phase
     uint32_t pending = 0;    // bit i: stage i has been filled and not yet waited for
 
     // producer: runs kStages - 1 tiles ahead of the consumer
-    Cursor pc = cc;
+    auto pc = cc;
     int64_t Tp = T0;
     int p_bid = tile_block(pc, a);
     int stage_p = 0;
@@ -693,7 +841,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmap_k,
             issue_tile(pc, p_bid, ring + stage_p * kStageBytes, bar0 + 8 * stage_p, a, &tmap_k,
                        &tmap_v, lane);
             pending |= 1u << stage_p;
-            cursor_advance(pc, a, max_len);
+            advance(pc);
             ++Tp;
             p_bid = Tp < T1 ? tile_block(pc, a) : 0;
         }
@@ -714,7 +862,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmap_k,
             issue_tile(pc, p_bid, ring + stage_p * kStageBytes, bar0 + 8 * stage_p, a, &tmap_k,
                        &tmap_v, lane);
             pending |= 1u << stage_p;
-            cursor_advance(pc, a, max_len);
+            advance(pc);
             ++Tp;
             p_bid = Tp < T1 ? tile_block(pc, a) : 0;
         }
@@ -736,7 +884,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmap_k,
         uint8_t *stage = ring + stage_c * kStageBytes;
         const int valid = tile_valid(cc);
         if (valid > 0 && valid < 16) zero_v_tail(stage + kTileBytes, valid, lane);
-        tl.tile(stage, cc.j << 4, a.scale_log2, scratch, lane);
+        tl.tile(stage, first_token(cc), a.scale_log2, scratch, lane);
         stage_c = stage_c + 1 == kStages ? 0 : stage_c + 1;
 
         const bool unit_end = cc.j == cc.nt - 1;
@@ -745,7 +893,14 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmap_k,
             // it serves as transpose scratch here
             float oc[GP][4];
             __syncwarp();
-            tl.finish(reinterpret_cast<float *>(stage), sm_m, sm_l, oc, lane);
+            float *scr = reinterpret_cast<float *>(stage);
+            if constexpr (SHARED) {
+                tl.put(scr, sm_m, sm_l, lane);
+                if (piece_j0 == 0) merge_prefix<GP>(a, sh, cc.s, cc.kvh, scr, sm_m, sm_l);
+                tl.take(scr, oc, lane);
+            } else {
+                tl.finish(scr, sm_m, sm_l, oc, lane);
+            }
             tc::fence_proxy_async();     // the TMA that refills the stage lands after these stores
             __syncwarp();
             if (piece_j0 == 0 && unit_end) {
@@ -783,7 +938,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmap_k,
             ++piece;
             fresh = true;
         }
-        cursor_advance(cc, a, max_len);
+        advance(cc);
     }
     if (failed) {
         // a copy did not land in time: record it, give the copies still in
@@ -795,6 +950,23 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmap_k,
         task = make_int4(-1, 0, 0, 0);
     }
     if (lane == 0) a.tasks[w] = task;
+    if (SHARED) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+
+template <class Tile, int GP>
+__global__ void __launch_bounds__(kWarps * 32)
+decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmap_k,
+              const __grid_constant__ CUtensorMap tmap_v) {
+    decode_body<Tile, GP, false>(a, SharedArgs{}, tmap_k, tmap_v);
+}
+
+// Three CTAs on an SM, as decode_kernel (two for groups of 16).
+template <int GP>
+__global__ void __launch_bounds__(kWarps * 32, GP > 8 ? 2 : 3)
+decode_shared_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ SharedArgs sh,
+                     const __grid_constant__ CUtensorMap tmap_k,
+                     const __grid_constant__ CUtensorMap tmap_v) {
+    decode_body<MmaTile<GP>, GP, true>(a, sh, tmap_k, tmap_v);
 }
 
 // Log-sum-exp merge of the pieces of each split unit. Block (x, y) holds
@@ -885,8 +1057,12 @@ struct Launcher {
         cfg.numAttrs = 1;
         return cudaLaunchKernelExC(&cfg, fn, args);
     }
-    static cudaError_t launch(const DecodeArgs &a, cudaStream_t st) {
-        cudaError_t e = prepare();
+    // `sh` null: the plain decode. With shared prefixes the tiles are MmaTile's.
+    static cudaError_t launch(const DecodeArgs &a, cudaStream_t st, const SharedArgs *sh = nullptr) {
+        cudaError_t e = sh ? cudaFuncSetAttribute(decode_shared_kernel<GP>,
+                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  Lay::kCtaBytes)
+                           : prepare();
         if (e != cudaSuccess) return e;
         CUtensorMap mk, mv;
         const int bs = 1 << a.block_size_log2;
@@ -895,9 +1071,12 @@ struct Launcher {
             return cudaErrorInvalidValue;
         const unsigned grid = (a.num_workers + kWarps - 1) / kWarps;
         DecodeArgs args_copy = a;
+        SharedArgs sh_copy = sh ? *sh : SharedArgs{};
         void *dargs[] = {&args_copy, &mk, &mv};
-        e = launch_pdl(reinterpret_cast<const void *>(&decode_kernel<Tile, GP>), dim3(grid),
-                       kWarps * 32, Lay::kCtaBytes, dargs, st);
+        void *sargs[] = {&args_copy, &sh_copy, &mk, &mv};
+        e = launch_pdl(sh ? reinterpret_cast<const void *>(&decode_shared_kernel<GP>)
+                          : reinterpret_cast<const void *>(&decode_kernel<Tile, GP>),
+                       dim3(grid), kWarps * 32, Lay::kCtaBytes, sh ? sargs : dargs, st);
         if (e != cudaSuccess) return e;
         void *cargs[] = {&args_copy};
         e = launch_pdl(reinterpret_cast<const void *>(&combine_kernel<GP>),
@@ -971,6 +1150,18 @@ void decode_carve_workspace(DecodeArgs &a, void *workspace, int group_pad) {
     a.part_ml = reinterpret_cast<float *>(p);
     p += 2 * P * group_pad * 2 * sizeof(float);
     a.tasks = reinterpret_cast<int4 *>(p);
+}
+
+cudaError_t launch_decode_shared(const DecodeArgs &a, const SharedArgs &sh, int group_pad,
+                                 cudaStream_t stream) {
+    switch (group_pad) {
+        case 1: return Launcher<MmaTile<1>, 1>::launch(a, stream, &sh);
+        case 2: return Launcher<MmaTile<2>, 2>::launch(a, stream, &sh);
+        case 4: return Launcher<MmaTile<4>, 4>::launch(a, stream, &sh);
+        case 8: return Launcher<MmaTile<8>, 8>::launch(a, stream, &sh);
+        case 16: return Launcher<MmaTile<16>, 16>::launch(a, stream, &sh);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 cudaError_t launch_decode(const DecodeArgs &a, int group_pad, DecodeKernel k, cudaStream_t stream) {

@@ -1,0 +1,58 @@
+// Plan, buffers and launches of decode over shared prefixes (shared.cu plans
+// and computes the prefixes, decode.cu the rest of every sequence).
+#pragma once
+
+#include "kernels.h"
+
+namespace pa {
+
+constexpr int kSharedMaxGroups = 4096;  // groups of one call (the plan keeps 20 bytes each in shared memory)
+constexpr int kSharedMinSeqs = 2;       // a prefix is computed apart for at least this many sequences
+constexpr int kPairRows = 256;      // rows of a prefix unit: two query tiles of 128
+
+// A group whose prefix is computed once. Its tile space: (KV head, pair of
+// query tiles, key tile), the key tile fastest, from `base` on.
+struct alignas(16) SharedGroup {
+    int64_t base;       // flat index of the group's first key tile
+    int row;            // table row the prefix is read through
+    int s0, n;          // its sequences
+    int tokens;         // prefix tokens computed together, a multiple of 16
+    int nt, pairs;      // key tiles of 128; pairs of query tiles
+};
+static_assert(sizeof(SharedGroup) == 32, "one 32-byte sector");
+
+struct SharedHeader {
+    int64_t tiles;          // key tiles of all active groups
+    int num_active;
+    int s_lo, s_hi;         // sequences the call covers
+    int workers;            // shares the tiles are cut into
+};
+
+// Pointers are device memory.
+struct SharedArgs {
+    const int32_t *group_starts;    // [num_groups + 1]
+    const int32_t *prefix_blocks;   // [num_groups]
+    int num_groups;
+    int group_pad;                  // G: query heads per KV head, rounded up to a power of two
+    int max_workers;                // CTAs of the prefix kernel
+    // in the workspace
+    SharedHeader *hdr;
+    int2 *seq;                      // [S] tokens computed with the group's prefix, active group or -1
+    SharedGroup *groups;            // [num_groups] the active ones
+    float4 *part_o;                 // [2 max_workers][32][256] pieces of units that several workers share
+    float2 *part_ml;                // [2 max_workers][256] (running max in log2 units, sum)
+    float4 *unit_o;                 // [Hkv][32][S G] units one worker computed whole
+    float2 *unit_ml;                // [Hkv][S G]
+};
+
+size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_kv_heads, int group_pad,
+                              int sm_count);
+void shared_carve_workspace(SharedArgs &sh, void *workspace, int num_seqs, int num_kv_heads);
+
+// Plan and prefixes, then (launch_decode_shared) the rest and the combine.
+cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t stream);
+cudaError_t launch_decode_shared(const DecodeArgs &a, const SharedArgs &sh, int group_pad,
+                                 cudaStream_t stream);
+cudaError_t take_shared_error(cudaStream_t stream, int *code);
+
+}  // namespace pa

@@ -47,6 +47,9 @@ SIGNATURES = {
                          _I64, _P, _SZ, _P], _I32),
     "pa_decode_step": ([_P, _P, _P, _I64, _P, _P, _P, _P, _I32, _P, _F32, _P, _I32, _I32, _I32,
                         _I32, _I32, _I64, _I32, _P, _SZ, _P], _I32),
+    "pa_decode_shared_workspace_size": ([_I32, _I32, _I32, _I32, _I32], _SZ),
+    "pa_decode_shared": ([_P, _P, _P, _P, _I32, _P, _P, _P, _I32, _F32, _P, _I32, _I32, _I32, _I32,
+                          _I32, _I64, _I32, _P, _SZ, _P], _I32),
     "pa_copy_blocks": ([_P, _I32, _P, _I64, _I32, _I32, _I32, _I64, _P], _I32),
     "pa_blocks_workspace_size": ([_I32, _I64], _SZ),
     "pa_fork_blocks": ([_P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _I64,
@@ -309,6 +312,63 @@ def decode_multi(q, k_cache, v_cache, block_tables, context_lens, scale, out=Non
                                           workspace.data_ptr(), ws_bytes, _stream_ptr(stream, dev))
     _check("pa_decode_multi_layout", st)
     return out
+
+
+def decode_shared(q, k_cache, v_cache, block_tables, context_lens, group_starts, prefix_blocks, scale,
+                  out=None, workspace=None, stream=None, head_major=False):
+    """Single-token decode for sequences in groups that share their first
+    blocks; returns ``out`` (bf16 [S, Hq, D]).
+
+    group_starts: int32 [G + 1]; group g is sequences group_starts[g] ..
+    group_starts[g + 1] - 1, whose first prefix_blocks[g] (int32 [G]) table
+    entries are the same. The prefix is read once per group; the results are
+    decode's, but for the order of the sums. Rows of ``out`` outside all groups
+    are left as they were. The other arguments are decode's."""
+    dev = q.device
+    for t, n, dt in ((q, "q", torch.bfloat16), (k_cache, "k_cache", torch.bfloat16),
+                     (v_cache, "v_cache", torch.bfloat16), (block_tables, "block_tables", torch.int32),
+                     (context_lens, "context_lens", torch.int32),
+                     (group_starts, "group_starts", torch.int32),
+                     (prefix_blocks, "prefix_blocks", torch.int32)):
+        _cuda(t, n, dt, dev)
+    S, Hq, D = q.shape
+    if head_major:
+        NB, Hkv, bs, D2 = k_cache.shape
+    else:
+        NB, bs, Hkv, D2 = k_cache.shape
+    G = prefix_blocks.shape[0]
+    if v_cache.shape != k_cache.shape or D2 != D or block_tables.dim() != 2 \
+            or block_tables.shape[0] != S or context_lens.shape != (S,) \
+            or prefix_blocks.dim() != 1 or group_starts.shape != (G + 1,):
+        raise ValueError("shape mismatch between q, caches, block_tables, context_lens and groups")
+    if out is None:
+        out = torch.empty_like(q)
+        if stream is not None:
+            out.record_stream(stream)
+    else:
+        _cuda(out, "out", torch.bfloat16, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if workspace is None:
+        workspace = _scratch(decode_shared_workspace_size(S, G, Hq, Hkv, D, dev), dev, stream)
+    else:
+        _cuda(workspace, "workspace", workspace.dtype, dev)
+    _call("pa_decode_shared", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+          group_starts.data_ptr(), prefix_blocks.data_ptr(), G, float(scale), out.data_ptr(), S, Hq, Hkv,
+          D, bs, NB, 1 if head_major else 0, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return out
+
+
+def decode_shared_workspace_size(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int,
+                                 head_dim: int = 128, device=None) -> int:
+    """Workspace bytes pa_decode_shared needs on ``device`` (default: current)."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        n = lib().pa_decode_shared_workspace_size(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim)
+    if n == 0:
+        raise ValueError("unsupported head configuration or number of groups")
+    return int(n)
 
 
 def prefill(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
