@@ -479,7 +479,7 @@ size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_h
     const size_t dec = pa_decode_workspace_size(num_q_heads, num_kv_heads, head_dim, 0);
     const int sms = current_sm_count();
     if (dec == 0 || sms <= 0) return 0;
-    return round256(dec) + pa::shared_workspace_bytes(num_seqs, num_groups, num_kv_heads,
+    return round256(dec) + pa::shared_workspace_bytes(num_seqs, num_groups, num_q_heads, num_kv_heads,
                                                       pa::decode_group_pad(num_q_heads / num_kv_heads), sms);
 }
 
@@ -506,7 +506,8 @@ pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_c
     if (P <= 0 || sms <= 0) return PA_ERR_CUDA;
     const size_t dec = round256(pa::decode_workspace_bytes(gp, P));
     if (!workspace || !aligned16(workspace) ||
-        workspace_bytes < dec + pa::shared_workspace_bytes(num_seqs, num_groups, num_kv_heads, gp, sms))
+        workspace_bytes < dec + pa::shared_workspace_bytes(num_seqs, num_groups, num_q_heads,
+                                                           num_kv_heads, gp, sms))
         return PA_ERR_WORKSPACE;
     pa::DecodeArgs a = decode_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                                    context_lens, 1, scale, out, num_seqs, num_q_heads, num_kv_heads,
@@ -520,7 +521,7 @@ pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_c
     sh.num_groups = num_groups;
     sh.group_pad = gp;
     sh.max_workers = sms;
-    pa::shared_carve_workspace(sh, static_cast<char *>(workspace) + dec, num_seqs, num_kv_heads);
+    pa::shared_carve_workspace(sh, static_cast<char *>(workspace) + dec, a);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = pa::launch_shared_prefix(a, sh, st);
     if (e == cudaSuccess) e = pa::launch_decode_shared(a, sh, gp, st);

@@ -34,9 +34,10 @@
 //     kept as the comparison and a second parity path, selected only by the
 //     test hook pa_debug_kernel_variant.
 // With shared prefixes (decode_shared_kernel) a unit is only what follows the
-// tokens its group's prefix covers, and the share that holds the unit's first
-// tile folds the prefix's (m, l, o), left by shared.cu, into its own at the
-// end. The tiles do not need the prefix, so they stream while its kernel ends.
+// tokens its group's prefix covers. A unit that has a prefix is left in fp32
+// even when one share holds it whole, and combine_shared_kernel merges it with
+// the prefix's (m, l, o), left by shared.cu. The two kernels before it do not
+// need one another.
 // The kernels never wait on one another inside a launch; a warp waits only on
 // its own copies, and every such wait is bounded (1 s, then the launch records
 // code 2 and the warp exits).
@@ -367,12 +368,6 @@ struct MmaTile {
     // running max and total sum in sm_m / sm_l. `scr` is a free 8 KB stage.
     __device__ __forceinline__ void finish(float *scr, float *sm_m, float *sm_l, float (&oc)[GP][4],
                                            int lane) {
-        put(scr, sm_m, sm_l, lane);
-        take(scr, oc, lane);
-    }
-
-    // The two halves of finish: o[h][0 .. 127] in scr[h], and back.
-    __device__ __forceinline__ void put(float *scr, float *sm_m, float *sm_l, int lane) {
         const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -407,8 +402,6 @@ struct MmaTile {
             }
         }
         __syncwarp();
-    }
-    __device__ __forceinline__ void take(const float *scr, float (&oc)[GP][4], int lane) {
 #pragma unroll
         for (int h = 0; h < GP; ++h) {
             const float4 v = reinterpret_cast<const float4 *>(scr + h * kHeadDim)[lane];
@@ -665,91 +658,6 @@ __device__ __forceinline__ void prefetch_inputs(const DecodeArgs &a) {
     }
 }
 
-// Fold the prefix of unit (s, kvh) into the unit's own part: o[h] in scr[h],
-// the columns' running max and sum in sm_m / sm_l; lane l handles dims
-// [4l, 4l + 4). The prefix is one row of unit_o or, when several CTAs shared
-// its keys, one row per CTA in part_o. Up to eight 16-byte loads are in flight
-// per lane, and the sources are merged in the order of their keys. Not inlined:
-// it runs once per unit, and inlined it took the tile loop's registers
-// (254 instead of 152 for groups of 8, two CTAs on an SM instead of three).
-template <int GP>
-__device__ __noinline__ void merge_prefix(const DecodeArgs &a, const SharedArgs &sh, int s, int kvh,
-                                          float *scr, float *sm_m, float *sm_l) {
-    constexpr int kPairSeqs = kPairRows / GP;
-    constexpr int kCols = GP < 4 ? GP : 4;          // columns merged together
-    constexpr int kBatch = 8 / kCols < 4 ? 8 / kCols : 4;   // sources loaded together
-    const int lane = threadIdx.x & 31;
-    const int act = __ldcg(&sh.seq[s].y);
-    if (act < 0) return;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");    // the prefix kernel is complete
-    const SharedHeader hdr = *sh.hdr;
-    const SharedGroup gr = sh.groups[act];
-    const int tok = s - gr.s0, pair = tok / kPairSeqs;
-    const int64_t U0 = gr.base + ((int64_t)kvh * gr.pairs + pair) * gr.nt;
-    // share w of the tile space is [w tiles / workers, (w + 1) tiles / workers)
-    const int w0 = (int)(((U0 + 1) * hdr.workers - 1) / hdr.tiles);
-    const int w1 = (int)(((U0 + gr.nt) * hdr.workers - 1) / hdr.tiles);
-    const bool whole = w0 == w1;
-    const int64_t unit_rows = (int64_t)a.num_seqs * GP;
-    const int64_t stride = whole ? unit_rows : kPairRows;
-    const int64_t row = whole ? (int64_t)s * GP : (tok - pair * kPairSeqs) * GP;
-    // part_o: share w's slot 2 w holds its first piece, 2 w + 1 its last; only
-    // share w0 may have begun before the unit
-    const int64_t slot0 = 2 * (int64_t)w0 + ((int64_t)w0 * hdr.tiles / hdr.workers < U0 ? 1 : 0);
-    const float4 *po = (whole ? sh.unit_o + (int64_t)kvh * 32 * unit_rows : sh.part_o) + lane * stride + row;
-    const float2 *pml = (whole ? sh.unit_ml + kvh * unit_rows : sh.part_ml) + row;
-    const int n = 1 + w1 - w0;
-    for (int h0 = 0; h0 < a.cols; h0 += kCols) {
-        float m[kCols], l[kCols];
-        float4 x[kCols];
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-            m[c] = sm_m[h0 + c];
-            l[c] = sm_l[h0 + c];
-            x[c] = reinterpret_cast<const float4 *>(scr + (h0 + c) * kHeadDim)[lane];
-        }
-        for (int i0 = 0; i0 < n; i0 += kBatch) {
-            float4 o[kBatch][kCols];
-            float2 e[kBatch][kCols];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int64_t at = whole ? 0 : (i0 + k == 0 ? slot0 : 2 * (int64_t)(w0 + i0 + k)) * kPairRows;
-#pragma unroll
-                for (int c = 0; c < kCols; ++c)
-                    if (i0 + k < n && h0 + c < a.cols) {
-                        o[k][c] = po[at * 32 + h0 + c];
-                        e[k][c] = pml[at + h0 + c];
-                    }
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-                for (int c = 0; c < kCols; ++c)
-                    if (i0 + k < n && h0 + c < a.cols) {
-                        const float mn = fmaxf(m[c], e[k][c].x);
-                        const float ms = mn == kNegInf ? 0.f : mn;
-                        const float al = ex2(m[c] - ms), be = ex2(e[k][c].x - ms);
-                        l[c] = l[c] * al + e[k][c].y * be;
-                        x[c].x = x[c].x * al + o[k][c].x * be;
-                        x[c].y = x[c].y * al + o[k][c].y * be;
-                        x[c].z = x[c].z * al + o[k][c].z * be;
-                        x[c].w = x[c].w * al + o[k][c].w * be;
-                        m[c] = mn;
-                    }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-            reinterpret_cast<float4 *>(scr + (h0 + c) * kHeadDim)[lane] = x[c];
-            if (lane == 0) {
-                sm_m[h0 + c] = m[c];
-                sm_l[h0 + c] = l[c];
-            }
-        }
-    }
-    __syncwarp();
-}
-
 // What the two kernels have in common; SHARED takes `sh` into account.
 template <class Tile, int GP, bool SHARED>
 __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArgs &sh,
@@ -781,9 +689,9 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
     // kernel is known to be this step's store (plan_early), which writes the
     // caches only, the split of the work is planned from the lengths first.
     // With shared prefixes the previous kernel is the prefixes', whose CTAs have
-    // all waited for everything before them: only its results are waited for,
-    // where they are merged, and by every thread before it ends, so that what
-    // follows this grid follows that one too.
+    // all waited for everything before them and whose results nothing here
+    // reads: every thread waits for it only before it ends, so that what follows
+    // this grid follows that one too.
     prefetch_inputs(a);
     if (SHARED) {
         asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -817,7 +725,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
     }
     const int w = blockIdx.x * kWarps + warp;
     if (w >= a.num_workers || T0 >= T1) {
-        if (w < a.num_workers && lane == 0) a.tasks[w] = make_int4(-1, 0, 0, 0);
+        if (!SHARED && w < a.num_workers && lane == 0) a.tasks[w] = make_int4(-1, 0, 0, 0);
         if (SHARED) asm volatile("griddepcontrol.wait;\n" ::: "memory");
         return;
     }
@@ -893,17 +801,29 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
             // it serves as transpose scratch here
             float oc[GP][4];
             __syncwarp();
-            float *scr = reinterpret_cast<float *>(stage);
-            if constexpr (SHARED) {
-                tl.put(scr, sm_m, sm_l, lane);
-                if (piece_j0 == 0) merge_prefix<GP>(a, sh, cc.s, cc.kvh, scr, sm_m, sm_l);
-                tl.take(scr, oc, lane);
-            } else {
-                tl.finish(scr, sm_m, sm_l, oc, lane);
-            }
+            tl.finish(reinterpret_cast<float *>(stage), sm_m, sm_l, oc, lane);
             tc::fence_proxy_async();     // the TMA that refills the stage lands after these stores
             __syncwarp();
-            if (piece_j0 == 0 && unit_end) {
+            bool prefixed = false;
+            if constexpr (SHARED) prefixed = cc.start > 0;
+            if (SHARED && piece_j0 == 0 && lane == 0) {
+                // how the combine finds the unit's parts: {first slot, last
+                // share, first share}, slot -1: whole in own_o, -2: nothing left
+                const int64_t unit_end_T = T - cc.j + cc.nt;
+                sh.units[(int64_t)cc.s * a.num_kv_heads + cc.kvh] =
+                    unit_end ? make_int4(prefixed ? -1 : -2, w, w, 0)
+                             : make_int4(2 * w + (piece == 0 ? 0 : 1),
+                                         (int)((unit_end_T * p_eff - 1) / W), w, 0);
+            }
+            if (prefixed && piece_j0 == 0 && unit_end) {
+#pragma unroll
+                for (int h = 0; h < GP; ++h)
+                    if (h < a.cols) {
+                        const int64_t row = (int64_t)cc.s * a.num_q_heads + (int64_t)cc.kvh * a.group + h;
+                        sh.own_o[row * 32 + lane] = make_float4(oc[h][0], oc[h][1], oc[h][2], oc[h][3]);
+                        if (lane == 0) sh.own_ml[row] = make_float2(sm_m[h], sm_l[h]);
+                    }
+            } else if (piece_j0 == 0 && unit_end) {
                 // the whole unit is in this share: normalise and write bf16
 #pragma unroll
                 for (int h = 0; h < GP; ++h) {
@@ -927,7 +847,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
                 if (lane < GP)
                     reinterpret_cast<float2 *>(a.part_ml)[(int64_t)slot * GP + lane] =
                         make_float2(sm_m[lane], sm_l[lane]);
-                if (piece_j0 == 0) {
+                if (!SHARED && piece_j0 == 0) {
                     // this share holds the unit's first tile: it owns the combine
                     const int64_t unit_end_T = piece_T + cc.nt;
                     const int w_last = (int)((unit_end_T * p_eff - 1) / W);
@@ -949,7 +869,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
             if ((pending >> i) & 1u && i != stage_c) warp_wait(bar0 + 8 * i, (phase >> i) & 1u, lane);
         task = make_int4(-1, 0, 0, 0);
     }
-    if (lane == 0) a.tasks[w] = task;
+    if (!SHARED && lane == 0) a.tasks[w] = task;
     if (SHARED) asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
 
@@ -963,8 +883,7 @@ decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmap_k,
 // Three CTAs on an SM, as decode_kernel (two for groups of 16).
 template <int GP>
 __global__ void __launch_bounds__(kWarps * 32, GP > 8 ? 2 : 3)
-decode_shared_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ SharedArgs sh,
-                     const __grid_constant__ CUtensorMap tmap_k,
+decode_shared_kernel(const DecodeArgs a, const SharedArgs sh, const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v) {
     decode_body<MmaTile<GP>, GP, true>(a, sh, tmap_k, tmap_v);
 }
@@ -1025,6 +944,100 @@ __global__ void __launch_bounds__(128) combine_kernel(const DecodeArgs a) {
     reinterpret_cast<uint2 *>(static_cast<uint32_t *>(a.out) + col_row(a, task.x, task.y, h) / 2)[lane] = pk;
 }
 
+// Running merge of parts in the order they come: (m, l, o) of a set of keys.
+struct Merge {
+    float m = kNegInf, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void add(const float2 e, const float4 p) {
+        if (e.y == 0.f) return;             // no visible token in the part
+        const float mn = fmaxf(m, e.x);
+        const float al = ex2(m - mn), be = ex2(e.x - mn);
+        l = l * al + e.y * be;
+        o.x = o.x * al + p.x * be;
+        o.y = o.y * al + p.y * be;
+        o.z = o.z * al + p.z * be;
+        o.w = o.w * al + p.w * be;
+        m = mn;
+    }
+};
+
+// Parts [0, n) of one output row, `at(i)` giving part i's place in `o` (in
+// float4, this lane's word) and `ml`; a batch's loads are all in flight before
+// its merge.
+template <class At>
+__device__ __forceinline__ void merge_parts(Merge &acc, int n, const float4 *o, const float2 *ml, At at) {
+    for (int i0 = 0; i0 < n; i0 += kCombineBatch) {
+        float2 e[kCombineBatch];
+        float4 p[kCombineBatch];
+#pragma unroll
+        for (int k = 0; k < kCombineBatch; ++k)
+            if (i0 + k < n) {
+                const longlong2 x = at(i0 + k);
+                p[k] = o[x.x];
+                e[k] = ml[x.y];
+            }
+#pragma unroll
+        for (int k = 0; k < kCombineBatch; ++k)
+            if (i0 + k < n) acc.add(e[k], p[k]);
+    }
+}
+
+// With shared prefixes: one CTA per (sequence, KV head) unit, one warp per
+// query head. The prefix's parts, then the unit's own; lane l handles dims
+// [4l, 4l + 4). A prefix computed whole by one CTA is a row of unit_o, one that
+// several CTAs shared a row of part_o per CTA. Both are [dim / 4][row], and the
+// rows of a unit's heads lie side by side, so the warps of a CTA share sectors.
+template <int GP>
+__global__ void __launch_bounds__(GP * 32)
+combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    constexpr int kPairSeqs = kPairRows / GP;
+    const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = blockIdx.x / a.num_kv_heads, kvh = blockIdx.x - s * a.num_kv_heads;
+    const SharedHeader hdr = *sh.hdr;
+    if (s < hdr.s_lo || s >= hdr.s_hi || h >= a.cols) return;
+    const int4 u = sh.units[blockIdx.x];
+    if (u.x == -2) return;
+    Merge acc;
+    const int act = sh.seq[s].y;
+    if (act >= 0) {
+        const SharedGroup gr = sh.groups[act];
+        const int tok = s - gr.s0, pair = tok / kPairSeqs;
+        const int64_t U0 = gr.base + ((int64_t)kvh * gr.pairs + pair) * gr.nt;
+        // share w of the tile space is [w tiles / workers, (w + 1) tiles / workers)
+        const int w0 = (int)(((U0 + 1) * hdr.workers - 1) / hdr.tiles);
+        const int w1 = (int)(((U0 + gr.nt) * hdr.workers - 1) / hdr.tiles);
+        if (w0 == w1) {
+            const int64_t rows = (int64_t)a.num_seqs * GP, row = (int64_t)s * GP + h;
+            acc.add(sh.unit_ml[kvh * rows + row], sh.unit_o[((int64_t)kvh * 32 + lane) * rows + row]);
+        } else {
+            // share w's slot 2 w holds its first piece, 2 w + 1 its last; only
+            // share w0 may have begun before the unit
+            const int64_t slot0 = 2 * (int64_t)w0 + ((int64_t)w0 * hdr.tiles / hdr.workers < U0 ? 1 : 0);
+            const int row = (tok - pair * kPairSeqs) * GP + h;
+            merge_parts(acc, 1 + w1 - w0, sh.part_o, sh.part_ml, [&](int i) {
+                const int64_t slot = i == 0 ? slot0 : 2 * (int64_t)(w0 + i);
+                return make_longlong2((slot * 32 + lane) * kPairRows + row, slot * kPairRows + row);
+            });
+        }
+    }
+    if (u.x == -1) {
+        const int64_t row = (int64_t)s * a.num_q_heads + (int64_t)kvh * a.group + h;
+        acc.add(sh.own_ml[row], sh.own_o[row * 32 + lane]);
+    } else {
+        merge_parts(acc, 1 + u.y - u.z, reinterpret_cast<const float4 *>(a.part_o),
+                    reinterpret_cast<const float2 *>(a.part_ml), [&](int i) {
+            const int64_t slot = i == 0 ? u.x : 2 * (int64_t)(u.z + i);
+            return make_longlong2((slot * GP + h) * 32 + lane, slot * GP + h);
+        });
+    }
+    const float inv = acc.l > 0.f ? 1.f / acc.l : 0.f;
+    uint2 pk;
+    pk.x = pack_bf16x2(acc.o.x * inv, acc.o.y * inv);
+    pk.y = pack_bf16x2(acc.o.z * inv, acc.o.w * inv);
+    reinterpret_cast<uint2 *>(static_cast<uint32_t *>(a.out) + col_row(a, s, kvh, h) / 2)[lane] = pk;
+}
+
 template <class Tile, int GP>
 struct Launcher {
     using Lay = Layout<Tile, GP>;
@@ -1078,6 +1091,11 @@ struct Launcher {
                           : reinterpret_cast<const void *>(&decode_kernel<Tile, GP>),
                        dim3(grid), kWarps * 32, Lay::kCtaBytes, sh ? sargs : dargs, st);
         if (e != cudaSuccess) return e;
+        if (sh) {
+            e = launch_pdl(reinterpret_cast<const void *>(&combine_shared_kernel<GP>),
+                           dim3(a.num_seqs * a.num_kv_heads), GP * 32, 0, sargs, st);
+            return e != cudaSuccess ? e : cudaGetLastError();
+        }
         void *cargs[] = {&args_copy};
         e = launch_pdl(reinterpret_cast<const void *>(&combine_kernel<GP>),
                        dim3((a.num_workers + 3) / 4, a.cols), 128, 0, cargs, st);

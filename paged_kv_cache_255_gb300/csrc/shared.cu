@@ -790,9 +790,9 @@ cudaError_t launch_g(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t st)
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct Carve {
-    size_t hdr, seq, groups, part_o, part_ml, unit_o, unit_ml, end;
-    Carve(int S, int G, int hkv, int gp, int workers) {
-        const size_t rows = (size_t)S * gp * hkv, slots = 2 * (size_t)workers;
+    size_t hdr, seq, groups, part_o, part_ml, unit_o, unit_ml, units, own_o, own_ml, end;
+    Carve(int S, int G, int hq, int hkv, int gp, int workers) {
+        const size_t rows = (size_t)S * gp * hkv, own = (size_t)S * hq, slots = 2 * (size_t)workers;
         hdr = 0;
         seq = hdr + round256(sizeof(SharedHeader));
         groups = seq + round256((size_t)S * sizeof(int2));
@@ -800,7 +800,10 @@ struct Carve {
         part_ml = part_o + slots * 32 * kPairRows * sizeof(float4);
         unit_o = part_ml + slots * kPairRows * sizeof(float2);
         unit_ml = unit_o + rows * 32 * sizeof(float4);
-        end = unit_ml + round256(rows * sizeof(float2));
+        units = unit_ml + round256(rows * sizeof(float2));
+        own_o = units + round256((size_t)S * hkv * sizeof(int4));
+        own_ml = own_o + own * 32 * sizeof(float4);
+        end = own_ml + round256(own * sizeof(float2));
     }
 };
 
@@ -810,13 +813,13 @@ cudaError_t take_shared_error(cudaStream_t stream, int *code) {
     return take_device_word(g_shared_error, stream, code);
 }
 
-size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_kv_heads, int group_pad,
-                              int sm_count) {
-    return Carve(num_seqs, num_groups, num_kv_heads, group_pad, sm_count).end;
+size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
+                              int group_pad, int sm_count) {
+    return Carve(num_seqs, num_groups, num_q_heads, num_kv_heads, group_pad, sm_count).end;
 }
 
-void shared_carve_workspace(SharedArgs &sh, void *workspace, int num_seqs, int num_kv_heads) {
-    const Carve c(num_seqs, sh.num_groups, num_kv_heads, sh.group_pad, sh.max_workers);
+void shared_carve_workspace(SharedArgs &sh, void *workspace, const DecodeArgs &a) {
+    const Carve c(a.num_seqs, sh.num_groups, a.num_q_heads, a.num_kv_heads, sh.group_pad, sh.max_workers);
     char *p = static_cast<char *>(workspace);
     sh.hdr = reinterpret_cast<SharedHeader *>(p + c.hdr);
     sh.seq = reinterpret_cast<int2 *>(p + c.seq);
@@ -825,6 +828,9 @@ void shared_carve_workspace(SharedArgs &sh, void *workspace, int num_seqs, int n
     sh.part_ml = reinterpret_cast<float2 *>(p + c.part_ml);
     sh.unit_o = reinterpret_cast<float4 *>(p + c.unit_o);
     sh.unit_ml = reinterpret_cast<float2 *>(p + c.unit_ml);
+    sh.units = reinterpret_cast<int4 *>(p + c.units);
+    sh.own_o = reinterpret_cast<float4 *>(p + c.own_o);
+    sh.own_ml = reinterpret_cast<float2 *>(p + c.own_ml);
 }
 
 cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t stream) {

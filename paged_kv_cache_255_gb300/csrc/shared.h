@@ -43,11 +43,14 @@ struct SharedArgs {
     float2 *part_ml;                // [2 max_workers][256] (running max in log2 units, sum)
     float4 *unit_o;                 // [Hkv][32][S G] units one worker computed whole
     float2 *unit_ml;                // [Hkv][S G]
+    int4 *units;                    // [S Hkv] where a unit's own parts are (decode.cu)
+    float4 *own_o;                  // [S Hq][32] own part of units one share computed whole
+    float2 *own_ml;                 // [S Hq]
 };
 
-size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_kv_heads, int group_pad,
-                              int sm_count);
-void shared_carve_workspace(SharedArgs &sh, void *workspace, int num_seqs, int num_kv_heads);
+size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
+                              int group_pad, int sm_count);
+void shared_carve_workspace(SharedArgs &sh, void *workspace, const DecodeArgs &a);
 
 // Plan and prefixes, then (launch_decode_shared) the rest and the combine.
 cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t stream);
