@@ -566,19 +566,17 @@ struct Layout {
 
 // CTA prologue: the total tile count W, the share count actually used, and
 // the position (sequence, KV head, tile) of this warp's first tile.
-// `lo`, `hi`: the sequences the call covers; `tiles(s)`: those of one unit of s.
-template <class Tiles>
-__device__ __forceinline__ void plan_share(const DecodeArgs &a, int max_len, int lo, int hi,
-                                           Tiles tiles, int64_t &W, int &p_eff, int64_t &T0,
-                                           int64_t &T1, Cursor &c) {
+__device__ __forceinline__ void plan_share(const DecodeArgs &a, int max_len, int64_t &W,
+                                           int &p_eff, int64_t &T0, int64_t &T1, Cursor &c) {
     __shared__ long long s_wsum[kWarps];
     __shared__ long long s_scan[kWarps * 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int Hkv = a.num_kv_heads;
+    const int S = a.num_seqs, Hkv = a.num_kv_heads;
 
     // pass 1: total tiles
     long long local = 0;
-    for (int s = lo + threadIdx.x; s < hi; s += kWarps * 32) local += tiles(s);
+    for (int s = threadIdx.x; s < S; s += kWarps * 32)
+        local += unit_tiles(clamp_len(a.context_lens, s, max_len));
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) local += __shfl_xor_sync(0xffffffffu, local, m);
     if (lane == 0) s_wsum[warp] = local;
@@ -605,9 +603,9 @@ __device__ __forceinline__ void plan_share(const DecodeArgs &a, int max_len, int
     // the sequence holding tile T0
     bool found = T0 >= T1;
     long long base = 0;
-    for (int c0 = lo; c0 < hi; c0 += kWarps * 32) {
+    for (int c0 = 0; c0 < S; c0 += kWarps * 32) {
         const int s = c0 + threadIdx.x;
-        long long v = s < hi ? tiles(s) : 0;
+        long long v = s < S ? unit_tiles(clamp_len(a.context_lens, s, max_len)) : 0;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const long long n = __shfl_up_sync(0xffffffffu, v, off);
@@ -639,6 +637,55 @@ __device__ __forceinline__ void plan_share(const DecodeArgs &a, int max_len, int
         base = chunk_end;
         __syncthreads();
     }
+}
+
+// The same with shared prefixes: the plan kernel has left the scan of the
+// units' tiles (sh.scan, through sequence s), the total and the share count; a
+// CTA stages the scan in its ring and each warp searches it.
+__device__ __forceinline__ void plan_shared(const DecodeArgs &a, const SharedArgs &sh, int max_len,
+                                            long long *stage, int64_t &W, int &p_eff, int64_t &T0,
+                                            int64_t &T1, int &s_hi, SharedCursor &c) {
+    constexpr int kChunk = kWarps * kRingBytes / 8;
+    const int warp = threadIdx.x >> 5, Hkv = a.num_kv_heads;
+    const int s_lo = __ldcg(&sh.hdr->s_lo);
+    s_hi = __ldcg(&sh.hdr->s_hi);
+    W = __ldcg(&sh.hdr->own_tiles);
+    p_eff = __ldcg(&sh.hdr->own_workers);
+    const int w = blockIdx.x * kWarps + warp;
+    T0 = T1 = W;
+    if (w < p_eff) {
+        T0 = (int64_t)w * W / p_eff;
+        T1 = (int64_t)(w + 1) * W / p_eff;
+    }
+    bool found = T0 >= T1;
+    long long before = 0;               // tiles before the chunk
+    for (int c0 = s_lo; c0 < s_hi; c0 += kChunk) {
+        const int n = s_hi - c0 < kChunk ? s_hi - c0 : kChunk;
+        for (int i = threadIdx.x; i < n; i += kWarps * 32) stage[i] = __ldcg(sh.scan + c0 + i);
+        __syncthreads();
+        const long long end = stage[n - 1];
+        if (!found && T0 < end * Hkv) {
+            int lo = 0, hi = n - 1;     // the first sequence whose tiles end past T0
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (stage[mid] * Hkv > T0) hi = mid; else lo = mid + 1;
+            }
+            const long long excl = lo == 0 ? before : stage[lo - 1];
+            const long long nt = stage[lo] - excl, rem = T0 - excl * Hkv;
+            c.s = c0 + lo;
+            c.nt = (int)nt;
+            c.kvh = (int)(rem / nt);
+            c.j = (int)(rem - c.kvh * nt);
+            c.L = clamp_len(a.context_lens, c.s, max_len);
+            c.start = __ldcg(&sh.seq[c.s].x);
+            found = true;
+        }
+        before = end;
+        __syncthreads();
+    }
+    // the stage is a TMA destination next
+    tc::fence_proxy_async();
+    __syncthreads();
 }
 
 // L2 prefetch of context_lens, block_tables and q, in 128-byte lines spread
@@ -707,18 +754,10 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
     typename std::conditional<SHARED, SharedCursor, Cursor>::type cc{};
     cc.nt = 1;
     int s_hi = a.num_seqs;
-    if constexpr (SHARED) {
-        const int s_lo = __ldcg(&sh.hdr->s_lo);
-        s_hi = __ldcg(&sh.hdr->s_hi);
-        plan_share(a, max_len, s_lo, s_hi, [&](int s) {
-            return unit_tiles(clamp_len(a.context_lens, s, max_len) - __ldcg(&sh.seq[s].x));
-        }, W, p_eff, T0, T1, cc);
-        if (T0 < T1) cc.start = __ldcg(&sh.seq[cc.s].x);
-    } else {
-        plan_share(a, max_len, 0, s_hi, [&](int s) {
-            return unit_tiles(clamp_len(a.context_lens, s, max_len));
-        }, W, p_eff, T0, T1, cc);
-    }
+    if constexpr (SHARED)
+        plan_shared(a, sh, max_len, reinterpret_cast<long long *>(smem), W, p_eff, T0, T1, s_hi, cc);
+    else
+        plan_share(a, max_len, W, p_eff, T0, T1, cc);
     if (!SHARED && a.plan_early) {
         asm volatile("griddepcontrol.wait;\n" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -961,81 +1000,100 @@ struct Merge {
     }
 };
 
-// Parts [0, n) of one output row, `at(i)` giving part i's place in `o` (in
-// float4, this lane's word) and `ml`; a batch's loads are all in flight before
-// its merge.
+// Parts [0, n) of one output row, `at(i)` giving part i's places in `o` and
+// `ml`; a batch's loads are all in flight before its merge.
 template <class At>
 __device__ __forceinline__ void merge_parts(Merge &acc, int n, const float4 *o, const float2 *ml, At at) {
-    for (int i0 = 0; i0 < n; i0 += kCombineBatch) {
-        float2 e[kCombineBatch];
-        float4 p[kCombineBatch];
+    constexpr int kBatch = 4;
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+        float2 e[kBatch];
+        float4 p[kBatch];
 #pragma unroll
-        for (int k = 0; k < kCombineBatch; ++k)
+        for (int k = 0; k < kBatch; ++k)
             if (i0 + k < n) {
                 const longlong2 x = at(i0 + k);
                 p[k] = o[x.x];
                 e[k] = ml[x.y];
             }
 #pragma unroll
-        for (int k = 0; k < kCombineBatch; ++k)
+        for (int k = 0; k < kBatch; ++k)
             if (i0 + k < n) acc.add(e[k], p[k]);
     }
 }
 
-// With shared prefixes: one CTA per (sequence, KV head) unit, one warp per
-// query head. The prefix's parts, then the unit's own; lane l handles dims
-// [4l, 4l + 4). A prefix computed whole by one CTA is a row of unit_o, one that
-// several CTAs shared a row of part_o per CTA. Both are [dim / 4][row], and the
-// rows of a unit's heads lie side by side, so the warps of a CTA share sectors.
+// With shared prefixes: the prefix's parts of an output row, then its own. A
+// prefix computed whole by one CTA is a row of unit_o, one that several CTAs
+// shared a row of part_o per CTA, both [dim / 4][row]. A CTA takes 8 rows
+// (sequence, head of the group) of one KV head, a thread 4 dims of a row: a
+// warp's 8 rows x 4 words are whole 128-byte lines of those arrays, and whole
+// sectors of the others and of `out`. (One warp per row, each lane in a line of
+// its own, took 17 us instead of 5 for 8192 rows of 6 parts.)
+// What does not depend on the two kernels before is looked up while they run.
 template <int GP>
-__global__ void __launch_bounds__(GP * 32)
-combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+__global__ void __launch_bounds__(256, 4) combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
     constexpr int kPairSeqs = kPairRows / GP;
-    const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = blockIdx.x / a.num_kv_heads, kvh = blockIdx.x - s * a.num_kv_heads;
-    const SharedHeader hdr = *sh.hdr;
-    if (s < hdr.s_lo || s >= hdr.s_hi || h >= a.cols) return;
-    const int4 u = sh.units[blockIdx.x];
-    if (u.x == -2) return;
-    Merge acc;
-    const int act = sh.seq[s].y;
-    if (act >= 0) {
-        const SharedGroup gr = sh.groups[act];
-        const int tok = s - gr.s0, pair = tok / kPairSeqs;
-        const int64_t U0 = gr.base + ((int64_t)kvh * gr.pairs + pair) * gr.nt;
-        // share w of the tile space is [w tiles / workers, (w + 1) tiles / workers)
-        const int w0 = (int)(((U0 + 1) * hdr.workers - 1) / hdr.tiles);
-        const int w1 = (int)(((U0 + gr.nt) * hdr.workers - 1) / hdr.tiles);
-        if (w0 == w1) {
-            const int64_t rows = (int64_t)a.num_seqs * GP, row = (int64_t)s * GP + h;
-            acc.add(sh.unit_ml[kvh * rows + row], sh.unit_o[((int64_t)kvh * 32 + lane) * rows + row]);
-        } else {
+    struct Row {
+        int prefix_parts, prefix_row;   // 0: none, 1: whole in unit_o, else pieces
+        int64_t slot0, w0;
+    };
+    __shared__ Row s_row[8];
+    const int word = threadIdx.x >> 3;                  // dims [4 word, 4 word + 4)
+    const int64_t rows = (int64_t)a.num_seqs * GP;
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x & 7);
+    const int kvh = blockIdx.y;
+    const int s = (int)(row / GP), h = (int)(row % GP);
+    const bool mine = row < rows && h < a.cols && s >= __ldcg(&sh.hdr->s_lo) && s < __ldcg(&sh.hdr->s_hi);
+    if (threadIdx.x < 8 && mine) {
+        Row r{0, 0, 0, 0};
+        const int act = __ldcg(&sh.seq[s].y);
+        if (act >= 0) {
+            const int64_t tiles = __ldcg(&sh.hdr->tiles);
+            const int workers = __ldcg(&sh.hdr->workers);
+            const SharedGroup *g = sh.groups + act;
+            const int tok = s - __ldcg(&g->s0), pair = tok / kPairSeqs, nt = __ldcg(&g->nt);
+            const int64_t U0 = __ldcg(&g->base) + ((int64_t)kvh * __ldcg(&g->pairs) + pair) * nt;
+            // share w of the tile space is [w tiles / workers, (w + 1) tiles / workers)
+            const int w0 = (int)(((U0 + 1) * workers - 1) / tiles);
+            const int w1 = (int)(((U0 + nt) * workers - 1) / tiles);
+            r.prefix_parts = 1 + w1 - w0;
+            r.prefix_row = (tok - pair * kPairSeqs) * GP + h;
             // share w's slot 2 w holds its first piece, 2 w + 1 its last; only
             // share w0 may have begun before the unit
-            const int64_t slot0 = 2 * (int64_t)w0 + ((int64_t)w0 * hdr.tiles / hdr.workers < U0 ? 1 : 0);
-            const int row = (tok - pair * kPairSeqs) * GP + h;
-            merge_parts(acc, 1 + w1 - w0, sh.part_o, sh.part_ml, [&](int i) {
-                const int64_t slot = i == 0 ? slot0 : 2 * (int64_t)(w0 + i);
-                return make_longlong2((slot * 32 + lane) * kPairRows + row, slot * kPairRows + row);
-            });
+            r.slot0 = 2 * (int64_t)w0 + ((int64_t)w0 * tiles / workers < U0 ? 1 : 0);
+            r.w0 = w0;
         }
+        s_row[threadIdx.x] = r;
     }
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    if (!mine) return;
+    const int4 u = sh.units[(int64_t)s * a.num_kv_heads + kvh];
+    if (u.x == -2) return;
+    const Row r = s_row[threadIdx.x & 7];
+    Merge acc;
+    if (r.prefix_parts == 1)
+        acc.add(sh.unit_ml[kvh * rows + row], sh.unit_o[((int64_t)kvh * 32 + word) * rows + row]);
+    else if (r.prefix_parts > 1)
+        merge_parts(acc, r.prefix_parts, sh.part_o, sh.part_ml, [&](int i) {
+            const int64_t slot = i == 0 ? r.slot0 : 2 * (r.w0 + i);
+            return make_longlong2((slot * 32 + word) * kPairRows + r.prefix_row,
+                                  slot * kPairRows + r.prefix_row);
+        });
     if (u.x == -1) {
-        const int64_t row = (int64_t)s * a.num_q_heads + (int64_t)kvh * a.group + h;
-        acc.add(sh.own_ml[row], sh.own_o[row * 32 + lane]);
+        const int64_t own = (int64_t)s * a.num_q_heads + (int64_t)kvh * a.group + h;
+        acc.add(sh.own_ml[own], sh.own_o[own * 32 + word]);
     } else {
         merge_parts(acc, 1 + u.y - u.z, reinterpret_cast<const float4 *>(a.part_o),
                     reinterpret_cast<const float2 *>(a.part_ml), [&](int i) {
             const int64_t slot = i == 0 ? u.x : 2 * (int64_t)(u.z + i);
-            return make_longlong2((slot * GP + h) * 32 + lane, slot * GP + h);
+            return make_longlong2((slot * GP + h) * 32 + word, slot * GP + h);
         });
     }
     const float inv = acc.l > 0.f ? 1.f / acc.l : 0.f;
     uint2 pk;
     pk.x = pack_bf16x2(acc.o.x * inv, acc.o.y * inv);
     pk.y = pack_bf16x2(acc.o.z * inv, acc.o.w * inv);
-    reinterpret_cast<uint2 *>(static_cast<uint32_t *>(a.out) + col_row(a, s, kvh, h) / 2)[lane] = pk;
+    reinterpret_cast<uint2 *>(static_cast<uint32_t *>(a.out) + col_row(a, s, kvh, h) / 2)[word] = pk;
 }
 
 template <class Tile, int GP>
@@ -1093,7 +1151,8 @@ struct Launcher {
         if (e != cudaSuccess) return e;
         if (sh) {
             e = launch_pdl(reinterpret_cast<const void *>(&combine_shared_kernel<GP>),
-                           dim3(a.num_seqs * a.num_kv_heads), GP * 32, 0, sargs, st);
+                           dim3((unsigned)(((int64_t)a.num_seqs * GP + 7) / 8), a.num_kv_heads), 256, 0,
+                           sargs, st);
             return e != cudaSuccess ? e : cudaGetLastError();
         }
         void *cargs[] = {&args_copy};

@@ -151,6 +151,11 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+__device__ __forceinline__ void piece_end(SharedWalk &w) {
+    const int64_t left = w.T1 - w.T;
+    w.j1 = w.gr.nt - w.j0 < left ? w.gr.nt : w.j0 + (int)left;
+}
+
 // -- plan ------------------------------------------------------------------------
 
 // Inclusive scan of v over the CTA's 1024 threads; `sums` is scratch of 32.
@@ -169,24 +174,54 @@ __device__ __forceinline__ long long block_scan(long long v, long long *sums) {
     return v + before;
 }
 
+// Estimated time (us) when x of the SMs compute `tiles` prefix tiles of `units`
+// units and the others read `own` 16-token tiles at the same time. Measured: a
+// prefix tile pair takes 2.3 us on an SM, 2.6 beside the other reads; a piece
+// (its queries, first keys, last product and rows) 3 us; an SM reads 75 GB/s of
+// K and V, and all together 6.4 TB/s. Equal shares of one group's units that
+// end where units end have no piece more than they need. With x = all SMs the
+// own tiles come after. Batch of 128 sequences x 64 heads, 2048 shared tokens
+// and 256 own: x = 152, 88, 64, 40 took 65, 50, 48, 63 us.
+__device__ __forceinline__ float split_cost(int x, int sms, long long tiles, long long units,
+                                            long long own, bool one_group) {
+    constexpr float kTile = 2.6f, kTileAlone = 2.3f, kPiece = 3.f, kRate = 75e3f, kRateAll = 6.4e6f;
+    const float own_bytes = (float)own * (2.f * kTileBytes);
+    const long long share = (tiles + x - 1) / x;
+    const float nt = (float)tiles / (float)units;
+    float pieces = 1.f + (float)share / nt;
+    if (one_group && tiles % x == 0) {
+        const long long n = tiles / units;
+        if (n % share == 0) pieces = 1.f;
+        else if (share % n == 0) pieces = (float)(share / n);
+    }
+    if (x == sms) return pieces * kPiece + (float)share * kTileAlone + own_bytes / kRateAll;
+    const float rate = fminf((float)(sms - x) * kRate, kRateAll);
+    return fmaxf(pieces * kPiece + (float)share * kTile, kPiece + own_bytes / rate);
+}
+
 __global__ void __launch_bounds__(kPlanThreads, 1)
 shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
-    extern __shared__ int plan_smem[];
+    extern __shared__ long long plan_smem[];
     __shared__ long long s_sums[32];
-    const int G = sh.num_groups, S = a.num_seqs;
-    int *starts = plan_smem;            // [G + 1]
-    int *shortest = starts + G + 1;     // [G] shortest non-empty length
+    __shared__ unsigned long long s_best;
+    const int G = sh.num_groups, S = a.num_seqs, tid = threadIdx.x;
+    long long *bases = plan_smem;       // [G] flat index of the group's first tile
+    int *starts = reinterpret_cast<int *>(bases + G);   // [G + 1]
+    int *shortest = starts + G + 1;     // [G] shortest non-empty length, then tokens computed together
     int *first = shortest + G;          // [G] first non-empty sequence
-    int *live = first + G;              // [G] non-empty sequences
-    int *active = live + G;             // [G] index among the active groups, or -1
+    int *live = first + G;              // [G] non-empty sequences, then index among the active groups or -1
     // programmatic dependent of whatever precedes the call
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int64_t max_len64 = (int64_t)a.max_blocks_per_seq << a.block_size_log2;
     const int max_len = (int)(max_len64 < INT_MAX ? max_len64 : INT_MAX);
-    for (int g = threadIdx.x; g <= G; g += kPlanThreads) {
-        const int s = sh.group_starts[g];
-        starts[g] = s < 0 ? 0 : (s > S ? S : s);
+    auto clamp = [](int x, int most) { return x < 0 ? 0 : (x > most ? most : x); };
+    // the first of each input in flight together
+    const int my_len = tid < S ? clamp(a.context_lens[tid], max_len) : 0;
+    const int my_prefix = tid < G ? sh.prefix_blocks[tid] : 0;
+    auto length = [&](int s) { return s == tid ? my_len : clamp(a.context_lens[s], max_len); };
+    for (int g = tid; g <= G; g += kPlanThreads) {
+        starts[g] = clamp(sh.group_starts[g], S);
         if (g < G) {
             shortest[g] = first[g] = INT_MAX;
             live[g] = 0;
@@ -202,13 +237,9 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
         }
         return starts[lo] <= s && s < starts[lo + 1] ? lo : -1;
     };
-    auto length = [&](int s) {
-        const int L = a.context_lens[s];
-        return L < 0 ? 0 : (L > max_len ? max_len : L);
-    };
     const int s_lo = starts[0], s_hi = starts[G];
-    for (int s = s_lo + threadIdx.x; s < s_hi; s += kPlanThreads) {
-        const int g = group_of(s), L = length(s);
+    for (int s = tid; s < s_hi; s += kPlanThreads) {
+        const int g = s < s_lo ? -1 : group_of(s), L = length(s);
         if (g >= 0 && L > 0) {
             atomicMin(shortest + g, L);
             atomicMin(first + g, s);
@@ -216,14 +247,14 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
         }
     }
     __syncthreads();
-    long long base = 0, act = 0;
+    long long base = 0, units = 0;
+    int act = 0;
     for (int g0 = 0; g0 < G; g0 += kPlanThreads) {
-        const int g = g0 + threadIdx.x;
+        const int g = g0 + tid;
         SharedGroup gr{};
         long long tiles = 0;
         if (g < G) {
-            const int pb = sh.prefix_blocks[g];
-            const int64_t want = (int64_t)(pb < 0 ? 0 : (pb > a.max_blocks_per_seq ? a.max_blocks_per_seq : pb))
+            const int64_t want = (int64_t)clamp(g0 == 0 ? my_prefix : sh.prefix_blocks[g], a.max_blocks_per_seq)
                                  << a.block_size_log2;
             const int most = live[g] > 0 ? shortest[g] & ~15 : 0;
             gr.tokens = live[g] >= kSharedMinSeqs ? (int)(want < most ? want : most) : 0;
@@ -235,89 +266,96 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
             tiles = (long long)gr.nt * gr.pairs * a.num_kv_heads;
         }
         const long long t_end = block_scan(tiles, s_sums);
-        const long long a_end = block_scan(tiles > 0 ? 1 : 0, s_sums);
+        const long long u_end = block_scan(tiles > 0 ? ((long long)gr.pairs * a.num_kv_heads << 16) + 1 : 0, s_sums);
+        const int a_end = (int)(u_end & 0xffff);        // at most kMaxGroups
         if (g < G) {
+            const int at = act + a_end - 1;
             gr.base = base + t_end - tiles;
-            const int at = (int)(act + a_end) - 1;
-            active[g] = tiles > 0 ? at : -1;
-            if (tiles > 0) sh.groups[at] = gr;
+            bases[g] = gr.base;
             shortest[g] = gr.tokens;
+            live[g] = tiles > 0 ? at : -1;
+            if (tiles > 0) sh.groups[at] = gr;
         }
         __syncthreads();
-        if (threadIdx.x == kPlanThreads - 1) s_sums[0] = t_end, s_sums[1] = a_end;
+        if (tid == kPlanThreads - 1) s_sums[0] = t_end, s_sums[1] = u_end;
         __syncthreads();
         base += s_sums[0];
-        act += s_sums[1];
+        act += (int)(s_sums[1] & 0xffff);
+        units += s_sums[1] >> 16;
         __syncthreads();
     }
-    for (int s = s_lo + threadIdx.x; s < s_hi; s += kPlanThreads) {
-        const int g = group_of(s);
-        const bool in = g >= 0 && active[g] >= 0 && length(s) > 0;
-        sh.seq[s] = in ? make_int2(shortest[g], active[g]) : make_int2(0, -1);
+    long long own = 0;
+    for (int c0 = s_lo; c0 < s_hi; c0 += kPlanThreads) {
+        const int s = c0 + tid;
+        long long n = 0;
+        if (s < s_hi) {
+            const int g = group_of(s), L = length(s);
+            const bool in = g >= 0 && live[g] >= 0 && L > 0;
+            const int start = in ? shortest[g] : 0;
+            sh.seq[s] = make_int2(start, in ? live[g] : -1);
+            n = L > start ? (L - start + kTileTokens - 1) / kTileTokens : 1;   // an empty unit owns one tile
+        }
+        const long long end = block_scan(n, s_sums);
+        if (s < s_hi) sh.scan[s] = own + end;
+        __syncthreads();
+        if (tid == kPlanThreads - 1) s_sums[0] = end;
+        __syncthreads();
+        own += s_sums[0];
+        __syncthreads();
     }
-    if (threadIdx.x == 0) {
+    own *= a.num_kv_heads;
+    // how many SMs compute prefixes while the others read the own tiles
+    const int sms = sh.max_workers, per_sm = a.num_workers / sms;
+    if (tid == 0) s_best = ~0ull;
+    __syncthreads();
+    for (int x = 1 + tid; x <= sms && x <= base; x += kPlanThreads) {
+        const float cost = split_cost(x, sms, base, units, own, act == 1);
+        atomicMin(&s_best, ((unsigned long long)__float_as_uint(cost) << 32) | (unsigned)x);
+    }
+    __syncthreads();
+    const int workers = base > 0 ? (int)(s_best & 0xffffffffu) : 0;
+    if (tid == 0) {
         SharedHeader h;
         h.tiles = base;
-        h.num_active = (int)act;
+        h.own_tiles = own;
         h.s_lo = s_lo;
         h.s_hi = s_hi;
-        h.workers = (int)(base < sh.max_workers ? base : sh.max_workers);
+        h.workers = workers;
+        const int64_t most = own / a.min_tiles;
+        const int beside = workers < sms ? (sms - workers) * per_sm : a.num_workers;
+        h.own_workers = (int)(most < 1 ? 1 : (most < beside ? most : beside));
         *sh.hdr = h;
+    }
+    // where each share begins: in the last group whose base is at or before its
+    // first tile (groups without tiles share their successor's base, and come
+    // before it)
+    for (int w = tid; w < workers; w += kPlanThreads) {
+        SharedWalk k{};
+        k.T = (int64_t)w * base / workers;
+        k.T1 = (int64_t)(w + 1) * base / workers;
+        int lo = 0, hi = G;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (bases[mid] <= k.T) lo = mid; else hi = mid;
+        }
+        k.act = live[lo];
+        k.gr = sh.groups[k.act];
+        const int64_t rem = k.T - k.gr.base;
+        const int unit = (int)(rem / k.gr.nt);
+        k.j0 = (int)(rem - (int64_t)unit * k.gr.nt);
+        k.kvh = unit / k.gr.pairs;
+        k.pair = unit - k.kvh * k.gr.pairs;
+        piece_end(k);
+        sh.walks[w] = k;
     }
 }
 
 // -- prefix ------------------------------------------------------------------------
 
-// A share's walk: its pieces are runs of key tiles [j0, j1) of one unit. Every
-// warp walks by itself and keeps its place in shared memory, where the fields
-// are read when they are needed: none of them stays live across the tile loop.
-struct Walk {
-    int64_t T, T1;      // next tile, end of the share
-    SharedGroup gr;
-    int act, kvh, pair, j0, j1;
-};
-static_assert(sizeof(Walk) == kWalkBytes, "Walk");
-
-__device__ __forceinline__ SharedGroup load_group(const SharedArgs &sh, int i) {
-    SharedGroup g;
-    const int4 *p = reinterpret_cast<const int4 *>(sh.groups + i);
-    reinterpret_cast<int4 *>(&g)[0] = __ldcg(p);
-    reinterpret_cast<int4 *>(&g)[1] = __ldcg(p + 1);
-    return g;
-}
-
-__device__ __forceinline__ void piece_end(Walk &w) {
-    const int64_t left = w.T1 - w.T;
-    w.j1 = w.gr.nt - w.j0 < left ? w.gr.nt : w.j0 + (int)left;
-}
-
-// The first piece of share [T0, T1), T0 < T1: the last active group that
-// starts at or before T0 holds it.
-__device__ __forceinline__ void walk_begin(volatile Walk &place, const SharedArgs &sh, int num_active,
-                                           int64_t T0, int64_t T1) {
-    const int lane = threadIdx.x & 31;
-    int hit = 0;
-    for (int i0 = 0; i0 < num_active; i0 += 32) {
-        const bool le = i0 + lane < num_active && __ldcg(&sh.groups[i0 + lane].base) <= T0;
-        const unsigned m = __ballot_sync(0xffffffffu, le);
-        if (m) hit = i0 + 31 - __clz(m);
-        if (m != 0xffffffffu) break;
-    }
-    if (lane == 0) {
-        Walk &w = const_cast<Walk &>(place);
-        w.T = T0;
-        w.T1 = T1;
-        w.act = hit;
-        w.gr = load_group(sh, hit);
-        const int64_t rem = T0 - w.gr.base;
-        const int unit = (int)(rem / w.gr.nt);
-        w.j0 = (int)(rem - (int64_t)unit * w.gr.nt);
-        w.kvh = unit / w.gr.pairs;
-        w.pair = unit - w.kvh * w.gr.pairs;
-        piece_end(w);
-    }
-    __syncwarp();
-}
+// Every warp walks by itself and keeps its place in shared memory, where the
+// fields are read when they are needed: none stays live across the tile loop.
+using Walk = SharedWalk;
+static_assert(sizeof(Walk) == kWalkBytes, "SharedWalk");
 
 // On to the next piece; false at the end of the share.
 __device__ __forceinline__ bool walk_next(volatile Walk &place, const SharedArgs &sh, int num_kv_heads) {
@@ -331,7 +369,7 @@ __device__ __forceinline__ bool walk_next(volatile Walk &place, const SharedArgs
             w.pair = 0;
             if (++w.kvh == num_kv_heads) {
                 w.kvh = 0;
-                w.gr = load_group(sh, ++w.act);
+                w.gr = sh.groups[++w.act];
             }
         }
         piece_end(w);
@@ -362,19 +400,11 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
     constexpr int BT = kRows / G;               // sequences per query tile
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5;
-    // the plan is complete before anything below reads it; the decode that
-    // follows may be scheduled as this grid's CTAs finish
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    const SharedHeader hdr = *sh.hdr;
     const int w_id = blockIdx.x;
-    if (w_id >= hdr.workers) return;
-    const int64_t T0 = (int64_t)w_id * hdr.tiles / hdr.workers;
-    const int64_t T1 = (int64_t)(w_id + 1) * hdr.tiles / hdr.workers;
-
     const uint32_t sbase = smem_u32(smem);
     if (sbase & 1023u) {                        // the swizzle atoms need 1024-byte alignment
         if (tid == 0) set_error(kErrSmemAlign);
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");
         return;
     }
     const uint32_t ctl = sbase + kOffCtl;
@@ -406,9 +436,19 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
     tc::fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kOffTmemSlot);
 
+    // the plan is complete before anything below reads it; the decode that
+    // follows may be scheduled as this grid's CTAs finish
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     volatile Walk &w = reinterpret_cast<Walk *>(smem + kOffWalk)[warp];
-    walk_begin(w, sh, hdr.num_active, T0, T1);
-    if (tid < kSoftmaxThreads) {
+    const bool works = w_id < sh.hdr->workers;
+    if (works && (tid & 31) < (int)(sizeof(Walk) / 16))
+        reinterpret_cast<int4 *>(smem + kOffWalk + warp * kWalkBytes)[tid & 31] =
+            reinterpret_cast<const int4 *>(sh.walks + w_id)[tid & 31];
+    __syncwarp();
+    if (!works) {
+        // more CTAs than tiles
+    } else if (tid < kSoftmaxThreads) {
         // ---------------- softmax warpgroups ----------------
         const int wg = tid >> 7, r = tid & 127;
         const uint32_t lane = (uint32_t)(r & ~31) << 16;
@@ -790,13 +830,15 @@ cudaError_t launch_g(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t st)
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct Carve {
-    size_t hdr, seq, groups, part_o, part_ml, unit_o, unit_ml, units, own_o, own_ml, end;
+    size_t hdr, seq, scan, groups, walks, part_o, part_ml, unit_o, unit_ml, units, own_o, own_ml, end;
     Carve(int S, int G, int hq, int hkv, int gp, int workers) {
         const size_t rows = (size_t)S * gp * hkv, own = (size_t)S * hq, slots = 2 * (size_t)workers;
         hdr = 0;
         seq = hdr + round256(sizeof(SharedHeader));
-        groups = seq + round256((size_t)S * sizeof(int2));
-        part_o = groups + round256((size_t)G * sizeof(SharedGroup));
+        scan = seq + round256((size_t)S * sizeof(int2));
+        groups = scan + round256((size_t)S * sizeof(long long));
+        walks = groups + round256((size_t)G * sizeof(SharedGroup));
+        part_o = walks + round256((size_t)workers * sizeof(SharedWalk));
         part_ml = part_o + slots * 32 * kPairRows * sizeof(float4);
         unit_o = part_ml + slots * kPairRows * sizeof(float2);
         unit_ml = unit_o + rows * 32 * sizeof(float4);
@@ -823,7 +865,9 @@ void shared_carve_workspace(SharedArgs &sh, void *workspace, const DecodeArgs &a
     char *p = static_cast<char *>(workspace);
     sh.hdr = reinterpret_cast<SharedHeader *>(p + c.hdr);
     sh.seq = reinterpret_cast<int2 *>(p + c.seq);
+    sh.scan = reinterpret_cast<long long *>(p + c.scan);
     sh.groups = reinterpret_cast<SharedGroup *>(p + c.groups);
+    sh.walks = reinterpret_cast<SharedWalk *>(p + c.walks);
     sh.part_o = reinterpret_cast<float4 *>(p + c.part_o);
     sh.part_ml = reinterpret_cast<float2 *>(p + c.part_ml);
     sh.unit_o = reinterpret_cast<float4 *>(p + c.unit_o);
@@ -834,9 +878,9 @@ void shared_carve_workspace(SharedArgs &sh, void *workspace, const DecodeArgs &a
 }
 
 cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t stream) {
-    const size_t plan_smem = (5 * (size_t)sh.num_groups + 1) * sizeof(int);
+    const size_t plan_smem = (6 * (size_t)sh.num_groups + 1) * sizeof(int);
     cudaError_t e = cudaFuncSetAttribute(shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)((5 * kMaxGroups + 1) * sizeof(int)));
+                                         (int)((6 * kMaxGroups + 1) * sizeof(int)));
     if (e != cudaSuccess) return e;
     DecodeArgs ac = a;
     SharedArgs sc = sh;

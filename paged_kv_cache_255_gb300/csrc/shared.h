@@ -6,7 +6,7 @@
 
 namespace pa {
 
-constexpr int kSharedMaxGroups = 4096;  // groups of one call (the plan keeps 20 bytes each in shared memory)
+constexpr int kSharedMaxGroups = 4096;  // groups of one call (the plan keeps 24 bytes each in shared memory)
 constexpr int kSharedMinSeqs = 2;       // a prefix is computed apart for at least this many sequences
 constexpr int kPairRows = 256;      // rows of a prefix unit: two query tiles of 128
 
@@ -21,11 +21,20 @@ struct alignas(16) SharedGroup {
 };
 static_assert(sizeof(SharedGroup) == 32, "one 32-byte sector");
 
+// A share's walk over the tile space: its pieces are runs of key tiles
+// [j0, j1) of one unit, a unit being 256 query rows of one (group, KV head).
+struct alignas(16) SharedWalk {
+    int64_t T, T1;          // next tile, end of the share
+    SharedGroup gr;
+    int act, kvh, pair, j0, j1;
+};
+
 struct SharedHeader {
-    int64_t tiles;          // key tiles of all active groups
-    int num_active;
+    int64_t tiles;          // prefix: key tiles of all active groups
+    int64_t own_tiles;      // what follows it: 16-token tiles of all units (decode.cu)
     int s_lo, s_hi;         // sequences the call covers
-    int workers;            // shares the tiles are cut into
+    int workers;            // CTAs the prefix tiles are shared among
+    int own_workers;        // warps the own tiles are shared among
 };
 
 // Pointers are device memory.
@@ -38,7 +47,9 @@ struct SharedArgs {
     // in the workspace
     SharedHeader *hdr;
     int2 *seq;                      // [S] tokens computed with the group's prefix, active group or -1
+    long long *scan;                // [S] own tiles of one KV head through sequence s
     SharedGroup *groups;            // [num_groups] the active ones
+    SharedWalk *walks;              // [max_workers] first piece of every share
     float4 *part_o;                 // [2 max_workers][32][256] pieces of units that several workers share
     float2 *part_ml;                // [2 max_workers][256] (running max in log2 units, sum)
     float4 *unit_o;                 // [Hkv][32][S G] units one worker computed whole
