@@ -240,6 +240,9 @@ pa_status_t prefill_impl(const void *q, const void *k_cache, const void *v_cache
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// Columns of the decode tiles of a call over shared prefixes.
+int shared_cols(int group_pad) { return group_pad <= 8 ? 8 : 16; }
+
 // The shape of the pools a block operation works on, and their addresses.
 pa_status_t check_pools(void *const *caches, int num_caches, int num_kv_heads, int head_dim,
                         int block_size, int64_t num_blocks) {
@@ -476,11 +479,15 @@ pa_status_t pa_decode_step(const void *k, const void *v, const int64_t *slot_map
 size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_heads,
                                        int num_kv_heads, int head_dim) {
     if (num_seqs < 0 || num_groups < 0 || num_groups > pa::kSharedMaxGroups) return 0;
-    const size_t dec = pa_decode_workspace_size(num_q_heads, num_kv_heads, head_dim, 0);
-    const int sms = current_sm_count();
-    if (dec == 0 || sms <= 0) return 0;
-    return round256(dec) + pa::shared_workspace_bytes(num_seqs, num_groups, num_q_heads, num_kv_heads,
-                                                      pa::decode_group_pad(num_q_heads / num_kv_heads), sms);
+    if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+        head_dim != pa::kHeadDimPublic)
+        return 0;
+    const int gp = pa::decode_group_pad(num_q_heads / num_kv_heads);
+    if (gp == 0) return 0;
+    const int P = plan_workers(shared_cols(gp), pa::DecodeKernel::kMma, 0), sms = current_sm_count();
+    if (P <= 0 || sms <= 0) return 0;
+    return round256(pa::decode_workspace_bytes(shared_cols(gp), P)) +
+           pa::shared_workspace_bytes(num_seqs, num_groups, num_q_heads, num_kv_heads, gp, sms);
 }
 
 pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_cache,
@@ -501,10 +508,10 @@ pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_c
     if (nothing_to_do || num_groups == 0) return PA_OK;
     if (!group_starts || !prefix_blocks) return PA_ERR_INVALID_ARG;
     const int gp = pa::decode_group_pad(num_q_heads / num_kv_heads);
-    const int P = plan_workers(gp, pa::DecodeKernel::kMma, 0);
+    const int P = plan_workers(shared_cols(gp), pa::DecodeKernel::kMma, 0);
     const int sms = current_sm_count();
     if (P <= 0 || sms <= 0) return PA_ERR_CUDA;
-    const size_t dec = round256(pa::decode_workspace_bytes(gp, P));
+    const size_t dec = round256(pa::decode_workspace_bytes(shared_cols(gp), P));
     if (!workspace || !aligned16(workspace) ||
         workspace_bytes < dec + pa::shared_workspace_bytes(num_seqs, num_groups, num_q_heads,
                                                            num_kv_heads, gp, sms))
@@ -513,18 +520,25 @@ pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_c
                                    context_lens, 1, scale, out, num_seqs, num_q_heads, num_kv_heads,
                                    block_size, num_blocks, layout);
     a.num_workers = P;
-    a.min_tiles = pa::kDefaultMinTiles;
-    pa::decode_carve_workspace(a, workspace, gp);
+    a.min_tiles = 1;
+    pa::decode_carve_workspace(a, workspace, shared_cols(gp));
     pa::SharedArgs sh{};
     sh.group_starts = group_starts;
     sh.prefix_blocks = prefix_blocks;
     sh.num_groups = num_groups;
     sh.group_pad = gp;
     sh.max_workers = sms;
+    // Two packed units read a prefix twice at most: never dearer than the prefix
+    // kernel, which is then not launched. Nor is it where its tiles could not be
+    // counted in 32 bits.
+    const int64_t key_tiles = (((int64_t)max_blocks_per_seq << a.block_size_log2) + 127) / 128;
+    const int64_t pairs = (int64_t)num_seqs * gp / pa::kPairRows + num_groups;
+    sh.tensor = (num_seqs + pa::shared_fit(a.group) - 1) / pa::shared_fit(a.group) > 2 &&
+                key_tiles <= INT32_MAX / num_kv_heads / pairs ? 1 : 0;
     pa::shared_carve_workspace(sh, static_cast<char *>(workspace) + dec, a);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = pa::launch_shared_prefix(a, sh, st);
-    if (e == cudaSuccess) e = pa::launch_decode_shared(a, sh, gp, st);
+    if (e == cudaSuccess) e = pa::launch_decode_shared(a, sh, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -34,10 +34,11 @@
 //     kept as the comparison and a second parity path, selected only by the
 //     test hook pa_debug_kernel_variant.
 // With shared prefixes (decode_shared_kernel) a unit is only what follows the
-// tokens its group's prefix covers. A unit that has a prefix is left in fp32
-// even when one share holds it whole, and combine_shared_kernel merges it with
-// the prefix's (m, l, o), left by shared.cu. The two kernels before it do not
-// need one another.
+// tokens its group's prefix covers; the prefix itself is computed by shared.cu,
+// or here, for a few sequences whose heads together fill the 8 columns of a
+// matrix instruction, as a unit of its own. A unit that is one part of several
+// is left in fp32 even when one share holds it whole, and combine_shared_kernel
+// merges the parts. The kernels before it do not need one another.
 // The kernels never wait on one another inside a launch; a warp waits only on
 // its own copies, and every such wait is bounded (1 s, then the launch records
 // code 2 and the warp exits).
@@ -123,23 +124,36 @@ __device__ __forceinline__ int unit_tiles(int L) { return L > 0 ? (L + 15) >> 4 
 struct Cursor {
     int s, kvh, j, nt, L;
 };
-// With shared prefixes the unit's tiles begin at token `start`, a multiple of 16.
-struct SharedCursor : Cursor {
-    int start;
+// With shared prefixes a unit belongs to an entry v of the plan's list: the own
+// tokens of a sequence, or the prefix of a few sequences at once.
+struct SharedCursor {
+    int v, kvh, j, nt;
+    SharedUnit u;
 };
 __device__ __forceinline__ int first_token(const Cursor &c) { return c.j << 4; }
-__device__ __forceinline__ int first_token(const SharedCursor &c) { return c.start + (c.j << 4); }
+__device__ __forceinline__ int first_token(const SharedCursor &c) { return c.u.start + (c.j << 4); }
+__device__ __forceinline__ int unit_len(const Cursor &c) { return c.L; }
+__device__ __forceinline__ int unit_len(const SharedCursor &c) { return c.u.len; }
+__device__ __forceinline__ int table_row(const Cursor &c) { return c.s; }
+__device__ __forceinline__ int table_row(const SharedCursor &c) { return c.u.row; }
+__device__ __forceinline__ int unit_seq(const Cursor &c) { return c.s; }
+__device__ __forceinline__ int unit_seq(const SharedCursor &c) { return c.u.first; }
+
+__device__ __forceinline__ SharedUnit load_unit(const SharedArgs &sh, int v) {
+    const int4 x = __ldcg(reinterpret_cast<const int4 *>(sh.entries + v));
+    const int2 y = __ldcg(reinterpret_cast<const int2 *>(sh.entries + v) + 2);
+    return SharedUnit{x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};
+}
 
 __device__ __forceinline__ void cursor_advance(SharedCursor &c, const DecodeArgs &a,
-                                               const SharedArgs &sh, int s_hi, int max_len) {
+                                               const SharedArgs &sh, int entries) {
     if (++c.j == c.nt) {
         c.j = 0;
         if (++c.kvh == a.num_kv_heads) {
             c.kvh = 0;
-            if (++c.s < s_hi) {
-                c.L = clamp_len(a.context_lens, c.s, max_len);
-                c.start = __ldcg(&sh.seq[c.s].x);
-                c.nt = unit_tiles(c.L - c.start);
+            if (++c.v < entries) {
+                c.u = load_unit(sh, c.v);
+                c.nt = unit_tiles(c.u.len - c.u.start);
             }
         }
     }
@@ -160,7 +174,7 @@ __device__ __forceinline__ void cursor_advance(Cursor &c, const DecodeArgs &a, i
 
 template <class C>
 __device__ __forceinline__ int tile_valid(const C &c) {
-    int v = c.L - first_token(c);
+    int v = unit_len(c) - first_token(c);
     return v < 0 ? 0 : (v > 16 ? 16 : v);
 }
 
@@ -168,7 +182,7 @@ __device__ __forceinline__ int tile_valid(const C &c) {
 template <class C>
 __device__ __forceinline__ int tile_block(const C &c, const DecodeArgs &a) {
     if (tile_valid(c) == 0) return 0;
-    return __ldg(a.block_tables + (int64_t)c.s * a.max_blocks_per_seq +
+    return __ldg(a.block_tables + (int64_t)table_row(c) * a.max_blocks_per_seq +
                  (first_token(c) >> a.block_size_log2));
 }
 
@@ -241,6 +255,18 @@ __device__ __forceinline__ int col_limit(const DecodeArgs &a, int L, int c) {
     return c < a.cols ? (lim > 0 ? lim : 0) : 0;
 }
 
+// Columns of a unit, and the tokens column c sees. With shared prefixes there
+// is one query token per sequence, and columns past the first sequence's heads
+// are the next sequences' (col_row's rows are consecutive that way).
+__device__ __forceinline__ int unit_cols(const DecodeArgs &a, const Cursor &) { return a.cols; }
+__device__ __forceinline__ int unit_cols(const DecodeArgs &, const SharedCursor &u) { return u.u.cols; }
+__device__ __forceinline__ int unit_limit(const DecodeArgs &a, const Cursor &u, int c) {
+    return col_limit(a, u.L, c);
+}
+__device__ __forceinline__ int unit_limit(const DecodeArgs &, const SharedCursor &u, int c) {
+    return c < u.u.cols ? u.u.len : 0;
+}
+
 // ---------------------------------------------------------------------------
 // Tile computation on the tensor cores.
 //
@@ -261,20 +287,21 @@ struct MmaTile {
     float m[NT][2], l[NT][2];
     int lim[NT][2];     // tokens visible to this lane's two score columns per column tile
 
-    __device__ __forceinline__ void begin(const DecodeArgs &a, const Cursor &cur, int lane) {
+    template <class C>
+    __device__ __forceinline__ void begin(const DecodeArgs &a, const C &cur, int lane) {
         const int gid = lane >> 2, tig = lane & 3;
         const uint16_t *qg = static_cast<const uint16_t *>(a.q);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int h = nt * 8 + gid;          // this lane's column of the Q^T operand
-            lim[nt][0] = col_limit(a, cur.L, nt * 8 + 2 * tig);
-            lim[nt][1] = col_limit(a, cur.L, nt * 8 + 2 * tig + 1);
+            lim[nt][0] = unit_limit(a, cur, nt * 8 + 2 * tig);
+            lim[nt][1] = unit_limit(a, cur, nt * 8 + 2 * tig + 1);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 uint32_t w0 = 0u, w1 = 0u;
-                if (h < a.cols) {
+                if (h < unit_cols(a, cur)) {
                     const uint32_t *p = reinterpret_cast<const uint32_t *>(
-                        qg + col_row(a, cur.s, cur.kvh, h) + kk * 16 + tig * 2);
+                        qg + col_row(a, unit_seq(cur), cur.kvh, h) + kk * 16 + tig * 2);
                     w0 = __ldg(p);
                     w1 = __ldg(p + 4);
                 }
@@ -640,44 +667,48 @@ __device__ __forceinline__ void plan_share(const DecodeArgs &a, int max_len, int
 }
 
 // The same with shared prefixes: the plan kernel has left the scan of the
-// units' tiles (sh.scan, through sequence s), the total and the share count; a
-// CTA stages the scan in its ring and each warp searches it.
-__device__ __forceinline__ void plan_shared(const DecodeArgs &a, const SharedArgs &sh, int max_len,
+// entries' tiles, the total and the share count; a CTA stages the scan in its
+// ring and each warp searches it.
+__device__ __forceinline__ void plan_shared(const DecodeArgs &a, const SharedArgs &sh,
                                             long long *stage, int64_t &W, int &p_eff, int64_t &T0,
-                                            int64_t &T1, int &s_hi, SharedCursor &c) {
+                                            int64_t &T1, int &entries, SharedCursor &c) {
     constexpr int kChunk = kWarps * kRingBytes / 8;
     const int warp = threadIdx.x >> 5, Hkv = a.num_kv_heads;
-    const int s_lo = __ldcg(&sh.hdr->s_lo);
-    s_hi = __ldcg(&sh.hdr->s_hi);
+    // the first chunk on its way together with the header (the array has room
+    // for 2 num_seqs entries; those past the last are not used)
+    const int ahead = 2 * a.num_seqs < kChunk ? 2 * a.num_seqs : kChunk;
+    for (int i = threadIdx.x; i < ahead; i += kWarps * 32) stage[i] = __ldcg(sh.scan + i);
+    entries = __ldcg(&sh.hdr->entries);
     W = __ldcg(&sh.hdr->own_tiles);
     p_eff = __ldcg(&sh.hdr->own_workers);
     const int w = blockIdx.x * kWarps + warp;
     T0 = T1 = W;
+    if (blockIdx.x * kWarps >= p_eff) return;           // no warp of the CTA has a share
     if (w < p_eff) {
         T0 = (int64_t)w * W / p_eff;
         T1 = (int64_t)(w + 1) * W / p_eff;
     }
     bool found = T0 >= T1;
     long long before = 0;               // tiles before the chunk
-    for (int c0 = s_lo; c0 < s_hi; c0 += kChunk) {
-        const int n = s_hi - c0 < kChunk ? s_hi - c0 : kChunk;
-        for (int i = threadIdx.x; i < n; i += kWarps * 32) stage[i] = __ldcg(sh.scan + c0 + i);
+    for (int c0 = 0; c0 < entries; c0 += kChunk) {
+        const int n = entries - c0 < kChunk ? entries - c0 : kChunk;
+        if (c0 > 0)
+            for (int i = threadIdx.x; i < n; i += kWarps * 32) stage[i] = __ldcg(sh.scan + c0 + i);
         __syncthreads();
         const long long end = stage[n - 1];
         if (!found && T0 < end * Hkv) {
-            int lo = 0, hi = n - 1;     // the first sequence whose tiles end past T0
+            int lo = 0, hi = n - 1;     // the first entry whose tiles end past T0
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
                 if (stage[mid] * Hkv > T0) hi = mid; else lo = mid + 1;
             }
             const long long excl = lo == 0 ? before : stage[lo - 1];
             const long long nt = stage[lo] - excl, rem = T0 - excl * Hkv;
-            c.s = c0 + lo;
+            c.v = c0 + lo;
             c.nt = (int)nt;
             c.kvh = (int)(rem / nt);
             c.j = (int)(rem - c.kvh * nt);
-            c.L = clamp_len(a.context_lens, c.s, max_len);
-            c.start = __ldcg(&sh.seq[c.s].x);
+            c.u = load_unit(sh, c.v);
             found = true;
         }
         before = end;
@@ -735,12 +766,13 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
     // let the combine launch queue up behind this grid. When the previous
     // kernel is known to be this step's store (plan_early), which writes the
     // caches only, the split of the work is planned from the lengths first.
-    // With shared prefixes the previous kernel is the prefixes', whose CTAs have
-    // all waited for everything before them and whose results nothing here
-    // reads: every thread waits for it only before it ends, so that what follows
-    // this grid follows that one too.
+    // With shared prefixes the previous kernel is the plan, or the prefix
+    // kernel, whose CTAs have all waited for everything before them and whose
+    // results nothing here reads: every thread waits for that one only before it
+    // ends, so that what follows this grid follows it too.
     prefetch_inputs(a);
     if (SHARED) {
+        if (!sh.tensor) asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the plan
         asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     } else if (!a.plan_early) {
         asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -753,9 +785,15 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
     int p_eff;
     typename std::conditional<SHARED, SharedCursor, Cursor>::type cc{};
     cc.nt = 1;
-    int s_hi = a.num_seqs;
+    int entries = 0;
+    if constexpr (SHARED) {
+        if (threadIdx.x == 0) {
+            tc::prefetch_map(&tmap_k);
+            tc::prefetch_map(&tmap_v);
+        }
+    }
     if constexpr (SHARED)
-        plan_shared(a, sh, max_len, reinterpret_cast<long long *>(smem), W, p_eff, T0, T1, s_hi, cc);
+        plan_shared(a, sh, reinterpret_cast<long long *>(smem), W, p_eff, T0, T1, entries, cc);
     else
         plan_share(a, max_len, W, p_eff, T0, T1, cc);
     if (!SHARED && a.plan_early) {
@@ -769,7 +807,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
         return;
     }
     auto advance = [&](auto &c) {
-        if constexpr (SHARED) cursor_advance(c, a, sh, s_hi, max_len);
+        if constexpr (SHARED) cursor_advance(c, a, sh, entries);
         else cursor_advance(c, a, max_len);
     };
 
@@ -843,36 +881,42 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
             tl.finish(reinterpret_cast<float *>(stage), sm_m, sm_l, oc, lane);
             tc::fence_proxy_async();     // the TMA that refills the stage lands after these stores
             __syncwarp();
-            bool prefixed = false;
-            if constexpr (SHARED) prefixed = cc.start > 0;
-            if (SHARED && piece_j0 == 0 && lane == 0) {
-                // how the combine finds the unit's parts: {first slot, last
-                // share, first share}, slot -1: whole in own_o, -2: nothing left
-                const int64_t unit_end_T = T - cc.j + cc.nt;
-                sh.units[(int64_t)cc.s * a.num_kv_heads + cc.kvh] =
-                    unit_end ? make_int4(prefixed ? -1 : -2, w, w, 0)
-                             : make_int4(2 * w + (piece == 0 ? 0 : 1),
-                                         (int)((unit_end_T * p_eff - 1) / W), w, 0);
+            // with shared prefixes: whether the unit is one part of several
+            bool part = false;
+            if constexpr (SHARED) {
+                part = cc.u.part != 0;
+                if (piece_j0 == 0 && lane == 0) {
+                    // how the combine finds the unit: {first slot, last share,
+                    // first share}; slot -1: whole in whole_o, -2: nothing left
+                    const int64_t unit_end_T = T - cc.j + cc.nt;
+                    sh.units[(int64_t)cc.v * a.num_kv_heads + cc.kvh] =
+                        unit_end ? make_int4(part ? -1 : -2, w, w, 0)
+                                 : make_int4(2 * w + (piece == 0 ? 0 : 1),
+                                             (int)((unit_end_T * p_eff - 1) / W), w, 0);
+                }
             }
-            if (prefixed && piece_j0 == 0 && unit_end) {
+            if (part && piece_j0 == 0 && unit_end) {
+                if constexpr (SHARED) {
+                    const int64_t base = cc.u.part & 2 ? (int64_t)a.num_seqs * a.num_q_heads : 0;
 #pragma unroll
-                for (int h = 0; h < GP; ++h)
-                    if (h < a.cols) {
-                        const int64_t row = (int64_t)cc.s * a.num_q_heads + (int64_t)cc.kvh * a.group + h;
-                        sh.own_o[row * 32 + lane] = make_float4(oc[h][0], oc[h][1], oc[h][2], oc[h][3]);
-                        if (lane == 0) sh.own_ml[row] = make_float2(sm_m[h], sm_l[h]);
-                    }
+                    for (int h = 0; h < GP; ++h)
+                        if (h < unit_cols(a, cc)) {
+                            const int64_t row = base + col_row(a, cc.u.first, cc.kvh, h) / kHeadDim;
+                            sh.whole_o[row * 32 + lane] = make_float4(oc[h][0], oc[h][1], oc[h][2], oc[h][3]);
+                            if (lane == 0) sh.whole_ml[row] = make_float2(sm_m[h], sm_l[h]);
+                        }
+                }
             } else if (piece_j0 == 0 && unit_end) {
                 // the whole unit is in this share: normalise and write bf16
 #pragma unroll
                 for (int h = 0; h < GP; ++h) {
-                    if (h < a.cols) {
+                    if (h < unit_cols(a, cc)) {
                         const float l = sm_l[h];
                         const float inv = l > 0.f ? 1.f / l : 0.f;
                         uint2 pk;
                         pk.x = pack_bf16x2(oc[h][0] * inv, oc[h][1] * inv);
                         pk.y = pack_bf16x2(oc[h][2] * inv, oc[h][3] * inv);
-                        reinterpret_cast<uint2 *>(outg + col_row(a, cc.s, cc.kvh, h) / 2)[lane] = pk;
+                        reinterpret_cast<uint2 *>(outg + col_row(a, unit_seq(cc), cc.kvh, h) / 2)[lane] = pk;
                     }
                 }
             } else {
@@ -890,7 +934,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
                     // this share holds the unit's first tile: it owns the combine
                     const int64_t unit_end_T = piece_T + cc.nt;
                     const int w_last = (int)((unit_end_T * p_eff - 1) / W);
-                    task = make_int4(cc.s, cc.kvh, slot, w_last);
+                    task = make_int4(unit_seq(cc), cc.kvh, slot, w_last);
                 }
             }
             __syncwarp();
@@ -1021,42 +1065,46 @@ __device__ __forceinline__ void merge_parts(Merge &acc, int n, const float4 *o, 
     }
 }
 
-// With shared prefixes: the prefix's parts of an output row, then its own. A
-// prefix computed whole by one CTA is a row of unit_o, one that several CTAs
-// shared a row of part_o per CTA, both [dim / 4][row]. A CTA takes 8 rows
+// With shared prefixes: the parts of an output row's prefix, then its own. The
+// prefix is left either by decode_shared_kernel, like the own part (a row of
+// whole_o, or a column of a slot per share), or by shared.cu (a row of unit_o,
+// or a row of part_o per CTA, both [dim / 4][row]). A CTA takes 8 rows
 // (sequence, head of the group) of one KV head, a thread 4 dims of a row: a
-// warp's 8 rows x 4 words are whole 128-byte lines of those arrays, and whole
-// sectors of the others and of `out`. (One warp per row, each lane in a line of
-// its own, took 17 us instead of 5 for 8192 rows of 6 parts.)
-// What does not depend on the two kernels before is looked up while they run.
-template <int GP>
+// warp's 8 rows x 4 words are whole 128-byte lines of shared.cu's arrays, and
+// whole sectors of the others and of `out`. (One warp per row, each lane in a
+// line of its own, took 17 us instead of 5 for 8192 rows of 6 parts.) What does
+// not depend on the two kernels before is looked up while they run. GP: heads
+// of a group, padded; COLS: columns of a slot.
+template <int GP, int COLS>
 __global__ void __launch_bounds__(256, 4) combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
     constexpr int kPairSeqs = kPairRows / GP;
     struct Row {
-        int prefix_parts, prefix_row;   // 0: none, 1: whole in unit_o, else pieces
+        int parts, row;                 // of shared.cu: 0 none, 1 whole in unit_o, else pieces
         int64_t slot0, w0;
+        int packed, col;                // entry and column of the prefix in decode_shared_kernel, or -1
     };
     __shared__ Row s_row[8];
     const int word = threadIdx.x >> 3;                  // dims [4 word, 4 word + 4)
     const int64_t rows = (int64_t)a.num_seqs * GP;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x & 7);
-    const int kvh = blockIdx.y;
+    const int kvh = blockIdx.y, Hkv = a.num_kv_heads;
     const int s = (int)(row / GP), h = (int)(row % GP);
-    const bool mine = row < rows && h < a.cols && s >= __ldcg(&sh.hdr->s_lo) && s < __ldcg(&sh.hdr->s_hi);
+    const int s_lo = __ldcg(&sh.hdr->s_lo);
+    const bool mine = row < rows && h < a.cols && s >= s_lo && s < __ldcg(&sh.hdr->s_hi);
     if (threadIdx.x < 8 && mine) {
-        Row r{0, 0, 0, 0};
-        const int act = __ldcg(&sh.seq[s].y);
-        if (act >= 0) {
+        const int4 q = __ldcg(sh.seq + s);
+        Row r{0, 0, 0, 0, q.y, q.z + h};
+        if (q.x >= 0) {
             const int64_t tiles = __ldcg(&sh.hdr->tiles);
             const int workers = __ldcg(&sh.hdr->workers);
-            const SharedGroup *g = sh.groups + act;
+            const SharedGroup *g = sh.groups + q.x;
             const int tok = s - __ldcg(&g->s0), pair = tok / kPairSeqs, nt = __ldcg(&g->nt);
             const int64_t U0 = __ldcg(&g->base) + ((int64_t)kvh * __ldcg(&g->pairs) + pair) * nt;
             // share w of the tile space is [w tiles / workers, (w + 1) tiles / workers)
             const int w0 = (int)(((U0 + 1) * workers - 1) / tiles);
             const int w1 = (int)(((U0 + nt) * workers - 1) / tiles);
-            r.prefix_parts = 1 + w1 - w0;
-            r.prefix_row = (tok - pair * kPairSeqs) * GP + h;
+            r.parts = 1 + w1 - w0;
+            r.row = (tok - pair * kPairSeqs) * GP + h;
             // share w's slot 2 w holds its first piece, 2 w + 1 its last; only
             // share w0 may have begun before the unit
             r.slot0 = 2 * (int64_t)w0 + ((int64_t)w0 * tiles / workers < U0 ? 1 : 0);
@@ -1067,33 +1115,43 @@ __global__ void __launch_bounds__(256, 4) combine_shared_kernel(const DecodeArgs
     __syncthreads();
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (!mine) return;
-    const int4 u = sh.units[(int64_t)s * a.num_kv_heads + kvh];
-    if (u.x == -2) return;
+    // Everything whose place is known goes out at once: the unit's record, its
+    // row if one share computed it whole (else unused), the first parts of the
+    // prefix.
+    const int4 u = sh.units[(int64_t)(s - s_lo) * Hkv + kvh];
     const Row r = s_row[threadIdx.x & 7];
+    const int64_t out_row = col_row(a, s, kvh, h) / kHeadDim;
+    const float2 own_ml = sh.whole_ml[out_row];
+    const float4 own_o = sh.whole_o[out_row * 32 + word];
     Merge acc;
-    if (r.prefix_parts == 1)
-        acc.add(sh.unit_ml[kvh * rows + row], sh.unit_o[((int64_t)kvh * 32 + word) * rows + row]);
-    else if (r.prefix_parts > 1)
-        merge_parts(acc, r.prefix_parts, sh.part_o, sh.part_ml, [&](int i) {
-            const int64_t slot = i == 0 ? r.slot0 : 2 * (r.w0 + i);
-            return make_longlong2((slot * 32 + word) * kPairRows + r.prefix_row,
-                                  slot * kPairRows + r.prefix_row);
-        });
-    if (u.x == -1) {
-        const int64_t own = (int64_t)s * a.num_q_heads + (int64_t)kvh * a.group + h;
-        acc.add(sh.own_ml[own], sh.own_o[own * 32 + word]);
-    } else {
-        merge_parts(acc, 1 + u.y - u.z, reinterpret_cast<const float4 *>(a.part_o),
+    auto add_slots = [&](const int4 x, int col) {
+        merge_parts(acc, 1 + x.y - x.z, reinterpret_cast<const float4 *>(a.part_o),
                     reinterpret_cast<const float2 *>(a.part_ml), [&](int i) {
-            const int64_t slot = i == 0 ? u.x : 2 * (int64_t)(u.z + i);
-            return make_longlong2((slot * GP + h) * 32 + word, slot * GP + h);
+            const int64_t slot = i == 0 ? x.x : 2 * (int64_t)(x.z + i);
+            return make_longlong2((slot * COLS + col) * 32 + word, slot * COLS + col);
         });
+    };
+    if (r.packed >= 0) {
+        const int4 x = sh.units[(int64_t)r.packed * Hkv + kvh];
+        const int64_t whole = (int64_t)a.num_seqs * a.num_q_heads + out_row;
+        if (x.x == -1) acc.add(sh.whole_ml[whole], sh.whole_o[whole * 32 + word]);
+        else add_slots(x, r.col);
     }
+    if (r.parts == 1)
+        acc.add(sh.unit_ml[kvh * rows + row], sh.unit_o[((int64_t)kvh * 32 + word) * rows + row]);
+    else if (r.parts > 1)
+        merge_parts(acc, r.parts, sh.part_o, sh.part_ml, [&](int i) {
+            const int64_t slot = i == 0 ? r.slot0 : 2 * (r.w0 + i);
+            return make_longlong2((slot * 32 + word) * kPairRows + r.row, slot * kPairRows + r.row);
+        });
+    if (u.x == -2) return;              // written by the share that computed it
+    if (u.x == -1) acc.add(own_ml, own_o);
+    else add_slots(u, h);
     const float inv = acc.l > 0.f ? 1.f / acc.l : 0.f;
     uint2 pk;
     pk.x = pack_bf16x2(acc.o.x * inv, acc.o.y * inv);
     pk.y = pack_bf16x2(acc.o.z * inv, acc.o.w * inv);
-    reinterpret_cast<uint2 *>(static_cast<uint32_t *>(a.out) + col_row(a, s, kvh, h) / 2)[word] = pk;
+    reinterpret_cast<uint2 *>(static_cast<uint32_t *>(a.out) + out_row * (kHeadDim / 2))[word] = pk;
 }
 
 template <class Tile, int GP>
@@ -1128,12 +1186,8 @@ struct Launcher {
         cfg.numAttrs = 1;
         return cudaLaunchKernelExC(&cfg, fn, args);
     }
-    // `sh` null: the plain decode. With shared prefixes the tiles are MmaTile's.
-    static cudaError_t launch(const DecodeArgs &a, cudaStream_t st, const SharedArgs *sh = nullptr) {
-        cudaError_t e = sh ? cudaFuncSetAttribute(decode_shared_kernel<GP>,
-                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  Lay::kCtaBytes)
-                           : prepare();
+    static cudaError_t launch(const DecodeArgs &a, cudaStream_t st) {
+        cudaError_t e = prepare();
         if (e != cudaSuccess) return e;
         CUtensorMap mk, mv;
         const int bs = 1 << a.block_size_log2;
@@ -1142,19 +1196,10 @@ struct Launcher {
             return cudaErrorInvalidValue;
         const unsigned grid = (a.num_workers + kWarps - 1) / kWarps;
         DecodeArgs args_copy = a;
-        SharedArgs sh_copy = sh ? *sh : SharedArgs{};
         void *dargs[] = {&args_copy, &mk, &mv};
-        void *sargs[] = {&args_copy, &sh_copy, &mk, &mv};
-        e = launch_pdl(sh ? reinterpret_cast<const void *>(&decode_shared_kernel<GP>)
-                          : reinterpret_cast<const void *>(&decode_kernel<Tile, GP>),
-                       dim3(grid), kWarps * 32, Lay::kCtaBytes, sh ? sargs : dargs, st);
+        e = launch_pdl(reinterpret_cast<const void *>(&decode_kernel<Tile, GP>), dim3(grid),
+                       kWarps * 32, Lay::kCtaBytes, dargs, st);
         if (e != cudaSuccess) return e;
-        if (sh) {
-            e = launch_pdl(reinterpret_cast<const void *>(&combine_shared_kernel<GP>),
-                           dim3((unsigned)(((int64_t)a.num_seqs * GP + 7) / 8), a.num_kv_heads), 256, 0,
-                           sargs, st);
-            return e != cudaSuccess ? e : cudaGetLastError();
-        }
         void *cargs[] = {&args_copy};
         e = launch_pdl(reinterpret_cast<const void *>(&combine_kernel<GP>),
                        dim3((a.num_workers + 3) / 4, a.cols), 128, 0, cargs, st);
@@ -1162,6 +1207,37 @@ struct Launcher {
         return cudaGetLastError();
     }
 };
+
+// The own tokens of a call over shared prefixes, then its combine. Tiles have
+// 8 columns (16 for groups above 8) whatever the group size: the 8 of a matrix instruction,
+// filled by several sequences where they share a prefix.
+template <int COLS>
+cudaError_t launch_own(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t st) {
+    using L = Launcher<MmaTile<COLS>, COLS>;
+    cudaError_t e = cudaFuncSetAttribute(decode_shared_kernel<COLS>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, L::Lay::kCtaBytes);
+    if (e != cudaSuccess) return e;
+    CUtensorMap mk, mv;
+    const int bs = 1 << a.block_size_log2;
+    if (!make_tile_map(&mk, a.k_cache, a.num_blocks, bs, a.num_kv_heads, a.head_major != 0) ||
+        !make_tile_map(&mv, a.v_cache, a.num_blocks, bs, a.num_kv_heads, a.head_major != 0))
+        return cudaErrorInvalidValue;
+    DecodeArgs ac = a;
+    SharedArgs sc = sh;
+    void *args[] = {&ac, &sc, &mk, &mv};
+    e = L::launch_pdl(reinterpret_cast<const void *>(&decode_shared_kernel<COLS>),
+                      dim3((a.num_workers + kWarps - 1) / kWarps), kWarps * 32, L::Lay::kCtaBytes, args, st);
+    if (e != cudaSuccess) return e;
+    const void *combine = reinterpret_cast<const void *>(&combine_shared_kernel<COLS, COLS>);
+    if constexpr (COLS == 8) {
+        if (sh.group_pad == 1) combine = reinterpret_cast<const void *>(&combine_shared_kernel<1, 8>);
+        if (sh.group_pad == 2) combine = reinterpret_cast<const void *>(&combine_shared_kernel<2, 8>);
+        if (sh.group_pad == 4) combine = reinterpret_cast<const void *>(&combine_shared_kernel<4, 8>);
+    }
+    e = L::launch_pdl(combine, dim3((unsigned)(((int64_t)a.num_seqs * sh.group_pad + 7) / 8), a.num_kv_heads),
+                      256, 0, args, st);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 template <int GP>
 int ctas_per_sm_for(DecodeKernel k) {
@@ -1229,16 +1305,8 @@ void decode_carve_workspace(DecodeArgs &a, void *workspace, int group_pad) {
     a.tasks = reinterpret_cast<int4 *>(p);
 }
 
-cudaError_t launch_decode_shared(const DecodeArgs &a, const SharedArgs &sh, int group_pad,
-                                 cudaStream_t stream) {
-    switch (group_pad) {
-        case 1: return Launcher<MmaTile<1>, 1>::launch(a, stream, &sh);
-        case 2: return Launcher<MmaTile<2>, 2>::launch(a, stream, &sh);
-        case 4: return Launcher<MmaTile<4>, 4>::launch(a, stream, &sh);
-        case 8: return Launcher<MmaTile<8>, 8>::launch(a, stream, &sh);
-        case 16: return Launcher<MmaTile<16>, 16>::launch(a, stream, &sh);
-        default: return cudaErrorInvalidValue;
-    }
+cudaError_t launch_decode_shared(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t stream) {
+    return sh.group_pad <= 8 ? launch_own<8>(a, sh, stream) : launch_own<16>(a, sh, stream);
 }
 
 cudaError_t launch_decode(const DecodeArgs &a, int group_pad, DecodeKernel k, cudaStream_t stream) {

@@ -158,58 +158,109 @@ __device__ __forceinline__ void piece_end(SharedWalk &w) {
 
 // -- plan ------------------------------------------------------------------------
 
-// Inclusive scan of v over the CTA's 1024 threads; `sums` is scratch of 32.
-__device__ __forceinline__ long long block_scan(long long v, long long *sums) {
+// Inclusive scans over the CTA's 1024 threads, several at once; `total` gets
+// the sums over all threads. `sums` is scratch; the next call may follow at once.
+template <int N, class T>
+__device__ __forceinline__ void block_scan(T (&v)[N], T (&total)[N], T (*sums)[kPlanThreads / 32]) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const long long n = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += n;
+    for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const T n = __shfl_up_sync(0xffffffffu, v[k], off);
+            if (lane >= off) v[k] += n;
+        }
+    if (lane == 31)
+#pragma unroll
+        for (int k = 0; k < N; ++k) sums[k][warp] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        T w = sums[k][lane];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const T n = __shfl_up_sync(0xffffffffu, w, off);
+            if (lane >= off) w += n;
+        }
+        total[k] = __shfl_sync(0xffffffffu, w, 31);
+        const T before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+        v[k] += warp > 0 ? before : 0;
     }
     __syncthreads();
-    if (lane == 31) sums[warp] = v;
-    __syncthreads();
-    long long before = 0;
-    for (int i = 0; i < warp; ++i) before += sums[i];
-    return v + before;
 }
 
-// Estimated time (us) when x of the SMs compute `tiles` prefix tiles of `units`
-// units and the others read `own` 16-token tiles at the same time. Measured: a
-// prefix tile pair takes 2.3 us on an SM, 2.6 beside the other reads; a piece
-// (its queries, first keys, last product and rows) 3 us; an SM reads 75 GB/s of
-// K and V, and all together 6.4 TB/s. Equal shares of one group's units that
-// end where units end have no piece more than they need. With x = all SMs the
-// own tiles come after. Batch of 128 sequences x 64 heads, 2048 shared tokens
-// and 256 own: x = 152, 88, 64, 40 took 65, 50, 48, 63 us.
-__device__ __forceinline__ float split_cost(int x, int sms, long long tiles, long long units,
-                                            long long own, bool one_group) {
-    constexpr float kTile = 2.6f, kTileAlone = 2.3f, kPiece = 3.f, kRate = 75e3f, kRateAll = 6.4e6f;
-    const float own_bytes = (float)own * (2.f * kTileBytes);
-    const long long share = (tiles + x - 1) / x;
-    const float nt = (float)tiles / (float)units;
-    float pieces = 1.f + (float)share / nt;
-    if (one_group && tiles % x == 0) {
-        const long long n = tiles / units;
-        if (n % share == 0) pieces = 1.f;
-        else if (share % n == 0) pieces = (float)(share / n);
+// How a group's prefix is computed: not apart, by decode_shared_kernel for as
+// many sequences at a time as fill the 8 columns of its tiles, or by
+// shared_prefix_kernel.
+enum Kind { kAlone, kPacked, kTensor };
+
+// The cheapest, in SM time per KV head (us): 128 tokens take decode_shared_kernel
+// 0.8 us for up to 8 columns (90 GB/s of K and V on an SM, once they are in L2);
+// a key tile takes the prefix kernel 2.6 us for 256 rows, 1.6 when they fit one
+// query tile, and every unit 3 us more.
+__device__ __forceinline__ Kind cheapest(int live, int n, int tokens, int group, int group_pad,
+                                         bool tensor_ok) {
+    const int fit = shared_fit(group);
+    const float len = (float)tokens * (1.f / kKeys);
+    const float packed = 0.8f * len * (float)((n + fit - 1) / fit);
+    const float pairs = (float)(((long long)n * group_pad + kPairRows - 1) / kPairRows);
+    const float tensor = pairs * (3.f + ceilf(len) * (n * group_pad <= kRows ? 1.6f : 2.6f));
+    if (live < kSharedMinSeqs || tokens == 0) return kAlone;
+    if (tensor_ok && tensor < packed) return kTensor;
+    return fit > 1 ? kPacked : kAlone;
+}
+
+// How many of the SMs compute the `tiles` prefix tiles of `units` units, while
+// the others work through `own` 16-token tiles. Measured: a prefix tile pair
+// takes 2.3 us on an SM beside the other reads, a piece of a unit (its queries,
+// first keys, last product and rows) 3 us more, and an SM reads 75 GB/s of K
+// and V, all together 6.4 TB/s. SMs go to both in the proportion of the work,
+// so that both end together. A count that is a multiple of the units gives
+// every SM one piece instead of two or more, and is taken when the longest
+// share is the shorter for it. (128 sequences x 64 heads, 2048 shared tokens and
+// 256 own: 152, 88, 64 and 40 SMs took 65, 50, 48 and 63 us.)
+__device__ __forceinline__ int prefix_sms(int sms, float tiles, float units, float own) {
+    constexpr float kTile = 2.3f, kPiece = 3.f, kRate = 75e3f, kRateAll = 6.4e6f;
+    const float bytes = own * (2.f * kTileBytes);
+    const float nt = tiles / units;
+    // the prefix needs a, the rest b SM microseconds; the rest is not faster
+    // than kRateAll, so more SMs than that takes need not be left to it
+    auto time = [&](float x, float pieces) {
+        return fmaxf(pieces * kPiece + ceilf(tiles / x) * kTile,
+                     x < (float)sms ? kPiece + bytes / fminf(((float)sms - x) * kRate, kRateAll) : 1e30f);
+    };
+    const float a = tiles * (kTile + kPiece / nt), b = bytes / kRate + 1.f;
+    float best = fmaxf(1.f, fminf(floorf((float)sms * a / (a + b) + 0.5f), (float)sms - 1.f));
+    best = fminf(best, tiles);
+    float t = time(best, tiles / best <= 1.f ? 1.f : 2.f + tiles / (best * nt));
+    const float k = floorf(best / units);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float x = (k + (float)i) * units;
+        if (x >= 1.f && x < (float)sms && x <= tiles) {
+            const float u = time(x, 1.f);
+            if (u < t) {
+                t = u;
+                best = x;
+            }
+        }
     }
-    if (x == sms) return pieces * kPiece + (float)share * kTileAlone + own_bytes / kRateAll;
-    const float rate = fminf((float)(sms - x) * kRate, kRateAll);
-    return fmaxf(pieces * kPiece + (float)share * kTile, kPiece + own_bytes / rate);
+    return (int)best;
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1)
 shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
-    extern __shared__ long long plan_smem[];
-    __shared__ long long s_sums[32];
-    __shared__ unsigned long long s_best;
-    const int G = sh.num_groups, S = a.num_seqs, tid = threadIdx.x;
-    long long *bases = plan_smem;       // [G] flat index of the group's first tile
-    int *starts = reinterpret_cast<int *>(bases + G);   // [G + 1]
-    int *shortest = starts + G + 1;     // [G] shortest non-empty length, then tokens computed together
-    int *first = shortest + G;          // [G] first non-empty sequence
-    int *live = first + G;              // [G] non-empty sequences, then index among the active groups or -1
+    extern __shared__ int plan_smem[];
+    __shared__ long long s_sums[1][kPlanThreads / 32];
+    __shared__ int s_counts[3][kPlanThreads / 32];
+    const int G = sh.num_groups, S = a.num_seqs, tid = threadIdx.x, lane = tid & 31;
+    const int Hkv = a.num_kv_heads;
+    int *bases = plan_smem;             // [G] flat index of the group's first tile
+    int *starts = bases + G;            // [G + 1]
+    int *tokens = starts + G + 1;       // [G] shortest non-empty length, then tokens computed together
+    int *first = tokens + G;            // [G] first non-empty sequence
+    int *where = first + G;             // [G] non-empty sequences, then index of the active group or
+                                        //     -2 - first entry of the packed prefix, or -1
     // programmatic dependent of whatever precedes the call
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -223,11 +274,14 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
     for (int g = tid; g <= G; g += kPlanThreads) {
         starts[g] = clamp(sh.group_starts[g], S);
         if (g < G) {
-            shortest[g] = first[g] = INT_MAX;
-            live[g] = 0;
+            tokens[g] = first[g] = INT_MAX;
+            where[g] = 0;
         }
     }
     __syncthreads();
+    bool falls = false;
+    for (int g = tid; g < G; g += kPlanThreads) falls |= starts[g] > starts[g + 1];
+    const bool ordered = !__syncthreads_or(falls);     // else nothing is shared
     // the group of sequence s: the last one that starts at or before it
     auto group_of = [&](int s) {
         int lo = 0, hi = G;
@@ -238,91 +292,114 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
         return starts[lo] <= s && s < starts[lo + 1] ? lo : -1;
     };
     const int s_lo = starts[0], s_hi = starts[G];
-    for (int s = tid; s < s_hi; s += kPlanThreads) {
-        const int g = s < s_lo ? -1 : group_of(s), L = length(s);
-        if (g >= 0 && L > 0) {
-            atomicMin(shortest + g, L);
+    const int covered = s_hi > s_lo ? s_hi - s_lo : 0;
+    int my_group = -1;                  // group of sequence tid
+    for (int s0 = 0; s0 < s_hi; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        const int g = s < s_lo || s >= s_hi ? -1 : group_of(s);
+        if (s0 == 0) my_group = g;
+        const int L = g >= 0 ? length(s) : 0;
+        const bool live = L > 0;
+        // one atomic per warp where its sequences are of one group
+        const int g0 = __shfl_sync(0xffffffffu, g, 0);
+        if (__all_sync(0xffffffffu, g == g0)) {
+            const int least = __reduce_min_sync(0xffffffffu, live ? L : INT_MAX);
+            const unsigned m = __ballot_sync(0xffffffffu, live);
+            if (m != 0 && lane == 0) {
+                atomicMin(tokens + g0, least);
+                atomicMin(first + g0, s + __ffs(m) - 1);
+                atomicAdd(where + g0, __popc(m));
+            }
+        } else if (live) {
+            atomicMin(tokens + g, L);
             atomicMin(first + g, s);
-            atomicAdd(live + g, 1);
+            atomicAdd(where + g, 1);
         }
     }
     __syncthreads();
-    long long base = 0, units = 0;
-    int act = 0;
+    int base = 0, units = 0, act = 0, entries = covered;    // the host has ruled out 2^31 tiles
     for (int g0 = 0; g0 < G; g0 += kPlanThreads) {
         const int g = g0 + tid;
         SharedGroup gr{};
-        long long tiles = 0;
+        Kind kind = kAlone;
+        int chunks = 0;
+        const int fit = shared_fit(a.group);
         if (g < G) {
             const int64_t want = (int64_t)clamp(g0 == 0 ? my_prefix : sh.prefix_blocks[g], a.max_blocks_per_seq)
                                  << a.block_size_log2;
-            const int most = live[g] > 0 ? shortest[g] & ~15 : 0;
-            gr.tokens = live[g] >= kSharedMinSeqs ? (int)(want < most ? want : most) : 0;
+            const int most = where[g] > 0 ? tokens[g] & ~15 : 0;
+            gr.tokens = (int)(want < most ? want : most);
             gr.row = first[g];
             gr.s0 = starts[g];
             gr.n = starts[g + 1] - starts[g];
+            if (ordered) kind = cheapest(where[g], gr.n, gr.tokens, a.group, sh.group_pad, sh.tensor != 0);
             gr.nt = (gr.tokens + kKeys - 1) / kKeys;
             gr.pairs = (int)(((int64_t)gr.n * sh.group_pad + kPairRows - 1) / kPairRows);
-            tiles = (long long)gr.nt * gr.pairs * a.num_kv_heads;
+            if (kind == kPacked) chunks = (gr.n + fit - 1) / fit;
         }
-        const long long t_end = block_scan(tiles, s_sums);
-        const long long u_end = block_scan(tiles > 0 ? ((long long)gr.pairs * a.num_kv_heads << 16) + 1 : 0, s_sums);
-        const int a_end = (int)(u_end & 0xffff);        // at most kMaxGroups
+        const bool tensor = kind == kTensor;
+        const int u = tensor ? gr.pairs * Hkv : 0, tiles = u * gr.nt;
+        // the active groups in the low 13 bits (kMaxGroups at most)
+        int v[3] = {tiles, u, (chunks << 13) + tensor}, total[3];
+        block_scan(v, total, s_counts);
         if (g < G) {
-            const int at = act + a_end - 1;
-            gr.base = base + t_end - tiles;
+            gr.base = base + v[0] - tiles;
             bases[g] = gr.base;
-            shortest[g] = gr.tokens;
-            live[g] = tiles > 0 ? at : -1;
-            if (tiles > 0) sh.groups[at] = gr;
+            tokens[g] = kind == kAlone ? 0 : gr.tokens;
+            where[g] = -1;
+            if (tensor) {
+                const int at = act + (v[2] & 0x1fff) - 1;
+                where[g] = at;
+                sh.groups[at] = gr;
+            } else if (kind == kPacked) {
+                const int at = entries + (v[2] >> 13) - chunks;
+                where[g] = -2 - at;
+                for (int c = 0; c < chunks; ++c) {
+                    const int n = gr.n - c * fit < fit ? gr.n - c * fit : fit;
+                    sh.entries[at + c] = SharedUnit{gr.row, gr.s0 + c * fit, 0, gr.tokens, n * a.group, 3, {0, 0}};
+                }
+            }
         }
-        __syncthreads();
-        if (tid == kPlanThreads - 1) s_sums[0] = t_end, s_sums[1] = u_end;
-        __syncthreads();
-        base += s_sums[0];
-        act += (int)(s_sums[1] & 0xffff);
-        units += s_sums[1] >> 16;
-        __syncthreads();
+        base += total[0];
+        units += total[1];
+        act += total[2] & 0x1fff;
+        entries += total[2] >> 13;
     }
+    __syncthreads();
     long long own = 0;
-    for (int c0 = s_lo; c0 < s_hi; c0 += kPlanThreads) {
-        const int s = c0 + tid;
-        long long n = 0;
-        if (s < s_hi) {
-            const int g = group_of(s), L = length(s);
-            const bool in = g >= 0 && live[g] >= 0 && L > 0;
-            const int start = in ? shortest[g] : 0;
-            sh.seq[s] = make_int2(start, in ? live[g] : -1);
-            n = L > start ? (L - start + kTileTokens - 1) / kTileTokens : 1;   // an empty unit owns one tile
+    for (int v0 = 0; v0 < entries; v0 += kPlanThreads) {
+        const int v = v0 + tid;
+        long long n[1] = {0}, total[1];
+        if (v < covered) {
+            const int s = s_lo + v;
+            const int g = s == tid ? my_group : group_of(s), L = length(s);
+            const int start = g >= 0 && L > 0 ? tokens[g] : 0;
+            const int at = start > 0 ? where[g] : -1;
+            const int nth = start > 0 ? s - starts[g] : 0, fit = shared_fit(a.group);
+            sh.seq[s] = at <= -2 ? make_int4(-1, -2 - at + nth / fit, nth % fit * a.group, 0)
+                                 : make_int4(at, -1, 0, 0);
+            sh.entries[v] = SharedUnit{s, s, start, L, a.group, start > 0 ? 1 : 0, {0, 0}};
+            // an empty unit owns one (empty) tile
+            n[0] = L > start ? (L - start + kTileTokens - 1) / kTileTokens : 1;
+        } else if (v < entries) {
+            n[0] = sh.entries[v].len / kTileTokens;
         }
-        const long long end = block_scan(n, s_sums);
-        if (s < s_hi) sh.scan[s] = own + end;
-        __syncthreads();
-        if (tid == kPlanThreads - 1) s_sums[0] = end;
-        __syncthreads();
-        own += s_sums[0];
-        __syncthreads();
+        block_scan(n, total, s_sums);
+        if (v < entries) sh.scan[v] = own + n[0];
+        own += total[0];
     }
-    own *= a.num_kv_heads;
-    // how many SMs compute prefixes while the others read the own tiles
+    own *= Hkv;
     const int sms = sh.max_workers, per_sm = a.num_workers / sms;
-    if (tid == 0) s_best = ~0ull;
-    __syncthreads();
-    for (int x = 1 + tid; x <= sms && x <= base; x += kPlanThreads) {
-        const float cost = split_cost(x, sms, base, units, own, act == 1);
-        atomicMin(&s_best, ((unsigned long long)__float_as_uint(cost) << 32) | (unsigned)x);
-    }
-    __syncthreads();
-    const int workers = base > 0 ? (int)(s_best & 0xffffffffu) : 0;
+    const int workers = base > 0 ? prefix_sms(sms, (float)base, (float)units, (float)own) : 0;
     if (tid == 0) {
         SharedHeader h;
         h.tiles = base;
         h.own_tiles = own;
         h.s_lo = s_lo;
         h.s_hi = s_hi;
+        h.entries = entries;
         h.workers = workers;
-        const int64_t most = own / a.min_tiles;
-        const int beside = workers < sms ? (sms - workers) * per_sm : a.num_workers;
+        const int64_t beside = (int64_t)(sms - workers) * per_sm, most = own / a.min_tiles;
         h.own_workers = (int)(most < 1 ? 1 : (most < beside ? most : beside));
         *sh.hdr = h;
     }
@@ -338,11 +415,10 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
             const int mid = (lo + hi) >> 1;
             if (bases[mid] <= k.T) lo = mid; else hi = mid;
         }
-        k.act = live[lo];
+        k.act = where[lo];
         k.gr = sh.groups[k.act];
-        const int64_t rem = k.T - k.gr.base;
-        const int unit = (int)(rem / k.gr.nt);
-        k.j0 = (int)(rem - (int64_t)unit * k.gr.nt);
+        const int rem = (int)(k.T - k.gr.base), unit = rem / k.gr.nt;
+        k.j0 = rem - unit * k.gr.nt;
         k.kvh = unit / k.gr.pairs;
         k.pair = unit - k.kvh * k.gr.pairs;
         piece_end(k);
@@ -401,6 +477,11 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5;
     const int w_id = blockIdx.x;
+    if (tid == 0) {
+        tc::prefetch_map(&tmap_k);
+        tc::prefetch_map(&tmap_v);
+        tc::prefetch_map(&tmap_q);
+    }
     const uint32_t sbase = smem_u32(smem);
     if (sbase & 1023u) {                        // the swizzle atoms need 1024-byte alignment
         if (tid == 0) set_error(kErrSmemAlign);
@@ -830,22 +911,23 @@ cudaError_t launch_g(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t st)
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct Carve {
-    size_t hdr, seq, scan, groups, walks, part_o, part_ml, unit_o, unit_ml, units, own_o, own_ml, end;
+    size_t hdr, seq, entries, scan, groups, walks, part_o, part_ml, unit_o, unit_ml, units, whole_o, whole_ml, end;
     Carve(int S, int G, int hq, int hkv, int gp, int workers) {
         const size_t rows = (size_t)S * gp * hkv, own = (size_t)S * hq, slots = 2 * (size_t)workers;
         hdr = 0;
         seq = hdr + round256(sizeof(SharedHeader));
-        scan = seq + round256((size_t)S * sizeof(int2));
-        groups = scan + round256((size_t)S * sizeof(long long));
+        entries = seq + round256((size_t)S * sizeof(int4));
+        scan = entries + round256(2 * (size_t)S * sizeof(SharedUnit));
+        groups = scan + round256(2 * (size_t)S * sizeof(long long));
         walks = groups + round256((size_t)G * sizeof(SharedGroup));
         part_o = walks + round256((size_t)workers * sizeof(SharedWalk));
         part_ml = part_o + slots * 32 * kPairRows * sizeof(float4);
         unit_o = part_ml + slots * kPairRows * sizeof(float2);
         unit_ml = unit_o + rows * 32 * sizeof(float4);
         units = unit_ml + round256(rows * sizeof(float2));
-        own_o = units + round256((size_t)S * hkv * sizeof(int4));
-        own_ml = own_o + own * 32 * sizeof(float4);
-        end = own_ml + round256(own * sizeof(float2));
+        whole_o = units + round256(2 * (size_t)S * hkv * sizeof(int4));
+        whole_ml = whole_o + 2 * own * 32 * sizeof(float4);
+        end = whole_ml + round256(2 * own * sizeof(float2));
     }
 };
 
@@ -864,7 +946,8 @@ void shared_carve_workspace(SharedArgs &sh, void *workspace, const DecodeArgs &a
     const Carve c(a.num_seqs, sh.num_groups, a.num_q_heads, a.num_kv_heads, sh.group_pad, sh.max_workers);
     char *p = static_cast<char *>(workspace);
     sh.hdr = reinterpret_cast<SharedHeader *>(p + c.hdr);
-    sh.seq = reinterpret_cast<int2 *>(p + c.seq);
+    sh.seq = reinterpret_cast<int4 *>(p + c.seq);
+    sh.entries = reinterpret_cast<SharedUnit *>(p + c.entries);
     sh.scan = reinterpret_cast<long long *>(p + c.scan);
     sh.groups = reinterpret_cast<SharedGroup *>(p + c.groups);
     sh.walks = reinterpret_cast<SharedWalk *>(p + c.walks);
@@ -873,14 +956,14 @@ void shared_carve_workspace(SharedArgs &sh, void *workspace, const DecodeArgs &a
     sh.unit_o = reinterpret_cast<float4 *>(p + c.unit_o);
     sh.unit_ml = reinterpret_cast<float2 *>(p + c.unit_ml);
     sh.units = reinterpret_cast<int4 *>(p + c.units);
-    sh.own_o = reinterpret_cast<float4 *>(p + c.own_o);
-    sh.own_ml = reinterpret_cast<float2 *>(p + c.own_ml);
+    sh.whole_o = reinterpret_cast<float4 *>(p + c.whole_o);
+    sh.whole_ml = reinterpret_cast<float2 *>(p + c.whole_ml);
 }
 
 cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t stream) {
-    const size_t plan_smem = (6 * (size_t)sh.num_groups + 1) * sizeof(int);
+    const size_t plan_smem = (5 * (size_t)sh.num_groups + 1) * sizeof(int);
     cudaError_t e = cudaFuncSetAttribute(shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)((6 * kMaxGroups + 1) * sizeof(int)));
+                                         (int)((5 * kMaxGroups + 1) * sizeof(int)));
     if (e != cudaSuccess) return e;
     DecodeArgs ac = a;
     SharedArgs sc = sh;
@@ -888,6 +971,7 @@ cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedArgs &sh, cuda
     e = launch_dependent(reinterpret_cast<const void *>(&shared_plan_kernel), 1, kPlanThreads, plan_smem,
                          args, stream);
     if (e != cudaSuccess) return e;
+    if (!sh.tensor) return cudaSuccess;
     switch (sh.group_pad) {
         case 1: return launch_g<1>(a, sh, stream);
         case 2: return launch_g<2>(a, sh, stream);

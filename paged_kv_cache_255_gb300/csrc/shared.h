@@ -6,8 +6,10 @@
 
 namespace pa {
 
-constexpr int kSharedMaxGroups = 4096;  // groups of one call (the plan keeps 24 bytes each in shared memory)
+constexpr int kSharedMaxGroups = 4096;  // groups of one call (the plan keeps 20 bytes each in shared memory)
 constexpr int kSharedMinSeqs = 2;       // a prefix is computed apart for at least this many sequences
+// Sequences whose heads fit the 8 columns of one unit of decode_shared_kernel.
+__host__ __device__ constexpr int shared_fit(int group) { return group <= 8 ? 8 / group : 1; }
 constexpr int kPairRows = 256;      // rows of a prefix unit: two query tiles of 128
 
 // A group whose prefix is computed once. Its tile space: (KV head, pair of
@@ -33,8 +35,20 @@ struct SharedHeader {
     int64_t tiles;          // prefix: key tiles of all active groups
     int64_t own_tiles;      // what follows it: 16-token tiles of all units (decode.cu)
     int s_lo, s_hi;         // sequences the call covers
+    int entries;            // of SharedArgs::entries
     int workers;            // CTAs the prefix tiles are shared among
     int own_workers;        // warps the own tiles are shared among
+};
+
+// An entry of decode_shared_kernel's work list: for every KV head, a unit of
+// the tokens [start, len) of a table row for `cols` query rows.
+struct alignas(16) SharedUnit {
+    int row;                // table row
+    int first;              // sequence of the first query row; the heads of the next ones follow
+    int start, len;         // start is a multiple of 16
+    int cols;
+    int part;               // other parts of the same query rows exist: +1; it is a prefix: +2
+    int pad[2];
 };
 
 // Pointers are device memory.
@@ -44,19 +58,21 @@ struct SharedArgs {
     int num_groups;
     int group_pad;                  // G: query heads per KV head, rounded up to a power of two
     int max_workers;                // CTAs of the prefix kernel
+    int tensor;                     // whether the prefix kernel is launched
     // in the workspace
     SharedHeader *hdr;
-    int2 *seq;                      // [S] tokens computed with the group's prefix, active group or -1
-    long long *scan;                // [S] own tiles of one KV head through sequence s
+    int4 *seq;                      // [S] {active group or -1, entry of its packed prefix or -1, column there}
+    SharedUnit *entries;            // [2 S] own tokens of every covered sequence, then packed prefixes
+    long long *scan;                // [2 S] tiles of one KV head through an entry
     SharedGroup *groups;            // [num_groups] the active ones
     SharedWalk *walks;              // [max_workers] first piece of every share
     float4 *part_o;                 // [2 max_workers][32][256] pieces of units that several workers share
     float2 *part_ml;                // [2 max_workers][256] (running max in log2 units, sum)
     float4 *unit_o;                 // [Hkv][32][S G] units one worker computed whole
     float2 *unit_ml;                // [Hkv][S G]
-    int4 *units;                    // [S Hkv] where a unit's own parts are (decode.cu)
-    float4 *own_o;                  // [S Hq][32] own part of units one share computed whole
-    float2 *own_ml;                 // [S Hq]
+    int4 *units;                    // [2 S Hkv] where the parts of an entry's units are (decode.cu)
+    float4 *whole_o;                // [2 S Hq][32] units one share computed whole: own, then packed
+    float2 *whole_ml;               // [2 S Hq]
 };
 
 size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
@@ -65,8 +81,7 @@ void shared_carve_workspace(SharedArgs &sh, void *workspace, const DecodeArgs &a
 
 // Plan and prefixes, then (launch_decode_shared) the rest and the combine.
 cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t stream);
-cudaError_t launch_decode_shared(const DecodeArgs &a, const SharedArgs &sh, int group_pad,
-                                 cudaStream_t stream);
+cudaError_t launch_decode_shared(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t stream);
 cudaError_t take_shared_error(cudaStream_t stream, int *code);
 
 }  // namespace pa

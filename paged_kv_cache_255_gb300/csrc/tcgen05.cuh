@@ -196,6 +196,10 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
+// The descriptor of a kernel-parameter tensor map on its way before its first use.
+__device__ __forceinline__ void prefetch_map(const void *tmap) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
 // Tiled 3-D tensor copy global -> shared (box of the tensor map at
 // coordinates c0 (innermost), c1, c2); completion counted on `bar` in bytes.
 // Coordinates outside the tensor read as zero.

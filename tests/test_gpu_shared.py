@@ -154,9 +154,11 @@ def test_sequences_shorter_than_their_prefix():
 
 
 def test_groups_of_one_and_no_prefix_are_plain_decode():
+    # decode's sums over other shares of the tokens: each result is within the
+    # bound above, which does not depend on how the sums are split
     b = Batch([1] * 9, [4] * 9, [5, 100, 33])
-    out = b.check()
-    assert torch.equal(out, pa.decode(b.q, b.k, b.v, b.tables, b.lens, b.scale))
+    b.check()
+    b.check(pa.decode(b.q, b.k, b.v, b.tables, b.lens, b.scale))
     Batch([5, 4], [0, 0], [5, 100, 33]).check()
 
 
