@@ -1214,8 +1214,8 @@ struct Launcher {
 template <int COLS>
 cudaError_t launch_own(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t st) {
     using L = Launcher<MmaTile<COLS>, COLS>;
-    cudaError_t e = cudaFuncSetAttribute(decode_shared_kernel<COLS>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, L::Lay::kCtaBytes);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(reinterpret_cast<const void *>(&decode_shared_kernel<COLS>), L::Lay::kCtaBytes);
     if (e != cudaSuccess) return e;
     CUtensorMap mk, mv;
     const int bs = 1 << a.block_size_log2;

@@ -104,12 +104,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __forceinline__ float fmin3(float a, float b, float c) {
-    float r;
-    asm("min.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
@@ -534,9 +528,7 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
         const int wg = tid >> 7, r = tid & 127;
         const uint32_t lane = (uint32_t)(r & ~31) << 16;
         const uint32_t tS = tmem + lane + wg * 256, tO = tS + 128;
-        const float sc = a.scale_log2;
-        // loses against every score whatever the scale's sign
-        const float masked = sc >= 0.f ? -INFINITY : INFINITY;
+        const float sc = a.scale_log2;          // above 0
         uint32_t gt = 0;                        // this query tile's key tiles before this piece
         bool ok = true;
         int piece = 0;
@@ -561,32 +553,19 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
                     for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
                         for (int c = 0; c < 32; ++c)
-                            if (c >= nkeys - ch * 32) sr[ch][c] = __float_as_uint(masked);
+                            if (c >= nkeys - ch * 32) sr[ch][c] = 0xff800000u;     // -inf
                 }
-                // the extreme raw score of the row, in four running values
-                float e4[4] = {masked, masked, masked, masked};
-                if (sc >= 0.f) {
+                // the largest raw score of the row, in four running values
+                float e4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch)
+                for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
-                        for (int c = 0; c < 32; c += 8)
+                    for (int c = 0; c < 32; c += 8)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                e4[k] = fmax3(e4[k], __uint_as_float(sr[ch][c + 2 * k]),
-                                              __uint_as_float(sr[ch][c + 2 * k + 1]));
-                } else {
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-                        for (int c = 0; c < 32; c += 8)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                e4[k] = fmin3(e4[k], __uint_as_float(sr[ch][c + 2 * k]),
-                                              __uint_as_float(sr[ch][c + 2 * k + 1]));
-                }
-                const float ext = sc >= 0.f ? fmax3(fmaxf(e4[0], e4[1]), e4[2], e4[3])
-                                            : fmin3(fminf(e4[0], e4[1]), e4[2], e4[3]);
-                const float mt = ext == masked ? -INFINITY : ext * sc;
+                        for (int k = 0; k < 4; ++k)
+                            e4[k] = fmax3(e4[k], __uint_as_float(sr[ch][c + 2 * k]),
+                                          __uint_as_float(sr[ch][c + 2 * k + 1]));
+                const float mt = fmax3(fmaxf(e4[0], e4[1]), e4[2], e4[3]) * sc;
                 // the max is raised only when a tile exceeds it by 2^8: weights
                 // stay below 2^8, far inside fp32 and bf16 range, and O is
                 // rescaled rarely
@@ -608,12 +587,8 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
                     uint32_t pw[16];
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        float p0 = ex2(fmaf(__uint_as_float(sr[ch][2 * c]), sc, -mb));
-                        float p1 = ex2(fmaf(__uint_as_float(sr[ch][2 * c + 1]), sc, -mb));
-                        if (need_mask) {
-                            p0 = 2 * c < nkeys - ch * 32 ? p0 : 0.f;
-                            p1 = 2 * c + 1 < nkeys - ch * 32 ? p1 : 0.f;
-                        }
+                        const float p0 = ex2(fmaf(__uint_as_float(sr[ch][2 * c]), sc, -mb));
+                        const float p1 = ex2(fmaf(__uint_as_float(sr[ch][2 * c + 1]), sc, -mb));
                         l4[c & 3] += p0 + p1;
                         pw[c] = pack_bf16x2(p0, p1);
                     }
@@ -770,84 +745,69 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
                 if (release) tc::commit(release);
             }
         };
-        auto ready = [](uint32_t b, uint32_t parity) {
-            const bool r = __any_sync(0xffffffffu, tc::mbar_test_wait(b, parity));
-            if (r) __syncwarp();
-            return r;
-        };
-        // S_t(x) once K_x has landed and PV_t(x - 1) has been issued; PV_t(y)
-        // once P_t(y) is in TMEM and V_y has landed (and, for the first of a
-        // piece, the previous piece's O has been read). A stage is released
-        // after its last reader.
-        uint32_t gt = 0, gq0 = 0, gq1 = 0;
-        int piece = 0;
-        bool ok = true;
-#pragma unroll 1
-        do {
-            const int nta = piece_tiles<G>(w, 0), ntb = piece_tiles<G>(w, 1);
-            ok = warp_wait(bar(kBarQFull), piece & 1, abort);
-            int sj0 = 0, sj1 = 0, pj0 = 0, pj1 = 0;     // next S / PV tile of A, B
-            uint64_t t_idle = 0;
-            uint32_t idle = 0;
-#pragma unroll 1
-            while (ok && (pj0 < nta || pj1 < ntb)) {
-                bool progress = false;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    int &sj = t == 0 ? sj0 : sj1;
-                    int &pj = t == 0 ? pj0 : pj1;
-                    const int other_pj = t == 0 ? pj1 : pj0;
-                    const int other_sj = t == 0 ? sj1 : sj0;
-                    const int my_nt = t == 0 ? nta : ntb;
-                    const int other_nt = t == 0 ? ntb : nta;
-                    const uint32_t my_gq = t == 0 ? gq0 : gq1;
-                    if (pj < sj) {
-                        const uint32_t gp = gt + pj;
-                        const int st = gp % kVStages;
-                        bool go = ready(bar(kBarPReady + t), (my_gq + pj) & 1) &&
-                                  ready(bar(kBarVFull + st), (gp / kVStages) & 1);
-                        if (go && pj == 0 && piece > 0) go = ready(bar(kBarOFree + t), (piece - 1) & 1);
-                        if (go) {
-                            issue_pv(t, st, pj > 0, groups_used(w, w.j0 + pj),
-                                     other_pj > pj || other_nt <= pj ? bar(kBarVEmpty + st) : 0u);
-                            ++pj;
-                            progress = true;
-                        }
-                    }
-                    if (sj == pj && sj < my_nt) {
-                        const uint32_t gs = gt + sj;
-                        const int st = gs % kKStages;
-                        if (ready(bar(kBarKFull + st), (gs / kKStages) & 1)) {
-                            issue_s(t, st, other_sj > sj || other_nt <= sj ? bar(kBarKEmpty + st) : 0u);
-                            ++sj;
-                            progress = true;
-                        }
-                    }
+        // the warp polls, converged: the answer to every lane's test, bounded
+        auto await = [&](uint32_t b, uint32_t parity) {
+            uint64_t t0 = 0;
+            for (uint32_t i = 0;; ++i) {
+                if (__any_sync(0xffffffffu, tc::mbar_test_wait(b, parity))) {
+                    __syncwarp();
+                    return true;
                 }
-                if (progress) {
-                    idle = 0;
-                    continue;
-                }
-                if (++idle == 1) {
-                    t_idle = tc::globaltimer_ns();
-                } else if ((idle & 255) == 0) {
+                if (i == 0) t0 = tc::globaltimer_ns();
+                if ((i & 255) == 255) {
                     const bool stop = __shfl_sync(0xffffffffu,
-                                                  (*abort || tc::globaltimer_ns() - t_idle > 2000000000ull) ? 1 : 0, 0) != 0;
+                                                  (*abort || tc::globaltimer_ns() - t0 > 2000000000ull) ? 1 : 0, 0) != 0;
                     if (stop) {
                         if ((threadIdx.x & 31) == 0 && !*abort) {
                             set_error(kErrTimeout);
                             *abort = 1;
                         }
-                        ok = false;
+                        return false;
                     }
+                }
+            }
+        };
+        // In turn: PV_A(j), S_A(j + 1), PV_B(j), S_B(j + 1). PV_t(j) once P_t(j)
+        // is in TMEM (and, for the first of a piece, the previous piece's O has
+        // been read); the tiles it and S need have been waited for before, off
+        // the chain from P to S. A stage is released after its last reader.
+        uint32_t gt = 0, gq0 = 0, gq1 = 0;
+        int piece = 0;
+        bool ok = true;
+#pragma unroll 1
+        do {
+            const int nt = w.j1 - w.j0;
+            const bool two = piece_tiles<G>(w, 1) > 0;
+            ok = await(bar(kBarQFull), piece & 1) && await(bar(kBarKFull + gt % kKStages), (gt / kKStages) & 1);
+            if (ok) {
+                issue_s(0, gt % kKStages, two ? 0u : bar(kBarKEmpty + gt % kKStages));
+                if (two) issue_s(1, gt % kKStages, bar(kBarKEmpty + gt % kKStages));
+            }
+#pragma unroll 1
+            for (int j = 0; ok && j < nt; ++j) {
+                const uint32_t gp = gt + j, gs = gp + 1;
+                const int vs = gp % kVStages, ks = gs % kKStages;
+                const bool more = j + 1 < nt;
+                const int nv = groups_used(w, w.j0 + j);
+                ok = await(bar(kBarVFull + vs), (gp / kVStages) & 1);
+                if (ok && more) ok = await(bar(kBarKFull + ks), (gs / kKStages) & 1);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t == 1 && !two) break;
+                    const bool last = t == 1 || !two;
+                    if (ok && j == 0 && piece > 0) ok = await(bar(kBarOFree + t), (piece - 1) & 1);
+                    if (ok) ok = await(bar(kBarPReady + t), ((t == 0 ? gq0 : gq1) + j) & 1);
+                    if (!ok) break;
+                    issue_pv(t, vs, j > 0, nv, last ? bar(kBarVEmpty + vs) : 0u);
+                    if (more) issue_s(t, ks, last ? bar(kBarKEmpty + ks) : 0u);
                 }
             }
             // the queries' buffers are free once this piece's MMAs are done
             if (tc::elect_one()) tc::commit(bar(kBarQEmpty));
             __syncwarp();
-            gt += w.j1 - w.j0;
-            gq0 += nta;
-            gq1 += ntb;
+            gt += nt;
+            gq0 += nt;
+            gq1 += two ? nt : 0;
             ++piece;
         } while (ok && walk_next(w, sh, a.num_kv_heads));
     }
@@ -892,8 +852,8 @@ cudaError_t launch_dependent(const void *fn, unsigned grid, unsigned block, size
 
 template <int G>
 cudaError_t launch_g(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(shared_prefix_kernel<G>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(reinterpret_cast<const void *>(&shared_prefix_kernel<G>), kSmemBytes);
     if (e != cudaSuccess) return e;
     const int bs = 1 << a.block_size_log2;
     CUtensorMap mk, mv, mq;
@@ -962,8 +922,9 @@ void shared_carve_workspace(SharedArgs &sh, void *workspace, const DecodeArgs &a
 
 cudaError_t launch_shared_prefix(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t stream) {
     const size_t plan_smem = (5 * (size_t)sh.num_groups + 1) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(shared_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)((5 * kMaxGroups + 1) * sizeof(int)));
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(reinterpret_cast<const void *>(&shared_plan_kernel),
+                                (int)((5 * kMaxGroups + 1) * sizeof(int)));
     if (e != cudaSuccess) return e;
     DecodeArgs ac = a;
     SharedArgs sc = sh;

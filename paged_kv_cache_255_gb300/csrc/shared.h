@@ -2,6 +2,8 @@
 // and computes the prefixes, decode.cu the rest of every sequence).
 #pragma once
 
+#include <atomic>
+
 #include "kernels.h"
 
 namespace pa {
@@ -73,6 +75,24 @@ struct SharedArgs {
     int4 *units;                    // [2 S Hkv] where the parts of an entry's units are (decode.cu)
     float4 *whole_o;                // [2 S Hq][32] units one share computed whole: own, then packed
     float2 *whole_ml;               // [2 S Hq]
+};
+
+// Raises a kernel's limit of dynamic shared memory, once on every device.
+class SmemLimit {
+  public:
+    cudaError_t raise(const void *kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = (uint64_t)1 << (dev & 63);     // the library's calls take devices 0 .. 63
+        if (done_.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+
+  private:
+    std::atomic<uint64_t> done_{0};
 };
 
 size_t shared_workspace_bytes(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,

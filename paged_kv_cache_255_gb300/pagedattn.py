@@ -325,12 +325,11 @@ def decode_shared(q, k_cache, v_cache, block_tables, context_lens, group_starts,
     decode's, but for the order of the sums. Rows of ``out`` outside all groups
     are left as they were. The other arguments are decode's."""
     dev = q.device
-    for t, n, dt in ((q, "q", torch.bfloat16), (k_cache, "k_cache", torch.bfloat16),
-                     (v_cache, "v_cache", torch.bfloat16), (block_tables, "block_tables", torch.int32),
-                     (context_lens, "context_lens", torch.int32),
-                     (group_starts, "group_starts", torch.int32),
-                     (prefix_blocks, "prefix_blocks", torch.int32)):
-        _cuda(t, n, dt, dev)
+    if not _fits(dev.index, torch.bfloat16, q, k_cache, v_cache):
+        _explain(dev, torch.bfloat16, q=q, k_cache=k_cache, v_cache=v_cache)
+    if not _fits(dev.index, torch.int32, block_tables, context_lens, group_starts, prefix_blocks):
+        _explain(dev, torch.int32, block_tables=block_tables, context_lens=context_lens,
+                 group_starts=group_starts, prefix_blocks=prefix_blocks)
     S, Hq, D = q.shape
     if head_major:
         NB, Hkv, bs, D2 = k_cache.shape
@@ -364,11 +363,11 @@ def decode_shared(q, k_cache, v_cache, block_tables, context_lens, group_starts,
 def decode_shared_workspace_size(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int,
                                  head_dim: int = 128, device=None) -> int:
     """Workspace bytes pa_decode_shared needs on ``device`` (default: current)."""
-    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
-        n = lib().pa_decode_shared_workspace_size(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim)
+    index = torch.cuda.current_device() if device is None else torch.device(device).index
+    n = _size("pa_decode_shared_workspace_size", index, num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim)
     if n == 0:
         raise ValueError("unsupported head configuration or number of groups")
-    return int(n)
+    return n
 
 
 def prefill(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
@@ -438,22 +437,45 @@ class CachePools:
         self._shape = (self.num_kv_heads, self.head_dim, self.block_size, self.num_blocks)
 
 
-def _check_tables(block_tables, context_lens, ref_counts, dev):
-    for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"),
-                 (ref_counts, "ref_counts")):
-        _cuda(t, n, torch.int32, dev)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _fits(index, dtype, *tensors):
+    """Whether every tensor is a contiguous one of this dtype on CUDA device
+    ``index``. The calls below cost a few microseconds on the GPU, less than
+    _cuda takes for each argument in turn; it is asked only for the message."""
+    try:
+        for t in tensors:
+            if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+                return False
+    except (AttributeError, TypeError):
+        return False
+    return True
+
+
+def _explain(dev, dtype, **tensors):
+    """Raise for the first tensor that is why _fits said no."""
+    for n, t in tensors.items():
+        _cuda(t, n, dtype, dev)
+
+
+def _check_table_shapes(block_tables, context_lens, ref_counts):
     if block_tables.dim() != 2 or context_lens.shape != block_tables.shape[:1] or ref_counts.dim() != 1:
         raise ValueError("shape mismatch between block_tables, context_lens and ref_counts")
 
 
 def _call(fn, dev, stream, *args):
     """One library call on ``dev`` and ``stream`` (None: the current one)."""
-    st = _stream_ptr(stream, dev)
-    if torch.cuda.current_device() == dev.index:
-        _check(fn, getattr(lib(), fn)(*args, st))
+    index = dev.index
+    st = _raw_stream(index) if stream is None else stream.cuda_stream
+    f = getattr(_lib or lib(), fn)
+    if torch._C._cuda_getDevice() == index:
+        status = f(*args, st)
     else:
         with torch.cuda.device(dev):
-            _check(fn, getattr(lib(), fn)(*args, st))
+            status = f(*args, st)
+    if status != PA_OK:
+        raise PagedAttnError(fn, status)
 
 
 def _scratch(nbytes, dev, stream):
@@ -465,12 +487,27 @@ def _scratch(nbytes, dev, stream):
     return ws
 
 
+_sizes = {}
+
+
+def _size(fn, index, *args):
+    """The library's answer to a workspace size question, asked once for the
+    same sizes on the same device."""
+    key = (fn, index, args)
+    n = _sizes.get(key)
+    if n is None:
+        with torch.cuda.device(index):
+            n = _sizes[key] = int(getattr(lib(), fn)(*args))
+    return n
+
+
 def copy_blocks(pools: CachePools, block_pairs, stream=None):
     """Block ``block_pairs[i, 1]`` becomes a copy of block ``block_pairs[i, 0]``
     in every pool (int32 [n, 2]; pairs holding -1 are skipped). A block one
     pair writes must not stand in another pair."""
     dev = pools.device
-    _cuda(block_pairs, "block_pairs", torch.int32, dev)
+    if not _fits(dev.index, torch.int32, block_pairs):
+        _explain(dev, torch.int32, block_pairs=block_pairs)
     if block_pairs.dim() != 2 or block_pairs.shape[1] != 2:
         raise ValueError("block_pairs must be [n, 2]")
     _call("pa_copy_blocks", dev, stream, *pools._args, block_pairs.data_ptr(),
@@ -486,9 +523,10 @@ def fork_blocks(pools: CachePools, block_tables, context_lens, ref_counts, paren
     rows must be empty; forks that cannot be made change nothing and are
     recorded (take_device_error: 6)."""
     dev = pools.device
-    _check_tables(block_tables, context_lens, ref_counts, dev)
-    _cuda(parents, "parents", torch.int32, dev)
-    _cuda(children, "children", torch.int32, dev)
+    if not _fits(dev.index, torch.int32, block_tables, context_lens, ref_counts, parents, children):
+        _explain(dev, torch.int32, block_tables=block_tables, context_lens=context_lens,
+                 ref_counts=ref_counts, parents=parents, children=children)
+    _check_table_shapes(block_tables, context_lens, ref_counts)
     n, (rows, width) = parents.shape[0], block_tables.shape
     if parents.dim() != 1 or children.shape != parents.shape:
         raise ValueError("parents and children must be [n]")
@@ -497,7 +535,7 @@ def fork_blocks(pools: CachePools, block_tables, context_lens, ref_counts, paren
     if n > rows:
         raise ValueError("more forks than rows")
     if workspace is None:
-        workspace = _scratch(lib().pa_blocks_workspace_size(rows, pools.num_blocks), dev, stream)
+        workspace = _scratch(_size("pa_blocks_workspace_size", dev.index, rows, pools.num_blocks), dev, stream)
     else:
         _cuda(workspace, "workspace", workspace.dtype, dev)
     _call("pa_fork_blocks", dev, stream, *pools._args, block_tables.data_ptr(), width,
@@ -510,8 +548,10 @@ def free_blocks(block_tables, context_lens, ref_counts, rows, block_size: int, s
     """The listed rows (int32 [n]; -1 is skipped) give up their blocks: counts
     go down by one per entry, entries and lengths become 0."""
     dev = block_tables.device
-    _check_tables(block_tables, context_lens, ref_counts, dev)
-    _cuda(rows, "rows", torch.int32, dev)
+    if not _fits(dev.index, torch.int32, block_tables, context_lens, ref_counts, rows):
+        _explain(dev, torch.int32, block_tables=block_tables, context_lens=context_lens,
+                 ref_counts=ref_counts, rows=rows)
+    _check_table_shapes(block_tables, context_lens, ref_counts)
     if rows.dim() != 1:
         raise ValueError("rows must be [n]")
     _call("pa_free_blocks", dev, stream, block_tables.data_ptr(), block_tables.shape[1],
@@ -525,7 +565,9 @@ def compact_blocks(pools: CachePools, block_tables, context_lens, ref_counts, re
     block_tables and ref_counts follow. Returns (remap, num_live): int32 [NB],
     the new id of every live block and 0 for the others, and int32 [1], n."""
     dev = pools.device
-    _check_tables(block_tables, context_lens, ref_counts, dev)
+    if not _fits(dev.index, torch.int32, block_tables, context_lens, ref_counts):
+        _explain(dev, torch.int32, block_tables=block_tables, context_lens=context_lens, ref_counts=ref_counts)
+    _check_table_shapes(block_tables, context_lens, ref_counts)
     NB, (rows, width) = pools.num_blocks, block_tables.shape
     if ref_counts.shape[0] != NB:
         raise ValueError("ref_counts must have one entry per block")
@@ -541,7 +583,7 @@ def compact_blocks(pools: CachePools, block_tables, context_lens, ref_counts, re
                 raise ValueError(f"{n} must be [{size}]")
         outs.append(t)
     if workspace is None:
-        workspace = _scratch(lib().pa_blocks_workspace_size(rows, NB), dev, stream)
+        workspace = _scratch(_size("pa_blocks_workspace_size", dev.index, rows, NB), dev, stream)
     else:
         _cuda(workspace, "workspace", workspace.dtype, dev)
     _call("pa_compact_blocks", dev, stream, *pools._args, block_tables.data_ptr(), width,

@@ -187,6 +187,13 @@ def test_long_prefix_for_few_and_many():
     Batch([50, 2], [400, 900], [9, 130], 32, 4).check()
 
 
+@pytest.mark.parametrize("n,blocks", [(128, 1000), (20, 700), (20, 701), (20, 3000), (9, 2999)])
+def test_many_key_tiles_per_share(n, blocks):
+    # every ring and barrier of the prefix kernel goes round many times
+    for _ in range(3):
+        Batch([n], [blocks], [3, 40], 16, 1).check()
+
+
 def test_long_own_part():
     Batch([4], [2], [5000, 20], 8, 4).check()
 
