@@ -528,6 +528,7 @@ pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_c
     sh.num_groups = num_groups;
     sh.group_pad = gp;
     sh.max_workers = sms;
+    sh.box_tokens = block_size < 128 ? block_size : 128;
     // Two packed units read a prefix twice at most: never dearer than the prefix
     // kernel, which is then not launched. Nor is it where its tiles could not be
     // counted in 32 bits, or for a scale that is not positive, which it does not

@@ -145,8 +145,11 @@ __device__ __forceinline__ SharedUnit load_unit(const SharedArgs &sh, int v) {
     return SharedUnit{x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};
 }
 
-__device__ __forceinline__ void cursor_advance(SharedCursor &c, const DecodeArgs &a,
-                                               const SharedArgs &sh, int entries) {
+// Returns the places of the flat tile space it passes besides the tile's own: a
+// unit's tiles are followed by kUnitTiles places without one, for the work a
+// unit costs whatever its length.
+__device__ __forceinline__ int cursor_advance(SharedCursor &c, const DecodeArgs &a,
+                                              const SharedArgs &sh, int entries) {
     if (++c.j == c.nt) {
         c.j = 0;
         if (++c.kvh == a.num_kv_heads) {
@@ -156,7 +159,9 @@ __device__ __forceinline__ void cursor_advance(SharedCursor &c, const DecodeArgs
                 c.nt = unit_tiles(c.u.len - c.u.start);
             }
         }
+        return kUnitTiles;
     }
+    return 0;
 }
 
 __device__ __forceinline__ void cursor_advance(Cursor &c, const DecodeArgs &a, int max_len) {
@@ -703,12 +708,17 @@ __device__ __forceinline__ void plan_shared(const DecodeArgs &a, const SharedArg
                 if (stage[mid] * Hkv > T0) hi = mid; else lo = mid + 1;
             }
             const long long excl = lo == 0 ? before : stage[lo - 1];
-            const long long nt = stage[lo] - excl, rem = T0 - excl * Hkv;
+            const long long places = stage[lo] - excl, rem = T0 - excl * Hkv;
             c.v = c0 + lo;
-            c.nt = (int)nt;
-            c.kvh = (int)(rem / nt);
-            c.j = (int)(rem - c.kvh * nt);
             c.u = load_unit(sh, c.v);
+            c.nt = (int)places - kUnitTiles;
+            c.kvh = (int)(rem / places);
+            c.j = (int)(rem - c.kvh * places);
+            if (c.j >= c.nt) {          // past the unit's tiles: the next unit begins here
+                T0 += places - c.j;
+                c.j = c.nt - 1;
+                cursor_advance(c, a, sh, entries);
+            }
             found = true;
         }
         before = end;
@@ -806,9 +816,13 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
         if (SHARED) asm volatile("griddepcontrol.wait;\n" ::: "memory");
         return;
     }
-    auto advance = [&](auto &c) {
-        if constexpr (SHARED) cursor_advance(c, a, sh, entries);
-        else cursor_advance(c, a, max_len);
+    auto advance = [&](auto &c) -> int {
+        if constexpr (SHARED) {
+            return cursor_advance(c, a, sh, entries);
+        } else {
+            cursor_advance(c, a, max_len);
+            return 0;
+        }
     };
 
     uint32_t *outg = static_cast<uint32_t *>(a.out);
@@ -826,7 +840,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
             issue_tile(pc, p_bid, ring + stage_p * kStageBytes, bar0 + 8 * stage_p, a, &tmap_k,
                        &tmap_v, lane);
             pending |= 1u << stage_p;
-            advance(pc);
+            Tp += advance(pc);
             ++Tp;
             p_bid = Tp < T1 ? tile_block(pc, a) : 0;
         }
@@ -847,7 +861,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
             issue_tile(pc, p_bid, ring + stage_p * kStageBytes, bar0 + 8 * stage_p, a, &tmap_k,
                        &tmap_v, lane);
             pending |= 1u << stage_p;
-            advance(pc);
+            Tp += advance(pc);
             ++Tp;
             p_bid = Tp < T1 ? tile_block(pc, a) : 0;
         }
@@ -941,7 +955,7 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
             ++piece;
             fresh = true;
         }
-        advance(cc);
+        T += advance(cc);
     }
     if (failed) {
         // a copy did not land in time: record it, give the copies still in
@@ -1044,27 +1058,6 @@ struct Merge {
     }
 };
 
-// Parts [0, n) of one output row, `at(i)` giving part i's places in `o` and
-// `ml`; a batch's loads are all in flight before its merge.
-template <class At>
-__device__ __forceinline__ void merge_parts(Merge &acc, int n, const float4 *o, const float2 *ml, At at) {
-    constexpr int kBatch = 4;
-    for (int i0 = 0; i0 < n; i0 += kBatch) {
-        float2 e[kBatch];
-        float4 p[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (i0 + k < n) {
-                const longlong2 x = at(i0 + k);
-                p[k] = o[x.x];
-                e[k] = ml[x.y];
-            }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (i0 + k < n) acc.add(e[k], p[k]);
-    }
-}
-
 // With shared prefixes: the parts of an output row's prefix, then its own. The
 // prefix is left either by decode_shared_kernel, like the own part (a row of
 // whole_o, or a column of a slot per share), or by shared.cu (a row of unit_o,
@@ -1077,7 +1070,7 @@ __device__ __forceinline__ void merge_parts(Merge &acc, int n, const float4 *o, 
 // of a group, padded; COLS: columns of a slot.
 template <int GP, int COLS>
 __global__ void __launch_bounds__(256, 4) combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
-    constexpr int kPairSeqs = kPairRows / GP;
+    constexpr int kPairSeqs = kPairRows / GP, kBatch = 5;
     struct Row {
         int parts, row;                 // of shared.cu: 0 none, 1 whole in unit_o, else pieces
         int64_t slot0, w0;
@@ -1115,38 +1108,53 @@ __global__ void __launch_bounds__(256, 4) combine_shared_kernel(const DecodeArgs
     __syncthreads();
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (!mine) return;
-    // Everything whose place is known goes out at once: the unit's record, its
-    // row if one share computed it whole (else unused), the first parts of the
-    // prefix.
-    const int4 u = sh.units[(int64_t)(s - s_lo) * Hkv + kvh];
     const Row r = s_row[threadIdx.x & 7];
-    const int64_t out_row = col_row(a, s, kvh, h) / kHeadDim;
-    const float2 own_ml = sh.whole_ml[out_row];
-    const float4 own_o = sh.whole_o[out_row * 32 + word];
-    Merge acc;
-    auto add_slots = [&](const int4 x, int col) {
-        merge_parts(acc, 1 + x.y - x.z, reinterpret_cast<const float4 *>(a.part_o),
-                    reinterpret_cast<const float2 *>(a.part_ml), [&](int i) {
-            const int64_t slot = i == 0 ? x.x : 2 * (int64_t)(x.z + i);
-            return make_longlong2((slot * COLS + col) * 32 + word, slot * COLS + col);
-        });
-    };
-    if (r.packed >= 0) {
-        const int4 x = sh.units[(int64_t)r.packed * Hkv + kvh];
-        const int64_t whole = (int64_t)a.num_seqs * a.num_q_heads + out_row;
-        if (x.x == -1) acc.add(sh.whole_ml[whole], sh.whole_o[whole * 32 + word]);
-        else add_slots(x, r.col);
-    }
-    if (r.parts == 1)
-        acc.add(sh.unit_ml[kvh * rows + row], sh.unit_o[((int64_t)kvh * 32 + word) * rows + row]);
-    else if (r.parts > 1)
-        merge_parts(acc, r.parts, sh.part_o, sh.part_ml, [&](int i) {
-            const int64_t slot = i == 0 ? r.slot0 : 2 * (r.w0 + i);
-            return make_longlong2((slot * 32 + word) * kPairRows + r.row, slot * kPairRows + r.row);
-        });
+    const int4 u = sh.units[(int64_t)(s - s_lo) * Hkv + kvh];
+    const int4 x = r.packed >= 0 ? sh.units[(int64_t)r.packed * Hkv + kvh] : make_int4(0, -1, 0, 0);
     if (u.x == -2) return;              // written by the share that computed it
-    if (u.x == -1) acc.add(own_ml, own_o);
-    else add_slots(u, h);
+    const int64_t out_row = col_row(a, s, kvh, h) / kHeadDim;
+    const int64_t whole_rows = (int64_t)a.num_seqs * a.num_q_heads;
+    // the parts in the order of their keys; a batch's loads are all in flight
+    // before its merge
+    const int n_packed = 1 + x.y - x.z, n_prefix = n_packed + r.parts, n = n_prefix + 1 + u.y - u.z;
+    const float4 *slots = reinterpret_cast<const float4 *>(a.part_o);
+    const float2 *slots_ml = reinterpret_cast<const float2 *>(a.part_ml);
+    Merge acc;
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+        float4 p[kBatch];
+        float2 e[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + k;
+            if (i >= n) break;
+            if (i >= n_packed && i < n_prefix) {
+                if (r.parts == 1) {
+                    p[k] = sh.unit_o[((int64_t)kvh * 32 + word) * rows + row];
+                    e[k] = sh.unit_ml[kvh * rows + row];
+                } else {
+                    const int64_t slot = i == n_packed ? r.slot0 : 2 * (r.w0 + i - n_packed);
+                    p[k] = sh.part_o[(slot * 32 + word) * kPairRows + r.row];
+                    e[k] = sh.part_ml[slot * kPairRows + r.row];
+                }
+            } else {
+                const bool own = i >= n_prefix;
+                const int first = own ? u.x : x.x, at = own ? i - n_prefix : i;
+                if (first == -1) {
+                    const int64_t whole = (own ? 0 : whole_rows) + out_row;
+                    p[k] = sh.whole_o[whole * 32 + word];
+                    e[k] = sh.whole_ml[whole];
+                } else {
+                    const int64_t slot = (at == 0 ? (int64_t)first : 2 * ((int64_t)(own ? u.z : x.z) + at)) * COLS +
+                                         (own ? h : r.col);
+                    p[k] = slots[slot * 32 + word];
+                    e[k] = slots_ml[slot];
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (i0 + k < n) acc.add(e[k], p[k]);
+    }
     const float inv = acc.l > 0.f ? 1.f / acc.l : 0.f;
     uint2 pk;
     pk.x = pack_bf16x2(acc.o.x * inv, acc.o.y * inv);

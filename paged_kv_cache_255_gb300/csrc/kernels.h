@@ -129,6 +129,11 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 bool make_pool_map(CUtensorMap *m, const void *pool, int64_t num_blocks, int block_size,
                    int num_kv_heads, bool head_major);
 
+// make_pool_map's map with boxes of box_tokens rows (a power of two that divides
+// block_size); block size and row count limits are the callers'.
+bool make_box_map(CUtensorMap *m, const void *pool, int64_t num_blocks, int block_size,
+                  int num_kv_heads, bool head_major, int box_tokens);
+
 // TMA tensor map over a K or V pool whose one box is a whole 16-token tile of
 // one KV head (both 64-dim halves, the same landing layout as two boxes of
 // make_pool_map's map). Coordinates: token-major (0, block * bs + offset, 0,

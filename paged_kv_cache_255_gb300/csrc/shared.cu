@@ -36,8 +36,9 @@
 // Inside the prefix kernel (TMEM: S_A 0-127, O_A 128-255, S_B 256-383, O_B
 // 384-511 columns; P_t in bf16 over the first 64 columns of S_t):
 //   warps 0-3, 4-7   softmax of tile A, B: thread t owns row t (TMEM lane t)
-//   warps 8, 9       K and V producers: 16 lanes fetch one box of 16 tokens x
-//                    64 dims each; the V warp also loads the queries
+//   warps 8, 9       K and V producers: a lane fetches one box of a block's
+//                    tokens (16 .. 128) x 64 dims; the V warp also loads the
+//                    queries
 //   warp 10          issues S = Q K^T and O += P V as their inputs arrive
 // Hand-offs are mbarriers; every wait is bounded (about 2 s), and a wait that
 // ran out makes every role skip to the end, where the CTA frees its TMEM.
@@ -65,7 +66,7 @@ constexpr int kKWarp = kSoftmaxThreads / 32;             // 8
 constexpr int kVWarp = kKWarp + 1;                       // 9
 constexpr int kMmaWarp = kKWarp + 2;                     // 10
 constexpr int kThreads = kSoftmaxThreads + 3 * 32;
-constexpr int kGroup = 16;                               // tokens per TMA box
+constexpr int kGroup = 16;                               // tokens of the smallest TMA box, and per MMA of P V
 constexpr int kGroups = kKeys / kGroup;                  // 8
 constexpr uint32_t kQBytes = kRows * kRowBytes;         // 32 KB: 2 halves of [128][128 B]
 constexpr uint32_t kQHalf = kRows * 128;
@@ -213,30 +214,26 @@ __device__ __forceinline__ Kind cheapest(int live, int n, int tokens, int group,
 // every SM one piece instead of two or more, and is taken when the longest
 // share is the shorter for it. (128 sequences x 64 heads, 2048 shared tokens and
 // 256 own: 152, 88, 64 and 40 SMs took 65, 50, 48 and 63 us.)
-__device__ __forceinline__ int prefix_sms(int sms, float tiles, float units, float own) {
+__device__ __forceinline__ int prefix_sms(int sm_count, float tiles, float units, float own) {
     constexpr float kTile = 2.3f, kPiece = 3.f, kRate = 75e3f, kRateAll = 6.4e6f;
-    const float bytes = own * (2.f * kTileBytes);
-    const float nt = tiles / units;
-    // the prefix needs a, the rest b SM microseconds; the rest is not faster
-    // than kRateAll, so more SMs than that takes need not be left to it
+    const float sms = (float)sm_count, bytes = own * (2.f * kTileBytes);
     auto time = [&](float x, float pieces) {
-        return fmaxf(pieces * kPiece + ceilf(tiles / x) * kTile,
-                     x < (float)sms ? kPiece + bytes / fminf(((float)sms - x) * kRate, kRateAll) : 1e30f);
+        const float rate = fminf((sms - x) * kRate, kRateAll);
+        return fmaxf(pieces * kPiece + ceilf(__fdividef(tiles, x)) * kTile, kPiece + __fdividef(bytes, rate));
     };
-    const float a = tiles * (kTile + kPiece / nt), b = bytes / kRate + 1.f;
-    float best = fmaxf(1.f, fminf(floorf((float)sms * a / (a + b) + 0.5f), (float)sms - 1.f));
+    // the prefix needs a SM microseconds, the rest b
+    const float a = tiles * kTile + units * kPiece, b = bytes * (1.f / kRate) + 1.f;
+    float best = fmaxf(1.f, fminf(floorf(__fdividef(sms * a, a + b) + 0.5f), sms - 1.f));
     best = fminf(best, tiles);
-    float t = time(best, tiles / best <= 1.f ? 1.f : 2.f + tiles / (best * nt));
-    const float k = floorf(best / units);
+    float t = time(best, best >= tiles ? 1.f : 2.f + __fdividef(units, best));
+    const float k = floorf(__fdividef(best, units));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const float x = (k + (float)i) * units;
-        if (x >= 1.f && x < (float)sms && x <= tiles) {
-            const float u = time(x, 1.f);
-            if (u < t) {
-                t = u;
-                best = x;
-            }
+        const float u = x >= 1.f && x < sms && x <= tiles ? time(x, 1.f) : INFINITY;
+        if (u < t) {
+            t = u;
+            best = x;
         }
     }
     return (int)best;
@@ -374,9 +371,9 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
                                  : make_int4(at, -1, 0, 0);
             sh.entries[v] = SharedUnit{s, s, start, L, a.group, start > 0 ? 1 : 0, {0, 0}};
             // an empty unit owns one (empty) tile
-            n[0] = L > start ? (L - start + kTileTokens - 1) / kTileTokens : 1;
+            n[0] = (L > start ? (L - start + kTileTokens - 1) / kTileTokens : 1) + kUnitTiles;
         } else if (v < entries) {
-            n[0] = sh.entries[v].len / kTileTokens;
+            n[0] = sh.entries[v].len / kTileTokens + kUnitTiles;
         }
         block_scan(n, total, s_sums);
         if (v < entries) sh.scan[v] = own + n[0];
@@ -402,8 +399,9 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
     // before it)
     for (int w = tid; w < workers; w += kPlanThreads) {
         SharedWalk k{};
-        k.T = (int64_t)w * base / workers;
-        k.T1 = (int64_t)(w + 1) * base / workers;
+        const int q = base / workers, r = base - q * workers;      // floor(w base / workers) in 32 bits
+        k.T = w * q + w * r / workers;
+        k.T1 = (w + 1) * q + (w + 1) * r / workers;
         int lo = 0, hi = G;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -651,7 +649,8 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
         const bool is_v = warp == kVWarp;
         const int nst = is_v ? kVStages : kKStages;
         const int lane = tid & 31;
-        const int q = lane >> 1, h = lane & 1;
+        const int q = lane >> 1, h = lane & 1;      // this lane's box of a tile, and its half of the dims
+        const int box = sh.box_tokens, boxes = kKeys / box;
         const void *map = is_v ? static_cast<const void *>(&tmap_v) : static_cast<const void *>(&tmap_k);
         const uint32_t bar_full = bar(is_v ? kBarVFull : kBarKFull);
         const uint32_t bar_empty = bar(is_v ? kBarVEmpty : kBarKEmpty);
@@ -674,17 +673,18 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
                 warp_arrive(bar(kBarQFull));
             }
             // coordinates (dim 1, dim 2) of this lane's box of tile j; dim 1 (or
-            // 2) at -kGroup reads zeros, for a block id outside the pool; x =
-            // INT_MIN: no box
+            // 2) at -kKeys reads zeros, for a block id outside the pool; x =
+            // INT_MIN: no box. A box may reach past the prefix, but not past
+            // its block: those keys are masked, their V not multiplied.
             auto box_at = [&](int j) -> int2 {
-                if (lane >= 2 * kGroups || j >= w.j1 || q >= groups_used(w, j)) return make_int2(INT_MIN, 0);
-                const int t = j * kKeys + q * kGroup;
+                const int t = j * kKeys + q * box;
+                if (q >= boxes || j >= w.j1 || t >= w.gr.tokens) return make_int2(INT_MIN, 0);
                 const int lb = a.block_size_log2;
                 const int bid = __ldg(a.block_tables + (int64_t)w.gr.row * a.max_blocks_per_seq + (t >> lb));
                 const int off = t & ((1 << lb) - 1);
                 if (bid < 0 || (int64_t)bid >= a.num_blocks) {
                     set_error(kErrBadBlock);
-                    return a.head_major ? make_int2(-kGroup, 0) : make_int2(w.kvh, -kGroup);
+                    return a.head_major ? make_int2(-kKeys, 0) : make_int2(w.kvh, -kKeys);
                 }
                 if (!a.head_major) return make_int2(w.kvh, (bid << lb) + off);
                 return make_int2(off, bid * a.num_kv_heads + w.kvh);
@@ -692,17 +692,17 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
             int2 box_next = box_at(w.j0);
 #pragma unroll 1
             for (int j = w.j0; j < w.j1; ++j) {
-                const int2 box = box_next;
+                const int2 at = box_next;
                 box_next = box_at(j + 1);
                 const uint32_t gj = gt + (j - w.j0);
                 const int st = gj % nst;
                 if (!warp_wait(bar_empty + 8 * st, ((gj / nst) & 1) ^ 1, abort)) { ok = false; break; }
                 const uint32_t full = bar_full + 8 * st;
-                if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)groups_used(w, j) * 2 * kGroup * 128);
+                const int n = __popc(__ballot_sync(0xffffffffu, at.x != INT_MIN));
+                if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)(n * box * 128));
                 __syncwarp();
-                if (box.x != INT_MIN)
-                    tc::tma_load_3d(base + st * kKVBytes + h * kKVHalf + q * kGroup * 128, map, h * 64, box.x,
-                                    box.y, full);
+                if (at.x != INT_MIN)
+                    tc::tma_load_3d(base + st * kKVBytes + h * kKVHalf + q * box * 128, map, h * 64, at.x, at.y, full);
                 warp_arrive(full);
             }
             gt += w.j1 - w.j0;
@@ -857,8 +857,8 @@ cudaError_t launch_g(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t st)
     if (e != cudaSuccess) return e;
     const int bs = 1 << a.block_size_log2;
     CUtensorMap mk, mv, mq;
-    if (!make_pool_map(&mk, a.k_cache, a.num_blocks, bs, a.num_kv_heads, a.head_major != 0) ||
-        !make_pool_map(&mv, a.v_cache, a.num_blocks, bs, a.num_kv_heads, a.head_major != 0) ||
+    if (!make_box_map(&mk, a.k_cache, a.num_blocks, bs, a.num_kv_heads, a.head_major != 0, sh.box_tokens) ||
+        !make_box_map(&mv, a.v_cache, a.num_blocks, bs, a.num_kv_heads, a.head_major != 0, sh.box_tokens) ||
         !make_q_map(&mq, a.q, a.num_seqs, a.num_q_heads, G))
         return cudaErrorInvalidValue;
     DecodeArgs ac = a;

@@ -10,6 +10,10 @@ namespace pa {
 
 constexpr int kSharedMaxGroups = 4096;  // groups of one call (the plan keeps 20 bytes each in shared memory)
 constexpr int kSharedMinSeqs = 2;       // a prefix is computed apart for at least this many sequences
+// What a unit of decode_shared_kernel costs besides its tiles (its queries, its
+// result), in tiles. Without it the shares of many short units ended up to 9 us
+// after the others (60 sequences of 1 .. 500 own tokens).
+constexpr int kUnitTiles = 4;
 // Sequences whose heads fit the 8 columns of one unit of decode_shared_kernel.
 __host__ __device__ constexpr int shared_fit(int group) { return group <= 8 ? 8 / group : 1; }
 constexpr int kPairRows = 256;      // rows of a prefix unit: two query tiles of 128
@@ -35,7 +39,7 @@ struct alignas(16) SharedWalk {
 
 struct SharedHeader {
     int64_t tiles;          // prefix: key tiles of all active groups
-    int64_t own_tiles;      // what follows it: 16-token tiles of all units (decode.cu)
+    int64_t own_tiles;      // decode.cu: 16-token tiles of all units, and kUnitTiles for each
     int s_lo, s_hi;         // sequences the call covers
     int entries;            // of SharedArgs::entries
     int workers;            // CTAs the prefix tiles are shared among
@@ -60,12 +64,13 @@ struct SharedArgs {
     int num_groups;
     int group_pad;                  // G: query heads per KV head, rounded up to a power of two
     int max_workers;                // CTAs of the prefix kernel
+    int box_tokens;                 // tokens of a TMA box of the prefix kernel: min(block size, 128)
     int tensor;                     // whether the prefix kernel is launched
     // in the workspace
     SharedHeader *hdr;
     int4 *seq;                      // [S] {active group or -1, entry of its packed prefix or -1, column there}
     SharedUnit *entries;            // [2 S] own tokens of every covered sequence, then packed prefixes
-    long long *scan;                // [2 S] tiles of one KV head through an entry
+    long long *scan;                // [2 S] the same of one KV head, through an entry
     SharedGroup *groups;            // [num_groups] the active ones
     SharedWalk *walks;              // [max_workers] first piece of every share
     float4 *part_o;                 // [2 max_workers][32][256] pieces of units that several workers share

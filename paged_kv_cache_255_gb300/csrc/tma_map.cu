@@ -31,14 +31,20 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // 2^31 (checked by the callers).
 bool make_pool_map(CUtensorMap *m, const void *pool, int64_t num_blocks, int block_size,
                    int num_kv_heads, bool head_major) {
+    return make_box_map(m, pool, num_blocks, block_size, num_kv_heads, head_major, kTileTokens);
+}
+
+// The same with boxes of box_tokens rows (a power of two that divides the block).
+bool make_box_map(CUtensorMap *m, const void *pool, int64_t num_blocks, int block_size,
+                  int num_kv_heads, bool head_major, int box_tokens) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t d1 = head_major ? block_size : num_kv_heads;
     const cuuint64_t d2 = head_major ? num_blocks * num_kv_heads : num_blocks * block_size;
     const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, d1, d2};
     const cuuint64_t strides[2] = {(cuuint64_t)kRowBytes, d1 * kRowBytes};
-    const cuuint32_t box[3] = {64, head_major ? (cuuint32_t)kTileTokens : 1u,
-                               head_major ? 1u : (cuuint32_t)kTileTokens};
+    const cuuint32_t box[3] = {64, head_major ? (cuuint32_t)box_tokens : 1u,
+                               head_major ? 1u : (cuuint32_t)box_tokens};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(pool), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
