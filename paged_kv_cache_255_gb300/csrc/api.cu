@@ -520,7 +520,7 @@ pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_c
                                    context_lens, 1, scale, out, num_seqs, num_q_heads, num_kv_heads,
                                    block_size, num_blocks, layout);
     a.num_workers = P;
-    a.min_tiles = 1;
+    a.min_tiles = pa::kDefaultMinTiles;
     pa::decode_carve_workspace(a, workspace, shared_cols(gp));
     pa::SharedArgs sh{};
     sh.group_starts = group_starts;

@@ -65,6 +65,7 @@ constexpr int kBoxBytes = kTileBytes / 2;     // one half of a tile: 16 rows x 1
 constexpr int kStageBytes = 2 * kTileBytes;   // K tile then V tile
 constexpr int kRingBytes = kStages * kStageBytes;
 constexpr int kCombineBatch = 8;              // pieces a combine warp loads at once
+constexpr int kCombineThreads = 128;          // of a combine_shared_kernel CTA
 constexpr float kNegInf = -INFINITY;
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;   // bounded waits give up after 1 s
 
@@ -1041,19 +1042,23 @@ __global__ void __launch_bounds__(128) combine_kernel(const DecodeArgs a) {
     reinterpret_cast<uint2 *>(static_cast<uint32_t *>(a.out) + col_row(a, task.x, task.y, h) / 2)[lane] = pk;
 }
 
-// Running merge of parts in the order they come: (m, l, o) of a set of keys.
+// Running merge of parts in the order they come: (m, l, o) of a set of keys, o
+// in two words of 4 dims.
 struct Merge {
     float m = kNegInf, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    __device__ __forceinline__ void add(const float2 e, const float4 p) {
+    float4 o[2] = {};
+    __device__ __forceinline__ void add(const float2 e, const float4 (&p)[2]) {
         if (e.y == 0.f) return;             // no visible token in the part
         const float mn = fmaxf(m, e.x);
         const float al = ex2(m - mn), be = ex2(e.x - mn);
         l = l * al + e.y * be;
-        o.x = o.x * al + p.x * be;
-        o.y = o.y * al + p.y * be;
-        o.z = o.z * al + p.z * be;
-        o.w = o.w * al + p.w * be;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            o[k].x = o[k].x * al + p[k].x * be;
+            o[k].y = o[k].y * al + p[k].y * be;
+            o[k].z = o[k].z * al + p[k].z * be;
+            o[k].w = o[k].w * al + p[k].w * be;
+        }
         m = mn;
     }
 };
@@ -1062,22 +1067,24 @@ struct Merge {
 // prefix is left either by decode_shared_kernel, like the own part (a row of
 // whole_o, or a column of a slot per share), or by shared.cu (a row of unit_o,
 // or a row of part_o per CTA, both [dim / 4][row]). A CTA takes 8 rows
-// (sequence, head of the group) of one KV head, a thread 4 dims of a row: a
-// warp's 8 rows x 4 words are whole 128-byte lines of shared.cu's arrays, and
-// whole sectors of the others and of `out`. (One warp per row, each lane in a
-// line of its own, took 17 us instead of 5 for 8192 rows of 6 parts.) What does
-// not depend on the two kernels before is looked up while they run. GP: heads
-// of a group, padded; COLS: columns of a slot.
+// (sequence, head of the group) of one KV head, a thread two words of 4 dims of
+// a row: a warp's 8 rows x 4 words are whole 128-byte lines of shared.cu's
+// arrays, and whole sectors of the others and of `out`. (One warp per row, each
+// lane in a line of its own, took 17 us for 8192 rows of 6 parts; one word per
+// thread needed two waves of CTAs and 7 us.) What does not depend on the two
+// kernels before is looked up while they run. GP: heads of a group, padded;
+// COLS: columns of a slot.
 template <int GP, int COLS>
-__global__ void __launch_bounds__(256, 4) combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
-    constexpr int kPairSeqs = kPairRows / GP, kBatch = 5;
+__global__ void __launch_bounds__(kCombineThreads, 8)
+combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
+    constexpr int kPairSeqs = kPairRows / GP, kBatch = 3;
     struct Row {
         int parts, row;                 // of shared.cu: 0 none, 1 whole in unit_o, else pieces
         int64_t slot0, w0;
         int packed, col;                // entry and column of the prefix in decode_shared_kernel, or -1
     };
     __shared__ Row s_row[8];
-    const int word = threadIdx.x >> 3;                  // dims [4 word, 4 word + 4)
+    const int word = threadIdx.x >> 3;                  // dims [4 word, 4 word + 4), and 64 further on
     const int64_t rows = (int64_t)a.num_seqs * GP;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x & 7);
     const int kvh = blockIdx.y, Hkv = a.num_kv_heads;
@@ -1121,19 +1128,23 @@ __global__ void __launch_bounds__(256, 4) combine_shared_kernel(const DecodeArgs
     const float2 *slots_ml = reinterpret_cast<const float2 *>(a.part_ml);
     Merge acc;
     for (int i0 = 0; i0 < n; i0 += kBatch) {
-        float4 p[kBatch];
+        float4 p[kBatch][2];
         float2 e[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int i = i0 + k;
             if (i >= n) break;
+            const float4 *from;         // this thread's words: from[0], from[step]
+            int64_t step = 16;
             if (i >= n_packed && i < n_prefix) {
                 if (r.parts == 1) {
-                    p[k] = sh.unit_o[((int64_t)kvh * 32 + word) * rows + row];
+                    from = sh.unit_o + ((int64_t)kvh * 32 + word) * rows + row;
+                    step = 16 * rows;
                     e[k] = sh.unit_ml[kvh * rows + row];
                 } else {
                     const int64_t slot = i == n_packed ? r.slot0 : 2 * (r.w0 + i - n_packed);
-                    p[k] = sh.part_o[(slot * 32 + word) * kPairRows + r.row];
+                    from = sh.part_o + (slot * 32 + word) * kPairRows + r.row;
+                    step = 16 * kPairRows;
                     e[k] = sh.part_ml[slot * kPairRows + r.row];
                 }
             } else {
@@ -1141,25 +1152,30 @@ __global__ void __launch_bounds__(256, 4) combine_shared_kernel(const DecodeArgs
                 const int first = own ? u.x : x.x, at = own ? i - n_prefix : i;
                 if (first == -1) {
                     const int64_t whole = (own ? 0 : whole_rows) + out_row;
-                    p[k] = sh.whole_o[whole * 32 + word];
+                    from = sh.whole_o + whole * 32 + word;
                     e[k] = sh.whole_ml[whole];
                 } else {
                     const int64_t slot = (at == 0 ? (int64_t)first : 2 * ((int64_t)(own ? u.z : x.z) + at)) * COLS +
                                          (own ? h : r.col);
-                    p[k] = slots[slot * 32 + word];
+                    from = slots + slot * 32 + word;
                     e[k] = slots_ml[slot];
                 }
             }
+            p[k][0] = from[0];
+            p[k][1] = from[step];
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
             if (i0 + k < n) acc.add(e[k], p[k]);
     }
     const float inv = acc.l > 0.f ? 1.f / acc.l : 0.f;
-    uint2 pk;
-    pk.x = pack_bf16x2(acc.o.x * inv, acc.o.y * inv);
-    pk.y = pack_bf16x2(acc.o.z * inv, acc.o.w * inv);
-    reinterpret_cast<uint2 *>(static_cast<uint32_t *>(a.out) + out_row * (kHeadDim / 2))[word] = pk;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint2 pk;
+        pk.x = pack_bf16x2(acc.o[k].x * inv, acc.o[k].y * inv);
+        pk.y = pack_bf16x2(acc.o[k].z * inv, acc.o[k].w * inv);
+        reinterpret_cast<uint2 *>(static_cast<uint32_t *>(a.out) + out_row * (kHeadDim / 2))[word + 16 * k] = pk;
+    }
 }
 
 template <class Tile, int GP>
@@ -1243,7 +1259,7 @@ cudaError_t launch_own(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t s
         if (sh.group_pad == 4) combine = reinterpret_cast<const void *>(&combine_shared_kernel<4, 8>);
     }
     e = L::launch_pdl(combine, dim3((unsigned)(((int64_t)a.num_seqs * sh.group_pad + 7) / 8), a.num_kv_heads),
-                      256, 0, args, st);
+                      kCombineThreads, 0, args, st);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
