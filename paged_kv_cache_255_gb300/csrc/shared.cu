@@ -207,15 +207,17 @@ __device__ __forceinline__ Kind cheapest(int live, int n, int tokens, int group,
 
 // How many of the SMs compute the `tiles` prefix tiles of `units` units, while
 // the others work through `own` 16-token tiles. Measured: a prefix tile pair
-// takes 2.3 us on an SM beside the other reads, a piece of a unit (its queries,
-// first keys, last product and rows) 3 us more, and an SM reads 75 GB/s of K
-// and V, all together 6.4 TB/s. SMs go to both in the proportion of the work,
-// so that both end together. A count that is a multiple of the units gives
-// every SM one piece instead of two or more, and is taken when the longest
-// share is the shorter for it. (128 sequences x 64 heads, 2048 shared tokens and
-// 256 own: 152, 88, 64 and 40 SMs took 65, 50, 48 and 63 us.)
+// takes about 2 us on an SM beside the other reads, a piece of a unit (its
+// queries, first keys, last product and rows) 3 us more, and an SM reads about
+// 70 GB/s of K and V, all together 6.4 TB/s. SMs go to both in the proportion of
+// the work, so that both end together. A count that is a multiple of the units
+// gives every SM one piece instead of two or more, and lets the units of a KV
+// head read the same keys at the same time; it is taken where the estimate is
+// not a tenth worse. (SMs for the prefix and measured us: 128 sequences x 64
+// heads over 2048 shared and 256 own tokens, 32 units: 49 51.5, 64 44.8; 256 x
+// 32 over 32768 and 16 .. 1000: 96 165.7, 100 185.6, 106 169.9.)
 __device__ __forceinline__ int prefix_sms(int sm_count, float tiles, float units, float own) {
-    constexpr float kTile = 2.3f, kPiece = 3.f, kRate = 75e3f, kRateAll = 6.4e6f;
+    constexpr float kTile = 2.f, kPiece = 3.f, kRate = 70e3f, kRateAll = 6.4e6f;
     const float sms = (float)sm_count, bytes = own * (2.f * kTileBytes);
     auto time = [&](float x, float pieces) {
         const float rate = fminf((sms - x) * kRate, kRateAll);
@@ -225,7 +227,7 @@ __device__ __forceinline__ int prefix_sms(int sm_count, float tiles, float units
     const float a = tiles * kTile + units * kPiece, b = bytes * (1.f / kRate) + 1.f;
     float best = fmaxf(1.f, fminf(floorf(__fdividef(sms * a, a + b) + 0.5f), sms - 1.f));
     best = fminf(best, tiles);
-    float t = time(best, best >= tiles ? 1.f : 2.f + __fdividef(units, best));
+    float t = 1.1f * time(best, best >= tiles ? 1.f : 2.f + __fdividef(units, best));
     const float k = floorf(__fdividef(best, units));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
