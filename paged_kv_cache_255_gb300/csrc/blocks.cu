@@ -98,7 +98,7 @@ __device__ __forceinline__ void copy_part(const uint4 *s, uint4 *d, int c0, int 
 #pragma unroll
     for (int k = 0; k < kLaneChunks; ++k) {
         const int c = c0 + k * 32 + lane;
-        if (c < n) v[k] = __ldcs(s + c);
+        if (c < n) v[k] = __ldcg(s + c);     // forks of one parent read the same rows
     }
 #pragma unroll
     for (int k = 0; k < kLaneChunks; ++k) {

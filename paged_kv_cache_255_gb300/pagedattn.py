@@ -349,7 +349,7 @@ def decode_shared(q, k_cache, v_cache, block_tables, context_lens, group_starts,
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
     if workspace is None:
-        workspace = _scratch(decode_shared_workspace_size(S, G, Hq, Hkv, D, dev), dev, stream)
+        workspace = _scratch("shared", decode_shared_workspace_size(S, G, Hq, Hkv, D, dev), dev, stream)
     else:
         _cuda(workspace, "workspace", workspace.dtype, dev)
     _call("pa_decode_shared", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
@@ -478,12 +478,24 @@ def _call(fn, dev, stream, *args):
         raise PagedAttnError(fn, status)
 
 
-def _scratch(nbytes, dev, stream):
-    """Workspace of one call from torch's allocator: calls on several streams,
-    and graphs captured apart, never share it."""
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if stream is not None:
-        ws.record_stream(stream)
+_kept = threading.local()
+
+
+def _scratch(kind, nbytes, dev, stream):
+    """Workspace of one call. Calls of one kind from one thread on its current
+    stream run one after the other and share a buffer that is kept (an
+    allocation costs as much as the rest of a short call); a call on another
+    stream, and every captured call, gets one of its own from torch's allocator,
+    so that calls that may run at the same time never share."""
+    if stream is not None or torch._C._cuda_isCurrentStreamCapturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            ws.record_stream(stream)
+        return ws
+    key = (kind, dev.index, _raw_stream(dev.index))
+    ws = _kept.__dict__.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _kept.__dict__[key] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     return ws
 
 
@@ -535,7 +547,8 @@ def fork_blocks(pools: CachePools, block_tables, context_lens, ref_counts, paren
     if n > rows:
         raise ValueError("more forks than rows")
     if workspace is None:
-        workspace = _scratch(_size("pa_blocks_workspace_size", dev.index, rows, pools.num_blocks), dev, stream)
+        workspace = _scratch("blocks", _size("pa_blocks_workspace_size", dev.index, rows, pools.num_blocks), dev,
+                             stream)
     else:
         _cuda(workspace, "workspace", workspace.dtype, dev)
     _call("pa_fork_blocks", dev, stream, *pools._args, block_tables.data_ptr(), width,
@@ -571,26 +584,26 @@ def compact_blocks(pools: CachePools, block_tables, context_lens, ref_counts, re
     NB, (rows, width) = pools.num_blocks, block_tables.shape
     if ref_counts.shape[0] != NB:
         raise ValueError("ref_counts must have one entry per block")
-    outs = []
-    for t, n, size in ((remap, "remap", NB), (num_live, "num_live", 1)):
-        if t is None:
-            t = torch.empty(size, dtype=torch.int32, device=dev)
-            if stream is not None:
-                t.record_stream(stream)
-        else:
-            _cuda(t, n, torch.int32, dev)
-            if t.shape != (size,):
-                raise ValueError(f"{n} must be [{size}]")
-        outs.append(t)
+    if remap is None:
+        remap = torch.empty(NB, dtype=torch.int32, device=dev)
+    if num_live is None:
+        num_live = torch.empty(1, dtype=torch.int32, device=dev)
+    if not _fits(dev.index, torch.int32, remap, num_live):
+        _explain(dev, torch.int32, remap=remap, num_live=num_live)
+    if remap.shape[0] != NB or remap.dim() != 1 or num_live.numel() != 1:
+        raise ValueError("remap must be [num_blocks] and num_live [1]")
+    if stream is not None:
+        remap.record_stream(stream)
+        num_live.record_stream(stream)
     if workspace is None:
-        workspace = _scratch(_size("pa_blocks_workspace_size", dev.index, rows, NB), dev, stream)
+        workspace = _scratch("blocks", _size("pa_blocks_workspace_size", dev.index, rows, NB), dev, stream)
     else:
         _cuda(workspace, "workspace", workspace.dtype, dev)
     _call("pa_compact_blocks", dev, stream, *pools._args, block_tables.data_ptr(), width,
-          context_lens.data_ptr(), rows, ref_counts.data_ptr(), outs[0].data_ptr(),
-          outs[1].data_ptr(), *pools._shape, workspace.data_ptr(),
+          context_lens.data_ptr(), rows, ref_counts.data_ptr(), remap.data_ptr(),
+          num_live.data_ptr(), *pools._shape, workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
-    return outs[0], outs[1]
+    return remap, num_live
 
 
 def take_device_error(stream=None, device=None) -> int:

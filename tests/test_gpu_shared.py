@@ -268,6 +268,30 @@ def test_same_bits_again_and_on_other_streams():
         assert torch.equal(o, want)
 
 
+def test_several_threads_and_current_streams():
+    import threading
+    batches = [Batch([9, 30], [40, 21], [3, 90, 250], 32, 8), Batch([4, 20], [12, 33], [60, 5], 16, 4, hm=True)]
+    want = [b.check().clone() for b in batches]
+    bad = []
+
+    def work(i, stream):
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                for b, w in zip(batches, want):
+                    if not torch.equal(b.run(), w):
+                        bad.append(i)
+
+    main = torch.cuda.current_stream()
+    streams = [main, main, torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i, s)) for i, s in enumerate(streams)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not bad
+
+
 def test_two_graphs_and_changed_groups():
     b, c = Batch([9, 6], [12, 5], [3, 90]), Batch([4, 4, 4], [30, 1, 8], [64, 2], 32, 4, hm=True)
     b.check(), c.check()
