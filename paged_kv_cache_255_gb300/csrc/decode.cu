@@ -65,7 +65,10 @@ constexpr int kBoxBytes = kTileBytes / 2;     // one half of a tile: 16 rows x 1
 constexpr int kStageBytes = 2 * kTileBytes;   // K tile then V tile
 constexpr int kRingBytes = kStages * kStageBytes;
 constexpr int kCombineBatch = 8;              // pieces a combine warp loads at once
-constexpr int kCombineThreads = 128;          // of a combine_shared_kernel CTA
+// combine_shared_kernel: up to so many sets of 8 rows a set has four CTAs of 16
+// groups (two CTAs fit an SM: 4 x 76 is one wave), then one of 4, then one of 1.
+constexpr int kCombineFew = 76;
+constexpr int kCombineSome = 304;
 constexpr float kNegInf = -INFINITY;
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;   // bounded waits give up after 1 s
 
@@ -1073,18 +1076,24 @@ struct Merge {
 // lane in a line of its own, took 17 us for 8192 rows of 6 parts; one word per
 // thread needed two waves of CTAs and 7 us.) What does not depend on the two
 // kernels before is looked up while they run. GP: heads of a group, padded;
-// COLS: columns of a slot.
-template <int GP, int COLS>
-__global__ void __launch_bounds__(kCombineThreads, 8)
+// COLS: columns of a slot. With few rows every one has many parts (8 units over
+// all warps of the GPU have 228 each): GROUPS groups of threads take contiguous
+// runs of them, their results merged in order, and a CTA takes only 2 WORDS of a
+// row's 32 words (4 sequences over 16000 tokens: 115 us with one group, 50 with
+// 8, the SMs that read all parts of their rows being the bound).
+template <int GP, int COLS, int GROUPS, int WORDS>
+__global__ void __launch_bounds__(8 * WORDS * GROUPS, GROUPS == 1 ? 8 : 2)
 combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
-    constexpr int kPairSeqs = kPairRows / GP, kBatch = 3;
+    constexpr int kPairSeqs = kPairRows / GP, kBatch = 3, kThreads = 8 * WORDS;
     struct Row {
         int parts, row;                 // of shared.cu: 0 none, 1 whole in unit_o, else pieces
         int64_t slot0, w0;
         int packed, col;                // entry and column of the prefix in decode_shared_kernel, or -1
     };
     __shared__ Row s_row[8];
-    const int word = threadIdx.x >> 3;                  // dims [4 word, 4 word + 4), and 64 further on
+    __shared__ Merge s_merge[GROUPS == 1 ? 1 : GROUPS - 1][GROUPS == 1 ? 1 : kThreads];
+    const int group = threadIdx.x / kThreads, tid = threadIdx.x % kThreads;
+    const int word = blockIdx.z * WORDS + (tid >> 3);   // dims [4 word, 4 word + 4), and 64 further on
     const int64_t rows = (int64_t)a.num_seqs * GP;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x & 7);
     const int kvh = blockIdx.y, Hkv = a.num_kv_heads;
@@ -1114,20 +1123,25 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
     }
     __syncthreads();
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    if (!mine) return;
-    const Row r = s_row[threadIdx.x & 7];
-    const int4 u = sh.units[(int64_t)(s - s_lo) * Hkv + kvh];
-    const int4 x = r.packed >= 0 ? sh.units[(int64_t)r.packed * Hkv + kvh] : make_int4(0, -1, 0, 0);
-    if (u.x == -2) return;              // written by the share that computed it
+    Row r{0, 0, 0, 0, -1, 0};
+    int4 u = make_int4(-2, 0, 0, 0), x = make_int4(0, -1, 0, 0);
+    if (mine) {
+        r = s_row[threadIdx.x & 7];
+        u = sh.units[(int64_t)(s - s_lo) * Hkv + kvh];
+        if (r.packed >= 0) x = sh.units[(int64_t)r.packed * Hkv + kvh];
+    }
+    const bool todo = u.x != -2;        // else not covered, or written by the share that computed it
     const int64_t out_row = col_row(a, s, kvh, h) / kHeadDim;
     const int64_t whole_rows = (int64_t)a.num_seqs * a.num_q_heads;
     // the parts in the order of their keys; a batch's loads are all in flight
     // before its merge
-    const int n_packed = 1 + x.y - x.z, n_prefix = n_packed + r.parts, n = n_prefix + 1 + u.y - u.z;
+    const int n_packed = 1 + x.y - x.z, n_prefix = n_packed + r.parts;
+    const int parts = todo ? n_prefix + 1 + u.y - u.z : 0;
+    const int n = parts * (group + 1) / GROUPS;
     const float4 *slots = reinterpret_cast<const float4 *>(a.part_o);
     const float2 *slots_ml = reinterpret_cast<const float2 *>(a.part_ml);
     Merge acc;
-    for (int i0 = 0; i0 < n; i0 += kBatch) {
+    for (int i0 = parts * group / GROUPS; i0 < n; i0 += kBatch) {
         float4 p[kBatch][2];
         float2 e[kBatch];
 #pragma unroll
@@ -1168,6 +1182,16 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
         for (int k = 0; k < kBatch; ++k)
             if (i0 + k < n) acc.add(e[k], p[k]);
     }
+    if constexpr (GROUPS > 1) {
+        if (group > 0) s_merge[group - 1][tid] = acc;
+        __syncthreads();
+        if (group > 0) return;
+        for (int g = 0; g < GROUPS - 1; ++g) {
+            const Merge o = s_merge[g][tid];
+            acc.add(make_float2(o.m, o.l), o.o);
+        }
+    }
+    if (!todo) return;
     const float inv = acc.l > 0.f ? 1.f / acc.l : 0.f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -1235,6 +1259,27 @@ struct Launcher {
 // The own tokens of a call over shared prefixes, then its combine. Tiles have
 // 8 columns (16 for groups above 8) whatever the group size: the 8 of a matrix instruction,
 // filled by several sequences where they share a prefix.
+enum CombineShape { kFew, kSome, kMany };
+
+template <int GP, int COLS>
+const void *combine_of(CombineShape shape) {
+    switch (shape) {
+        case kFew: return reinterpret_cast<const void *>(&combine_shared_kernel<GP, COLS, 16, 4>);
+        case kSome: return reinterpret_cast<const void *>(&combine_shared_kernel<GP, COLS, 4, 16>);
+        default: return reinterpret_cast<const void *>(&combine_shared_kernel<GP, COLS, 1, 16>);
+    }
+}
+
+template <int COLS>
+const void *combine_for(int group_pad, CombineShape shape) {
+    if constexpr (COLS == 8) {
+        if (group_pad == 1) return combine_of<1, 8>(shape);
+        if (group_pad == 2) return combine_of<2, 8>(shape);
+        if (group_pad == 4) return combine_of<4, 8>(shape);
+    }
+    return combine_of<COLS, COLS>(shape);
+}
+
 template <int COLS>
 cudaError_t launch_own(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t st) {
     using L = Launcher<MmaTile<COLS>, COLS>;
@@ -1252,14 +1297,12 @@ cudaError_t launch_own(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t s
     e = L::launch_pdl(reinterpret_cast<const void *>(&decode_shared_kernel<COLS>),
                       dim3((a.num_workers + kWarps - 1) / kWarps), kWarps * 32, L::Lay::kCtaBytes, args, st);
     if (e != cudaSuccess) return e;
-    const void *combine = reinterpret_cast<const void *>(&combine_shared_kernel<COLS, COLS>);
-    if constexpr (COLS == 8) {
-        if (sh.group_pad == 1) combine = reinterpret_cast<const void *>(&combine_shared_kernel<1, 8>);
-        if (sh.group_pad == 2) combine = reinterpret_cast<const void *>(&combine_shared_kernel<2, 8>);
-        if (sh.group_pad == 4) combine = reinterpret_cast<const void *>(&combine_shared_kernel<4, 8>);
-    }
-    e = L::launch_pdl(combine, dim3((unsigned)(((int64_t)a.num_seqs * sh.group_pad + 7) / 8), a.num_kv_heads),
-                      kCombineThreads, 0, args, st);
+    // one wave of CTAs whatever the number of rows (64 registers a thread)
+    const int64_t rows8 = ((int64_t)a.num_seqs * sh.group_pad + 7) / 8, ctas = rows8 * a.num_kv_heads;
+    const CombineShape shape = ctas <= kCombineFew ? kFew : ctas <= kCombineSome ? kSome : kMany;
+    const unsigned threads = shape == kFew ? 512 : shape == kSome ? 512 : 128;
+    e = L::launch_pdl(combine_for<COLS>(sh.group_pad, shape),
+                      dim3((unsigned)rows8, a.num_kv_heads, shape == kFew ? 4 : 1), threads, 0, args, st);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
