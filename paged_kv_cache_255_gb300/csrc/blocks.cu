@@ -9,9 +9,9 @@
 // trip and can be captured in a graph.
 //
 // fork and compact run as two kernels:
-//   plan   one cluster of 8 CTAs. Each of its 256 warps owns a contiguous run
+//   plan   one cluster of 8 CTAs. Each of its warps owns a contiguous run
 //          of block ids (and of forks), counts what it looks for with ballots,
-//          and after one scan of the 256 counts over the cluster's shared
+//          and after one scan of the counts over the cluster's shared
 //          memory walks its run again with the rank of each hit. The lowest
 //          free ids come out in order, whatever the timing, with two reads of
 //          the counts and no atomics.
@@ -34,9 +34,11 @@ __device__ int g_blocks_error;       // first device-side error of a block opera
 namespace {
 
 constexpr int kPlanCtas = 8;                         // one cluster
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;        // per CTA
-constexpr int kPlanAllWarps = kPlanCtas * kPlanWarps;
+// Warps of a plan CTA: each issues the whole plan, so few for small pools
+// (32 warps: 2.4 us more over 128 blocks), many where reading the counts is most.
+constexpr int kPlanFewWarps = 8;
+constexpr int kPlanManyWarps = 32;
+constexpr int64_t kPlanFewBlocks = 16384;            // 256 counts per warp
 constexpr int kApplyThreads = 256;
 constexpr int kApplyCtasPerSm = 8;
 constexpr int kUnitChunks = 256;                     // 16-byte chunks of a 4 KB unit
@@ -57,20 +59,21 @@ struct Scan {
     int total;
 };
 
-// Exclusive scan of one count per warp over the cluster's 256 warps, in CTA
-// then warp order. `mine` holds the CTA's 32 counts; every thread of the
-// cluster must call it, and `mine` may be reused after the next cluster sync.
+// Exclusive scan of one count per warp over the cluster's warps, in CTA then
+// warp order. `mine` holds the CTA's counts; every thread of the cluster must
+// call it, and `mine` may be reused after the next cluster sync.
+template <int WARPS>
 __device__ __forceinline__ Scan cluster_scan(cg::cluster_group &cl, int *mine, int count) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) mine[warp] = count;
     cl.sync();
     Scan r{0, 0};
-    const int self = (int)cl.block_rank() * kPlanWarps + warp;
+    const int self = (int)cl.block_rank() * WARPS + warp;
 #pragma unroll
-    for (int c = 0; c < kPlanCtas; ++c) {
-        const int v = cl.map_shared_rank(mine, c)[lane];
+    for (int i = lane; i < kPlanCtas * WARPS; i += 32) {
+        const int v = cl.map_shared_rank(mine, i / WARPS)[i % WARPS];
         r.total += v;
-        r.before += c * kPlanWarps + lane < self ? v : 0;
+        r.before += i < self ? v : 0;
     }
 #pragma unroll
     for (int x = 16; x >= 1; x >>= 1) {
@@ -81,8 +84,10 @@ __device__ __forceinline__ Scan cluster_scan(cg::cluster_group &cl, int *mine, i
 }
 
 // This warp's run [lo, hi) of n items, a multiple of 32 long but for the last.
+template <int WARPS>
 __device__ __forceinline__ void warp_run(int64_t n, int self, int64_t &lo, int64_t &hi) {
-    const int64_t per = ((n + kPlanAllWarps - 1) / kPlanAllWarps + 31) & ~(int64_t)31;
+    constexpr int kAll = kPlanCtas * WARPS;
+    const int64_t per = ((n + kAll - 1) / kAll + 31) & ~(int64_t)31;
     lo = per * self;
     hi = lo + per < n ? lo + per : n;
     lo = lo < n ? lo : n;
@@ -192,18 +197,19 @@ free_blocks_kernel(int32_t *block_tables, int max_blocks, int32_t *context_lens,
 
 // What the plan decides for a fork: {parent row, tokens, rank of its new block
 // among the free ones or -1, 0}; parent row -1 when the fork is skipped.
-__global__ void __launch_bounds__(kPlanThreads, 1) __cluster_dims__(kPlanCtas, 1, 1)
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 1) __cluster_dims__(kPlanCtas, 1, 1)
 fork_plan_kernel(const ForkArgs a) {
-    __shared__ int s_need[kPlanWarps], s_free[kPlanWarps];
+    __shared__ int s_need[WARPS], s_free[WARPS];
     cg::cluster_group cl = cg::this_cluster();
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int self = (int)cl.block_rank() * kPlanWarps + warp;
+    const int self = (int)cl.block_rank() * WARPS + warp;
     const int64_t max_len = (int64_t)a.max_blocks << a.block_size_log2;
 
     int64_t f0, f1, b0, b1;
-    warp_run(a.num_forks, self, f0, f1);
-    warp_run(a.num_blocks, self, b0, b1);
+    warp_run<WARPS>(a.num_forks, self, f0, f1);
+    warp_run<WARPS>(a.num_blocks, self, b0, b1);
 
     // a child may be forked once: the first fork that lists it gets it
     auto listed = [&a](int64_t i) {
@@ -213,6 +219,7 @@ fork_plan_kernel(const ForkArgs a) {
     for (int64_t i = f0 + lane; i < f1; i += 32)
         if (listed(i)) a.claim[a.children[i]] = 0x7fffffff;
     int nfree = 0;
+#pragma unroll 4
     for (int64_t i = b0; i < b1; i += 32) {
         const int64_t b = i + lane;
         nfree += __popc(__ballot_sync(0xffffffffu, b > 0 && b < b1 && a.ref_counts[b] <= 0));
@@ -248,8 +255,8 @@ fork_plan_kernel(const ForkArgs a) {
         need += __popc(__ballot_sync(0xffffffffu, tail));
         if (tail) a.forks[i + lane].z = 0;      // marks the fork until its rank is known
     }
-    const Scan sn = cluster_scan(cl, s_need, need);
-    const Scan sf = cluster_scan(cl, s_free, nfree);
+    const Scan sn = cluster_scan<WARPS>(cl, s_need, need);
+    const Scan sf = cluster_scan<WARPS>(cl, s_free, nfree);
 
     int rank = sn.before;
     for (int64_t i = f0; i < f1; i += 32) {
@@ -340,23 +347,25 @@ fork_apply_kernel(const __grid_constant__ PoolSet pools, const ForkArgs a, int w
 // With n live blocks, the k-th lowest live id above n moves to the k-th lowest
 // free id up to n: the fewest moves that make the live ids 1 .. n, and no
 // block is both read and written.
-__global__ void __launch_bounds__(kPlanThreads, 1) __cluster_dims__(kPlanCtas, 1, 1)
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 1) __cluster_dims__(kPlanCtas, 1, 1)
 compact_plan_kernel(const CompactArgs a) {
-    __shared__ int s_live[kPlanWarps];
+    __shared__ int s_live[WARPS];
     __shared__ int s_low;               // live ids up to n, in the CTA that holds id n
     cg::cluster_group cl = cg::this_cluster();
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int self = (int)cl.block_rank() * kPlanWarps + warp;
+    const int self = (int)cl.block_rank() * WARPS + warp;
     int64_t b0, b1;
-    warp_run(a.num_blocks, self, b0, b1);
+    warp_run<WARPS>(a.num_blocks, self, b0, b1);
     if (threadIdx.x == 0) s_low = 0;
     int live = 0;
+#pragma unroll 4
     for (int64_t i = b0; i < b1; i += 32) {
         const int64_t b = i + lane;
         live += __popc(__ballot_sync(0xffffffffu, b > 0 && b < b1 && a.ref_counts[b] > 0));
     }
-    const Scan s = cluster_scan(cl, s_live, live);
+    const Scan s = cluster_scan<WARPS>(cl, s_live, live);
     const int n = s.total;
     if (n >= b0 && n < b1) {            // live ids up to n = live before this run, and in it up to n
         int low = s.before;
@@ -386,7 +395,7 @@ compact_plan_kernel(const CompactArgs a) {
         rank += __popc(m);
     }
     cl.sync();                          // the whole list is written; s_low has been read
-    for (int k = self * 32 + lane; k < n - low; k += kPlanAllWarps * 32) {
+    for (int k = self * 32 + lane; k < n - low; k += kPlanCtas * WARPS * 32) {
         const int2 mv = a.moves[k];
         a.remap[mv.x] = mv.y;
         a.ref_counts[mv.y] = a.ref_counts[mv.x];
@@ -501,7 +510,10 @@ cudaError_t launch_fork_blocks(void *const *caches, int num_caches, ForkArgs a, 
     a.claim = reinterpret_cast<int32_t *>(w);
     w += round16((size_t)a.num_rows * sizeof(int32_t));
     a.free_ids = reinterpret_cast<int32_t *>(w);
-    fork_plan_kernel<<<kPlanCtas, kPlanThreads, 0, stream>>>(a);
+    if (a.num_blocks <= kPlanFewBlocks)
+        fork_plan_kernel<kPlanFewWarps><<<kPlanCtas, kPlanFewWarps * 32, 0, stream>>>(a);
+    else
+        fork_plan_kernel<kPlanManyWarps><<<kPlanCtas, kPlanManyWarps * 32, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return for_pools(caches, num_caches, [&](PoolSet set, bool first) {
@@ -519,7 +531,10 @@ cudaError_t launch_compact_blocks(void *const *caches, int num_caches, CompactAr
     char *w = static_cast<char *>(workspace);
     a.num_moves = reinterpret_cast<int32_t *>(w);
     a.moves = reinterpret_cast<int2 *>(w + 16);
-    compact_plan_kernel<<<kPlanCtas, kPlanThreads, 0, stream>>>(a);
+    if (a.num_blocks <= kPlanFewBlocks)
+        compact_plan_kernel<kPlanFewWarps><<<kPlanCtas, kPlanFewWarps * 32, 0, stream>>>(a);
+    else
+        compact_plan_kernel<kPlanManyWarps><<<kPlanCtas, kPlanManyWarps * 32, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return for_pools(caches, num_caches, [&](PoolSet set, bool first) {

@@ -326,3 +326,11 @@ def test_binding_refusals():
                           workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     assert e.value.status == pa.PA_ERR_WORKSPACE
     s.check(set())
+
+
+def test_a_pool_past_the_small_plan():
+    # 20000 blocks: more counts than the plan with few warps takes
+    s, _ = drawn(70, 4, 300, 16, 20000, lens=[4000, 4799, 33, 4800], shared=3, spare=5, Hkv=1, pools=1)
+    s.fork([0, 1, 2, 3, 0], [4, 5, 6, 7, 8])
+    s.free([1, 3, 4])
+    s.compact()
