@@ -529,13 +529,13 @@ pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_c
     sh.group_pad = gp;
     sh.max_workers = sms;
     sh.box_tokens = block_size < 128 ? block_size : 128;
-    // Two packed units read a prefix twice at most: never dearer than the prefix
-    // kernel, which is then not launched. Nor is it where its tiles could not be
+    // Where one packed unit takes every sequence, it is never dearer than the
+    // prefix kernel, which is then not launched. Nor is it where its tiles could not be
     // counted in 32 bits, or for a scale that is not positive, which it does not
     // take (every sequence then reads its prefix by itself, or packed).
     const int64_t key_tiles = (((int64_t)max_blocks_per_seq << a.block_size_log2) + 127) / 128;
     const int64_t pairs = (int64_t)num_seqs * gp / pa::kPairRows + num_groups;
-    sh.tensor = (num_seqs + pa::shared_fit(a.group) - 1) / pa::shared_fit(a.group) > 2 &&
+    sh.tensor = (num_seqs + pa::shared_fit(a.group) - 1) / pa::shared_fit(a.group) > 1 &&
                 key_tiles <= INT32_MAX / num_kv_heads / pairs && a.scale_log2 > 0.f ? 1 : 0;
     pa::shared_carve_workspace(sh, static_cast<char *>(workspace) + dec, a);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -191,15 +191,17 @@ enum Kind { kAlone, kPacked, kTensor };
 
 // The cheapest, in SM time per KV head (us): 128 tokens take decode_shared_kernel
 // 0.8 us for up to 8 columns (90 GB/s of K and V on an SM, once they are in L2);
-// a key tile takes the prefix kernel 2.6 us for 256 rows, 1.6 when they fit one
-// query tile, and every unit 3 us more.
+// a key tile takes the prefix kernel 2 us for 256 rows, 1 when they fit one
+// query tile, and every unit 4 us more. (12 prefixes of 3200 .. 9600 tokens for
+// 5 sequences x 2 heads: 110 us packed, 79 on the prefix kernel; of 64 .. 768
+// tokens: 25.0 packed, 28.4.)
 __device__ __forceinline__ Kind cheapest(int live, int n, int tokens, int group, int group_pad,
                                          bool tensor_ok) {
     const int fit = shared_fit(group);
     const float len = (float)tokens * (1.f / kKeys);
     const float packed = 0.8f * len * (float)((n + fit - 1) / fit);
     const float pairs = (float)(((long long)n * group_pad + kPairRows - 1) / kPairRows);
-    const float tensor = pairs * (3.f + ceilf(len) * (n * group_pad <= kRows ? 1.6f : 2.6f));
+    const float tensor = pairs * (4.f + ceilf(len) * (n * group_pad <= kRows ? 1.f : 2.f));
     if (live < kSharedMinSeqs || tokens == 0) return kAlone;
     if (tensor_ok && tensor < packed) return kTensor;
     return fit > 1 ? kPacked : kAlone;
