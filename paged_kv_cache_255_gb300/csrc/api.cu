@@ -478,7 +478,9 @@ pa_status_t pa_decode_step(const void *k, const void *v, const int64_t *slot_map
 
 size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_heads,
                                        int num_kv_heads, int head_dim) {
-    if (num_seqs < 0 || num_groups < 0 || num_groups > pa::kSharedMaxGroups) return 0;
+    if (num_seqs < 0 || num_groups < 0 || num_groups > pa::kSharedMaxGroups || num_seqs > 65535 ||
+        num_kv_heads > 65535)
+        return 0;
     if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
         head_dim != pa::kHeadDimPublic)
         return 0;
@@ -504,7 +506,8 @@ pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_c
         q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, 1, scale, out, num_seqs,
         num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, layout, 0, &nothing_to_do);
     if (chk != PA_OK) return chk;
-    if (num_groups > pa::kSharedMaxGroups) return PA_ERR_UNSUPPORTED;
+    if (num_groups > pa::kSharedMaxGroups || num_seqs > 65535 || num_kv_heads > 65535)
+        return PA_ERR_UNSUPPORTED;
     if (nothing_to_do || num_groups == 0) return PA_OK;
     if (!group_starts || !prefix_blocks) return PA_ERR_INVALID_ARG;
     const int gp = pa::decode_group_pad(num_q_heads / num_kv_heads);
@@ -536,7 +539,7 @@ pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_c
     const int64_t key_tiles = (((int64_t)max_blocks_per_seq << a.block_size_log2) + 127) / 128;
     const int64_t pairs = (int64_t)num_seqs * gp / pa::kPairRows + num_groups;
     sh.tensor = (num_seqs + pa::shared_fit(a.group) - 1) / pa::shared_fit(a.group) > 1 &&
-                key_tiles <= INT32_MAX / num_kv_heads / pairs && a.scale_log2 > 0.f ? 1 : 0;
+                key_tiles <= INT32_MAX / num_kv_heads / pairs && a.scale_log2 > 0.f && sms > 1 ? 1 : 0;
     pa::shared_carve_workspace(sh, static_cast<char *>(workspace) + dec, a);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = pa::launch_shared_prefix(a, sh, st);

@@ -1130,7 +1130,13 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
         u = sh.units[(int64_t)(s - s_lo) * Hkv + kvh];
         if (r.packed >= 0) x = sh.units[(int64_t)r.packed * Hkv + kvh];
     }
-    const bool todo = u.x != -2;        // else not covered, or written by the share that computed it
+    // A record is not there when the share that owed it gave up waiting for its
+    // tiles (the launch's outputs are undefined then): never an address from one.
+    auto sane = [&](const int4 v) {
+        return v.x >= -2 && v.x < 2 * a.num_workers && v.z >= 0 && v.z <= v.y && v.y < a.num_workers;
+    };
+    // else not covered, or written by the share that computed it
+    const bool todo = u.x != -2 && sane(u) && (r.packed < 0 || sane(x));
     const int64_t out_row = col_row(a, s, kvh, h) / kHeadDim;
     const int64_t whole_rows = (int64_t)a.num_seqs * a.num_q_heads;
     // the parts in the order of their keys; a batch's loads are all in flight

@@ -194,6 +194,20 @@ def test_many_key_tiles_per_share(n, blocks):
         Batch([n], [blocks], [3, 40], 16, 1).check()
 
 
+# parts of a row spread over groups of threads and over CTAs: few rows with many
+# parts, some, and many rows; prefixes packed into one unit and on the prefix kernel
+@pytest.mark.parametrize("sizes,blocks,Hq,Hkv,own", [
+    ([4], 1000, 16, 8, [3, 90]), ([2], 2500, 2, 1, [1, 700]), ([3, 2], 700, 8, 2, [3000, 20]),
+    ([16, 16], 60, 64, 8, [200, 17]), ([20, 12], 60, 16, 8, [200, 17]), ([300], 30, 16, 2, [64, 3, 0]),
+])
+def test_parts_of_rows(sizes, blocks, Hq, Hkv, own):
+    Batch(sizes, [blocks] * len(sizes), own, Hq, Hkv).check()
+
+
+def test_a_group_larger_than_the_plan():
+    Batch([1500, 700], [3, 2], [5, 20, 0, 33], 1, 1).check()
+
+
 def test_long_own_part():
     Batch([4], [2], [5000, 20], 8, 4).check()
 

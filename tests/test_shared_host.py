@@ -26,6 +26,8 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     (dict(S=-1), pa.PA_ERR_INVALID_ARG),
     (dict(G=-1), pa.PA_ERR_INVALID_ARG),
     (dict(G=4097), pa.PA_ERR_UNSUPPORTED),
+    (dict(S=65536), pa.PA_ERR_UNSUPPORTED),
+    (dict(Hq=65536, Hkv=65536), pa.PA_ERR_UNSUPPORTED),
     (dict(q=None), pa.PA_ERR_INVALID_ARG),
     (dict(cl=None), pa.PA_ERR_INVALID_ARG),
     (dict(gs=None), pa.PA_ERR_INVALID_ARG),
@@ -51,7 +53,7 @@ def test_host_checks(pa_lib, over, want):
 
 def test_workspace_size_rejects(pa_lib):
     for args in ((-1, 1, 16, 8, 128), (4, -1, 16, 8, 128), (4, 4097, 16, 8, 128), (4, 1, 12, 8, 128),
-                 (4, 1, 16, 8, 64), (4, 1, 34, 2, 128)):
+                 (4, 1, 16, 8, 64), (4, 1, 34, 2, 128), (65536, 1, 16, 8, 128), (4, 1, 65536, 65536, 128)):
         assert pa_lib.pa_decode_shared_workspace_size(*args) == 0
 
 
