@@ -140,6 +140,10 @@ __device__ __forceinline__ int unit_len(const Cursor &c) { return c.L; }
 __device__ __forceinline__ int unit_len(const SharedCursor &c) { return c.u.len; }
 __device__ __forceinline__ int table_row(const Cursor &c) { return c.s; }
 __device__ __forceinline__ int table_row(const SharedCursor &c) { return c.u.row; }
+// Whether a tile is read once and may leave L2 first. Beside the prefix kernel
+// that keeps the prefixes and the parts for the combine there.
+__device__ __forceinline__ constexpr bool once(const Cursor &) { return false; }
+__device__ __forceinline__ bool once(const SharedCursor &c) { return !(c.u.part & 2); }
 __device__ __forceinline__ int unit_seq(const Cursor &c) { return c.s; }
 __device__ __forceinline__ int unit_seq(const SharedCursor &c) { return c.u.first; }
 
@@ -221,8 +225,14 @@ __device__ __forceinline__ void issue_tile(const C &c, int bid, uint8_t *stage, 
             const int outer = a.head_major ? bid * a.num_kv_heads + c.kvh : c.kvh;
             const uint32_t dst = smem_u32(stage);
             mbar_arrive_expect_tx(bar, kStageBytes);
-            tc::tma_load_4d(dst, mk, 0, row, 0, outer, bar);               // K tile
-            tc::tma_load_4d(dst + kTileBytes, mv, 0, row, 0, outer, bar);  // V tile
+            if (once(c)) {
+                const uint64_t policy = tc::evict_first_policy();
+                tc::tma_load_4d_once(dst, mk, 0, row, 0, outer, bar, policy);
+                tc::tma_load_4d_once(dst + kTileBytes, mv, 0, row, 0, outer, bar, policy);
+            } else {
+                tc::tma_load_4d(dst, mk, 0, row, 0, outer, bar);               // K tile
+                tc::tma_load_4d(dst + kTileBytes, mv, 0, row, 0, outer, bar);  // V tile
+            }
         }
     } else {
         uint4 *z = reinterpret_cast<uint4 *>(stage);
