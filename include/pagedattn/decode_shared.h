@@ -36,8 +36,9 @@ extern "C" {
  * Values of group_starts are clamped to [0, num_seqs] and prefixes to the
  * table's width; a group_starts that decreases gives unspecified results within
  * the buffers. Requirements: pa_decode's; num_groups at most 4096, num_seqs and
- * num_kv_heads at most 65535; pools in either layout; workspace of pa_decode_shared_workspace_size(num_seqs,
- * num_groups, ...) bytes, 16-byte aligned. Results do not depend on timing.
+ * num_kv_heads at most 65535; pools in either layout; a workspace of
+ * pa_decode_shared_workspace_size(num_seqs, num_groups, ...) bytes, 16-byte
+ * aligned. Results do not depend on timing.
  */
 PA_API size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int num_q_heads,
                                               int num_kv_heads, int head_dim);

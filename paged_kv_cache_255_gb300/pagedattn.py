@@ -341,9 +341,7 @@ def decode_shared(q, k_cache, v_cache, block_tables, context_lens, group_starts,
             or prefix_blocks.dim() != 1 or group_starts.shape != (G + 1,):
         raise ValueError("shape mismatch between q, caches, block_tables, context_lens and groups")
     if out is None:
-        out = torch.empty_like(q)
-        if stream is not None:
-            out.record_stream(stream)
+        out = _new(q.shape, q.dtype, dev, stream)
     else:
         _cuda(out, "out", torch.bfloat16, dev)
         if out.shape != q.shape:
@@ -478,6 +476,18 @@ def _call(fn, dev, stream, *args):
         raise PagedAttnError(fn, status)
 
 
+def _new(shape, dtype, dev, stream):
+    """An output or workspace of a call on ``stream`` (None: the current one).
+    For another stream it comes from that stream's memory: what the current
+    stream has freed may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))     # the caller may use it there, too
+    return t
+
+
 _kept = threading.local()
 
 
@@ -486,12 +496,9 @@ def _scratch(kind, nbytes, dev, stream):
     stream run one after the other and share a buffer that is kept (an
     allocation costs as much as the rest of a short call); a call on another
     stream, and every captured call, gets one of its own from torch's allocator,
-    so that calls that may run at the same time never share."""
+    so calls that may run at the same time never share."""
     if stream is not None or torch._C._cuda_isCurrentStreamCapturing():
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            ws.record_stream(stream)
-        return ws
+        return _new(nbytes, torch.uint8, dev, stream)
     key = (kind, dev.index, _raw_stream(dev.index))
     ws = _kept.__dict__.get(key)
     if ws is None or ws.numel() < nbytes:
@@ -539,9 +546,9 @@ def fork_blocks(pools: CachePools, block_tables, context_lens, ref_counts, paren
         _explain(dev, torch.int32, block_tables=block_tables, context_lens=context_lens,
                  ref_counts=ref_counts, parents=parents, children=children)
     _check_table_shapes(block_tables, context_lens, ref_counts)
-    n, (rows, width) = parents.shape[0], block_tables.shape
     if parents.dim() != 1 or children.shape != parents.shape:
         raise ValueError("parents and children must be [n]")
+    n, (rows, width) = parents.shape[0], block_tables.shape
     if ref_counts.shape[0] != pools.num_blocks:
         raise ValueError("ref_counts must have one entry per block")
     if n > rows:
@@ -585,16 +592,15 @@ def compact_blocks(pools: CachePools, block_tables, context_lens, ref_counts, re
     if ref_counts.shape[0] != NB:
         raise ValueError("ref_counts must have one entry per block")
     if remap is None:
-        remap = torch.empty(NB, dtype=torch.int32, device=dev)
+        remap = _new(NB, torch.int32, dev, stream)
+    elif not _fits(dev.index, torch.int32, remap) or remap.shape != (NB,):
+        _explain(dev, torch.int32, remap=remap)
+        raise ValueError("remap must be [num_blocks]")
     if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=dev)
-    if not _fits(dev.index, torch.int32, remap, num_live):
-        _explain(dev, torch.int32, remap=remap, num_live=num_live)
-    if remap.shape[0] != NB or remap.dim() != 1 or num_live.numel() != 1:
-        raise ValueError("remap must be [num_blocks] and num_live [1]")
-    if stream is not None:
-        remap.record_stream(stream)
-        num_live.record_stream(stream)
+        num_live = _new(1, torch.int32, dev, stream)
+    elif not _fits(dev.index, torch.int32, num_live) or num_live.shape != (1,):
+        _explain(dev, torch.int32, num_live=num_live)
+        raise ValueError("num_live must be [1]")
     if workspace is None:
         workspace = _scratch("blocks", _size("pa_blocks_workspace_size", dev.index, rows, NB), dev, stream)
     else:

@@ -298,6 +298,33 @@ def test_another_stream():
     s.check(ref.fork(s.pools, s.tables, s.lens, s.refs, [2], [5], 16))
 
 
+def test_outputs_for_another_stream_come_from_its_memory():
+    # a buffer that the current stream has freed may still be in use there
+    s, _ = drawn(63, 3, 6, 16, 80, lens=[90, 33, 64], spare=6)
+    side = torch.cuda.Stream()
+    n = s.d_refs.shape[0]
+    freed = [torch.empty(n, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")]
+    old = {f.data_ptr() for f in freed}
+    side.wait_stream(torch.cuda.current_stream())
+    del freed
+    remap, live = pa.compact_blocks(s.handle, s.d_tables, s.d_lens, s.d_refs, stream=side)
+    assert not {remap.data_ptr(), live.data_ptr()} & old
+    side.synchronize()
+    codes, want, k = ref.compact(s.pools, s.tables, s.lens, s.refs, s.bs)
+    assert np.array_equal(remap.cpu().numpy(), want) and live.item() == k
+    s.check(codes, pool_ids=np.r_[0:k + 1])
+
+
+@pytest.mark.parametrize("remap,num_live", [((79,), (1,)), ((80, 1), (1,)), ((80,), ()), ((80,), (2,))])
+def test_compact_refuses_outputs_of_another_shape(remap, num_live):
+    s, _ = drawn(64, 3, 6, 16, 80, lens=[90, 33, 64], spare=6)
+    with pytest.raises(ValueError):
+        pa.compact_blocks(s.handle, s.d_tables, s.d_lens, s.d_refs,
+                          remap=torch.empty(remap, dtype=torch.int32, device="cuda"),
+                          num_live=torch.empty(num_live, dtype=torch.int32, device="cuda"))
+    s.check(set())
+
+
 def test_binding_refusals():
     s, _ = drawn(62, 2, 3, 16, 20, spare=1)
     i = ints([0])
@@ -307,6 +334,8 @@ def test_binding_refusals():
         pa.CachePools([s.d_pools[0], s.d_pools[1][:5]])                 # two shapes
     with pytest.raises(ValueError):
         pa.copy_blocks(s.handle, i)
+    with pytest.raises(ValueError):
+        pa.fork_blocks(s.handle, s.d_tables, s.d_lens, s.d_refs, i[0], i[0])
     with pytest.raises(ValueError):
         pa.fork_blocks(s.handle, s.d_tables, s.d_lens, s.d_refs, i, ints([0, 1]))
     with pytest.raises(ValueError):

@@ -282,6 +282,22 @@ def test_same_bits_again_and_on_other_streams():
         assert torch.equal(o, want)
 
 
+def test_buffers_for_another_stream_come_from_its_memory():
+    # a buffer that the current stream has freed may still be in use there
+    b = Batch([9, 30], [40, 21], [3, 90, 250], 32, 8)
+    want = b.check()
+    side = torch.cuda.Stream()
+    ws_bytes = 3 << 20
+    freed = [torch.empty_like(want), torch.empty(ws_bytes, dtype=torch.uint8, device="cuda")]
+    old = {f.data_ptr() for f in freed}
+    side.wait_stream(torch.cuda.current_stream())
+    del freed
+    out, ws = b.run(stream=side), pa._scratch("shared", ws_bytes, want.device, side)
+    assert not {out.data_ptr(), ws.data_ptr()} & old
+    side.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_several_threads_and_current_streams():
     import threading
     batches = [Batch([9, 30], [40, 21], [3, 90, 250], 32, 8), Batch([4, 20], [12, 33], [60, 5], 16, 4, hm=True)]
