@@ -20,10 +20,10 @@
 // Block data moves in units of 4 KB (16 rows of 256 bytes: every block is a
 // multiple of that), one warp per unit with all eight 16-byte loads of a lane
 // in flight before its stores. Large calls are bound by HBM: 2047 blocks of
-// 32 KB copied in 8 pools take 148.6 us (7.2 TB/s read and written), a pool of
-// 4096 such blocks, half of them live, compacted in 89.5 us (6.0 TB/s); small
+// 32 KB copied in 8 pools take 147 us (7.3 TB/s read and written), a pool of
+// 4096 such blocks, half of them live, compacted in 89 us (6.0 TB/s); small
 // ones by their launches: two blocks copied in 2.2 us, a pool of 128 compacted
-// in 7.3 us.
+// in 6.7 us.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -163,8 +163,8 @@ copy_blocks_kernel(const __grid_constant__ PoolSet pools, const int2 *pairs, int
 //
 // Bound by its chain of dependent reads (row, length, entries, counts), and
 // with many rows by the atomics on counts of far-apart blocks: 4 rows of 64 ..
-// 1024 tokens take 3.5 us, 255 rows of 512 .. 16384 tokens (134800 entries of
-// 16) 12.2 us, both with the copy that restores the tables between passes.
+// 1024 tokens take 3.7 us, 255 rows of 512 .. 16384 tokens (134800 blocks of
+// 16) 11.3 us, both with the copy that restores the tables between passes.
 
 // One reference to block b less. False when there was none to give up: the
 // count is put back, so it ends at 0 however many such calls there were.
