@@ -688,7 +688,8 @@ __device__ __forceinline__ void plan_share(const DecodeArgs &a, int max_len, int
 
 // The same with shared prefixes: the plan kernel has left the scan of the
 // entries' tiles, the total and the share count; a CTA stages the scan in its
-// ring and each warp searches it.
+// ring and each warp searches it. (The entries staged with it, one read's latency
+// less on the way to the first tile, took 0.5 us longer in all.)
 __device__ __forceinline__ void plan_shared(const DecodeArgs &a, const SharedArgs &sh,
                                             long long *stage, int64_t &W, int &p_eff, int64_t &T0,
                                             int64_t &T1, int &entries, SharedCursor &c) {
@@ -924,15 +925,27 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
                                              (int)((unit_end_T * p_eff - 1) / W), w, 0);
                 }
             }
+            // with shared prefixes: the row of column h, counted up (the columns
+            // after a sequence's heads are the next sequence's)
+            int64_t row = (int64_t)unit_seq(cc) * a.num_q_heads + (int64_t)cc.kvh * a.group;
+            int head = 0;
+            auto next_row = [&]() {
+                ++row;
+                if (++head == a.group) {
+                    head = 0;
+                    row += a.num_q_heads - a.group;
+                }
+            };
             if (part && piece_j0 == 0 && unit_end) {
                 if constexpr (SHARED) {
                     const int64_t base = cc.u.part & 2 ? (int64_t)a.num_seqs * a.num_q_heads : 0;
 #pragma unroll
                     for (int h = 0; h < GP; ++h)
                         if (h < unit_cols(a, cc)) {
-                            const int64_t row = base + col_row(a, cc.u.first, cc.kvh, h) / kHeadDim;
-                            sh.whole_o[row * 32 + lane] = make_float4(oc[h][0], oc[h][1], oc[h][2], oc[h][3]);
-                            if (lane == 0) sh.whole_ml[row] = make_float2(sm_m[h], sm_l[h]);
+                            sh.whole_o[(base + row) * 32 + lane] =
+                                make_float4(oc[h][0], oc[h][1], oc[h][2], oc[h][3]);
+                            if (lane == 0) sh.whole_ml[base + row] = make_float2(sm_m[h], sm_l[h]);
+                            next_row();
                         }
                 }
             } else if (piece_j0 == 0 && unit_end) {
@@ -940,12 +953,14 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
 #pragma unroll
                 for (int h = 0; h < GP; ++h) {
                     if (h < unit_cols(a, cc)) {
+                        const int64_t at = SHARED ? row * kHeadDim : col_row(a, unit_seq(cc), cc.kvh, h);
                         const float l = sm_l[h];
                         const float inv = l > 0.f ? 1.f / l : 0.f;
                         uint2 pk;
                         pk.x = pack_bf16x2(oc[h][0] * inv, oc[h][1] * inv);
                         pk.y = pack_bf16x2(oc[h][2] * inv, oc[h][3] * inv);
-                        reinterpret_cast<uint2 *>(outg + col_row(a, unit_seq(cc), cc.kvh, h) / 2)[lane] = pk;
+                        reinterpret_cast<uint2 *>(outg + at / 2)[lane] = pk;
+                        if (SHARED) next_row();
                     }
                 }
             } else {
@@ -1077,6 +1092,11 @@ struct Merge {
     }
 };
 
+// n / d, in 32 bits where both fit.
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+    return ((n | d) >> 32) == 0 ? (int64_t)((uint32_t)n / (uint32_t)d) : n / d;
+}
+
 // With shared prefixes: the parts of an output row's prefix, then its own. The
 // prefix is left either by decode_shared_kernel, like the own part (a row of
 // whole_o, or a column of a slot per share), or by shared.cu (a row of unit_o,
@@ -1089,7 +1109,7 @@ struct Merge {
 // kernels before is looked up while they run. GP: heads of a group, padded;
 // COLS: columns of a slot. With few rows every one has many parts (8 units over
 // all warps of the GPU have 228 each): GROUPS groups of threads take contiguous
-// runs of them, their results merged in order, and a CTA takes only 2 WORDS of a
+// runs of them, their results merged pairwise, and a CTA takes only 2 WORDS of a
 // row's 32 words (4 sequences over 16000 tokens: 115 us with one group, 50 with
 // 8, the SMs that read all parts of their rows being the bound).
 template <int GP, int COLS, int GROUPS, int WORDS>
@@ -1097,8 +1117,9 @@ __global__ void __launch_bounds__(8 * WORDS * GROUPS, GROUPS == 1 ? 8 : 2)
 combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
     constexpr int kPairSeqs = kPairRows / GP, kBatch = 3, kThreads = 8 * WORDS;
     struct Row {
-        int parts, row;                 // of shared.cu: 0 none, 1 whole in unit_o, else pieces
-        int64_t slot0, w0;
+        int parts;                      // of shared.cu: 0 none, 1 whole in unit_o, else pieces
+        int slot;                       // of the first piece; the next ones are at even slots
+        int place;                      // row | 2 lanes << 8: the row in a piece, the slots between pieces
         int packed, col;                // entry and column of the prefix in decode_shared_kernel, or -1
     };
     __shared__ Row s_row[8];
@@ -1110,46 +1131,47 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
     const int kvh = blockIdx.y, Hkv = a.num_kv_heads;
     const int s = (int)(row / GP), h = (int)(row % GP);
     const int s_lo = __ldcg(&sh.hdr->s_lo);
+    auto out_row = [&]() { return (int64_t)s * a.num_q_heads + kvh * a.group + h; };
     const bool mine = row < rows && h < a.cols && s >= s_lo && s < __ldcg(&sh.hdr->s_hi);
+    if (threadIdx.x < 8 && !mine) s_row[threadIdx.x] = Row{0, 0, 0, -1, 0};
     if (threadIdx.x < 8 && mine) {
         const int4 q = __ldcg(sh.seq + s);
-        Row r{0, 0, 0, 0, q.y, q.z + h};
+        Row r{0, 0, 0, q.y, q.z + h};
         if (q.x >= 0) {
             const int64_t tiles = __ldcg(&sh.hdr->tiles);
-            const int workers = __ldcg(&sh.hdr->workers);
+            const int lanes = __ldcg(&sh.hdr->lanes), shares = __ldcg(&sh.hdr->workers) / lanes;
             const SharedGroup *g = sh.groups + q.x;
             const int tok = s - __ldcg(&g->s0), pair = tok / kPairSeqs, nt = __ldcg(&g->nt);
-            const int64_t U0 = __ldcg(&g->base) + ((int64_t)kvh * __ldcg(&g->pairs) + pair) * nt;
-            // share w of the tile space is [w tiles / workers, (w + 1) tiles / workers)
-            const int w0 = (int)(((U0 + 1) * workers - 1) / tiles);
-            const int w1 = (int)(((U0 + nt) * workers - 1) / tiles);
-            r.parts = 1 + w1 - w0;
-            r.row = (tok - pair * kPairSeqs) * GP + h;
-            // share w's slot 2 w holds its first piece, 2 w + 1 its last; only
-            // share w0 may have begun before the unit
-            r.slot0 = 2 * (int64_t)w0 + ((int64_t)w0 * tiles / workers < U0 ? 1 : 0);
-            r.w0 = w0;
+            const int lane = pair % lanes;
+            const int64_t U0 = quotient(__ldcg(&g->base), lanes) +
+                               ((int64_t)kvh * (__ldcg(&g->pairs) / lanes) + pair / lanes) * nt;
+            // share i of a lane is [i tiles / shares, (i + 1) tiles / shares), worker i lanes + lane
+            const int i0 = (int)quotient((U0 + 1) * shares - 1, tiles);
+            const int i1 = (int)quotient((U0 + nt) * shares - 1, tiles);
+            r.parts = 1 + i1 - i0;
+            // worker w's slot 2 w holds its first piece, 2 w + 1 its last; only
+            // the first share may have begun before the unit
+            r.slot = 2 * (i0 * lanes + lane) + (quotient(i0 * tiles, shares) < U0 ? 1 : 0);
+            r.place = (tok - pair * kPairSeqs) * GP + h + (2 * lanes << 8);
         }
         s_row[threadIdx.x] = r;
     }
     __syncthreads();
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    Row r{0, 0, 0, 0, -1, 0};
+    const Row r = s_row[threadIdx.x & 7];
     int4 u = make_int4(-2, 0, 0, 0), x = make_int4(0, -1, 0, 0);
     if (mine) {
-        r = s_row[threadIdx.x & 7];
         u = sh.units[(int64_t)(s - s_lo) * Hkv + kvh];
         if (r.packed >= 0) x = sh.units[(int64_t)r.packed * Hkv + kvh];
     }
     // A record is not there when the share that owed it gave up waiting for its
     // tiles (the launch's outputs are undefined then): never an address from one.
     auto sane = [&](const int4 v) {
-        return v.x >= -2 && v.x < 2 * a.num_workers && v.z >= 0 && v.z <= v.y && v.y < a.num_workers;
+        return v.x >= -2 && v.x < 2 * a.num_workers && v.z >= 0 && v.z <= v.y && v.y < a.num_workers &&
+               (v.x < 0 || v.x >> 1 == v.z);
     };
     // else not covered, or written by the share that computed it
     const bool todo = u.x != -2 && sane(u) && (r.packed < 0 || sane(x));
-    const int64_t out_row = col_row(a, s, kvh, h) / kHeadDim;
-    const int64_t whole_rows = (int64_t)a.num_seqs * a.num_q_heads;
     // the parts in the order of their keys; a batch's loads are all in flight
     // before its merge
     const int n_packed = 1 + x.y - x.z, n_prefix = n_packed + r.parts;
@@ -1167,27 +1189,31 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
             if (i >= n) break;
             const float4 *from;         // this thread's words: from[0], from[step]
             int64_t step = 16;
+            // a share's first piece is where its record says, the next shares' at
+            // their even slots
+            auto slot_of = [](int first, int at, int apart) {
+                return (int64_t)(at == 0 ? first : (first & ~1) + at * apart);
+            };
             if (i >= n_packed && i < n_prefix) {
                 if (r.parts == 1) {
                     from = sh.unit_o + ((int64_t)kvh * 32 + word) * rows + row;
                     step = 16 * rows;
                     e[k] = sh.unit_ml[kvh * rows + row];
                 } else {
-                    const int64_t slot = i == n_packed ? r.slot0 : 2 * (r.w0 + i - n_packed);
-                    from = sh.part_o + (slot * 32 + word) * kPairRows + r.row;
+                    const int64_t slot = slot_of(r.slot, i - n_packed, r.place >> 8);
+                    from = sh.part_o + (slot * 32 + word) * kPairRows + (r.place & 255);
                     step = 16 * kPairRows;
-                    e[k] = sh.part_ml[slot * kPairRows + r.row];
+                    e[k] = sh.part_ml[slot * kPairRows + (r.place & 255)];
                 }
             } else {
                 const bool own = i >= n_prefix;
-                const int first = own ? u.x : x.x, at = own ? i - n_prefix : i;
+                const int first = own ? u.x : x.x;
                 if (first == -1) {
-                    const int64_t whole = (own ? 0 : whole_rows) + out_row;
+                    const int64_t whole = out_row() + (own ? 0 : (int64_t)a.num_seqs * a.num_q_heads);
                     from = sh.whole_o + whole * 32 + word;
                     e[k] = sh.whole_ml[whole];
                 } else {
-                    const int64_t slot = (at == 0 ? (int64_t)first : 2 * ((int64_t)(own ? u.z : x.z) + at)) * COLS +
-                                         (own ? h : r.col);
+                    const int64_t slot = slot_of(first, own ? i - n_prefix : i, 2) * COLS + (own ? h : r.col);
                     from = slots + slot * 32 + word;
                     e[k] = slots_ml[slot];
                 }
@@ -1200,13 +1226,17 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
             if (i0 + k < n) acc.add(e[k], p[k]);
     }
     if constexpr (GROUPS > 1) {
-        if (group > 0) s_merge[group - 1][tid] = acc;
-        __syncthreads();
-        if (group > 0) return;
-        for (int g = 0; g < GROUPS - 1; ++g) {
-            const Merge o = s_merge[g][tid];
-            acc.add(make_float2(o.m, o.l), o.o);
+        // groups [n, 2 n) hand theirs to groups [0, n)
+#pragma unroll
+        for (int n = GROUPS / 2; n >= 1; n >>= 1) {
+            if (group >= n && group < 2 * n) s_merge[group - 1][tid] = acc;
+            __syncthreads();
+            if (group < n) {
+                const Merge o = s_merge[n - 1 + group][tid];
+                acc.add(make_float2(o.m, o.l), o.o);
+            }
         }
+        if (group > 0) return;
     }
     if (!todo) return;
     const float inv = acc.l > 0.f ? 1.f / acc.l : 0.f;
@@ -1215,7 +1245,7 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
         uint2 pk;
         pk.x = pack_bf16x2(acc.o[k].x * inv, acc.o[k].y * inv);
         pk.y = pack_bf16x2(acc.o[k].z * inv, acc.o[k].w * inv);
-        reinterpret_cast<uint2 *>(static_cast<uint32_t *>(a.out) + out_row * (kHeadDim / 2))[word + 16 * k] = pk;
+        reinterpret_cast<uint2 *>(static_cast<uint32_t *>(a.out) + out_row() * (kHeadDim / 2))[word + 16 * k] = pk;
     }
 }
 

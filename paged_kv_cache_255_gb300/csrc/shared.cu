@@ -21,8 +21,10 @@
 //                  128 / G sequences x G heads, G = g rounded up to a power of
 //                  two) of one (group, KV head); its keys go in tiles of 128.
 //                  The P CTAs take equal contiguous shares of the flat space of
-//                  all units' key tiles, so any mix of groups fills the GPU. A
-//                  unit that one CTA computes whole leaves its rows in unit_o,
+//                  all units' key tiles, so any mix of groups fills the GPU;
+//                  where every group has n pairs of tiles, n lanes of P / n
+//                  CTAs each, so that the pairs of a KV head read the same
+//                  keys at the same time. A unit that one CTA computes whole leaves its rows in unit_o,
 //                  one that several share leaves a piece per CTA in part_o.
 //                  Both are written [dim / 4][row] in 16-byte words, so a warp
 //                  of rows writes 512 contiguous bytes.
@@ -167,6 +169,7 @@ __device__ __forceinline__ void piece_end(SharedWalk &w) {
 // the sums over all threads. `sums` is scratch; the next call may follow at once.
 template <int N, class T>
 __device__ __forceinline__ void block_scan(T (&v)[N], T (&total)[N], T (*sums)[kPlanThreads / 32]) {
+    constexpr int kWarps = kPlanThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1)
@@ -181,13 +184,13 @@ __device__ __forceinline__ void block_scan(T (&v)[N], T (&total)[N], T (*sums)[k
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        T w = lane < kPlanThreads / 32 ? sums[k][lane] : 0;
+        T w = lane < kWarps ? sums[k][lane] : 0;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
+        for (int off = 1; off < kWarps; off <<= 1) {
             const T n = __shfl_up_sync(0xffffffffu, w, off);
             if (lane >= off) w += n;
         }
-        total[k] = __shfl_sync(0xffffffffu, w, 31);
+        total[k] = __shfl_sync(0xffffffffu, w, kWarps - 1);
         const T before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
         v[k] += warp > 0 ? before : 0;
     }
@@ -207,9 +210,9 @@ enum Kind { kAlone, kPacked, kTensor };
 // tokens: 25.0 packed, 28.4.)
 __device__ __forceinline__ Kind cheapest(int live, int n, int tokens, int group, int group_pad,
                                          bool tensor_ok) {
-    const int fit = shared_fit(group);
+    const int fit_log2 = shared_fit_log2(group), fit = 1 << fit_log2;
     const float len = (float)tokens * (1.f / kKeys);
-    const float packed = 0.8f * len * (float)((n + fit - 1) / fit);
+    const float packed = 0.8f * len * (float)((n + fit - 1) >> fit_log2);
     const float pairs = (float)(((long long)n * group_pad + kPairRows - 1) / kPairRows);
     const float tensor = pairs * (4.f + ceilf(len) * (n * group_pad <= kRows ? 1.f : 2.f));
     if (live < kSharedMinSeqs || tokens == 0) return kAlone;
@@ -222,15 +225,15 @@ __device__ __forceinline__ Kind cheapest(int live, int n, int tokens, int group,
 // takes about 2 us on an SM beside the other reads, a piece of a unit (its
 // queries, first keys, last product and rows) 3 us more, and an SM reads about
 // 70 GB/s of K and V, all together 6.4 TB/s. SMs go to both in the proportion of
-// the work, so that both end together. A count that is a multiple of the units
-// gives every SM one piece instead of two or more, and lets the units of a KV
-// head read the same keys at the same time; it is taken where the estimate is
-// not a tenth worse. (SMs for the prefix and measured us: 128 sequences x 64
-// heads over 2048 shared and 256 own tokens, 32 units: 49 51.5, 64 44.8; 256 x
-// 32 over 32768 and 16 .. 1000: 96 165.7, 100 185.6, 106 169.9; before the own
-// tokens' cache hints.)
-__device__ __forceinline__ int prefix_sms(int sm_count, float tiles, float units, float own) {
-    constexpr float kTile = 2.f, kPiece = 3.f, kRate = 70e3f, kRateAll = 6.4e6f;
+// the work, so that both end together. The pairs of a (group, KV head) should
+// read the same keys at the same time, or the keys come from memory once for each:
+// so the count is a multiple of the lanes, or with one lane a multiple of the units
+// where the estimate is not a tenth worse; a multiple of the units also gives
+// every SM one piece instead of two. (SMs for the prefix and measured us, with one
+// lane: 256 sequences x 32 heads over 32768 and 16 .. 1000 tokens, 32 units of 4
+// pairs: 96 165.7, 100 185.6, 106 169.9; 128 x 64 over 2048 and 256: 49 51.5, 64 44.8.)
+__device__ __forceinline__ int prefix_sms(int sm_count, float tiles, float units, float own, int lanes) {
+    constexpr float kTile = 1.6f, kPiece = 3.f, kRate = 95e3f, kRateAll = 5.6e6f;
     const float sms = (float)sm_count, bytes = own * (2.f * kTileBytes);
     auto time = [&](float x, float pieces) {
         const float rate = fminf((sms - x) * kRate, kRateAll);
@@ -240,17 +243,26 @@ __device__ __forceinline__ int prefix_sms(int sm_count, float tiles, float units
     const float a = tiles * kTile + units * kPiece, b = bytes * (1.f / kRate) + 1.f;
     float best = fmaxf(1.f, fminf(floorf(__fdividef(sms * a, a + b) + 0.5f), sms - 1.f));
     best = fminf(best, tiles);
-    float t = 1.1f * time(best, best >= tiles ? 1.f : 2.f + __fdividef(units, best));
-    const float k = floorf(__fdividef(best, units));
+    auto pieces = [&](float x) { return x >= tiles ? 1.f : 2.f + __fdividef(units, x); };
+    float t = 1.1f * time(best, pieces(best)), from = best;
+    auto consider = [&](float step, float each) {       // multiples of `step` next to `from`
+        const float k = floorf(__fdividef(from, step));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float x = (k + (float)i) * units;
-        const float u = x >= 1.f && x < sms && x <= tiles ? time(x, 1.f) : INFINITY;
-        if (u < t) {
-            t = u;
-            best = x;
+        for (int i = 0; i < 2; ++i) {
+            const float x = (k + (float)i) * step;
+            const float u = x >= 1.f && x < sms && x <= tiles ? time(x, each > 0.f ? each : pieces(x)) : INFINITY;
+            if (u <= t) {
+                t = u;
+                best = x;
+            }
         }
+    };
+    if (lanes > 1) {
+        t = INFINITY;       // and no tenth: any multiple of the lanes will do
+        consider((float)lanes, 0.f);
+        if (t == INFINITY) t = 1.1f * time(best, pieces(best));
     }
+    consider(units, 1.f);
     return (int)best;
 }
 
@@ -261,6 +273,9 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
     __shared__ int s_counts[3][kPlanThreads / 32];
     const int G = sh.num_groups, S = a.num_seqs, tid = threadIdx.x, lane = tid & 31;
     const int Hkv = a.num_kv_heads;
+    const int fit_log2 = shared_fit_log2(a.group), fit = 1 << fit_log2;
+    __shared__ int s_pairs;             // pairs of the first active group
+    __shared__ int s_packed[kPlanThreads];              // tokens of the first packed prefixes' entries
     int *bases = plan_smem;             // [G] flat index of the group's first tile
     int *starts = bases + G;            // [G + 1]
     int *tokens = starts + G + 1;       // [G] shortest non-empty length, then tokens computed together
@@ -323,13 +338,15 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
         }
     }
     __syncthreads();
+    auto pairs_of = [&](int g) {
+        return (int)(((int64_t)(starts[g + 1] - starts[g]) * sh.group_pad + kPairRows - 1) / kPairRows);
+    };
     int base = 0, units = 0, act = 0, entries = covered;    // the host has ruled out 2^31 tiles
     for (int g0 = 0; g0 < G; g0 += kPlanThreads) {
         const int g = g0 + tid;
         SharedGroup gr{};
         Kind kind = kAlone;
         int chunks = 0;
-        const int fit = shared_fit(a.group);
         if (g < G) {
             const int64_t want = (int64_t)clamp(g0 == 0 ? my_prefix : sh.prefix_blocks[g], a.max_blocks_per_seq)
                                  << a.block_size_log2;
@@ -340,8 +357,8 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
             gr.n = starts[g + 1] - starts[g];
             if (ordered) kind = cheapest(where[g], gr.n, gr.tokens, a.group, sh.group_pad, sh.tensor != 0);
             gr.nt = (gr.tokens + kKeys - 1) / kKeys;
-            gr.pairs = (int)(((int64_t)gr.n * sh.group_pad + kPairRows - 1) / kPairRows);
-            if (kind == kPacked) chunks = (gr.n + fit - 1) / fit;
+            gr.pairs = pairs_of(g);
+            if (kind == kPacked) chunks = (gr.n + fit - 1) >> fit_log2;
         }
         const bool tensor = kind == kTensor;
         const int u = tensor ? gr.pairs * Hkv : 0, tiles = u * gr.nt;
@@ -357,12 +374,14 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
                 const int at = act + (v[2] & 0x1fff) - 1;
                 where[g] = at;
                 sh.groups[at] = gr;
+                if (at == 0) s_pairs = gr.pairs;
             } else if (kind == kPacked) {
                 const int at = entries + (v[2] >> 13) - chunks;
                 where[g] = -2 - at;
                 for (int c = 0; c < chunks; ++c) {
                     const int n = gr.n - c * fit < fit ? gr.n - c * fit : fit;
                     sh.entries[at + c] = SharedUnit{gr.row, gr.s0 + c * fit, 0, gr.tokens, n * a.group, 3, {0, 0}};
+                    if (at + c - covered < kPlanThreads) s_packed[at + c - covered] = gr.tokens;
                 }
             }
         }
@@ -372,6 +391,12 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
         entries += total[2] >> 13;
     }
     __syncthreads();
+    int lanes = 1;
+    if (base > 0) {
+        bool differ = false;
+        for (int g = tid; g < G; g += kPlanThreads) differ |= where[g] >= 0 && pairs_of(g) != s_pairs;
+        if (!__syncthreads_or(differ)) lanes = s_pairs;
+    }
     long long own = 0;
     for (int v0 = 0; v0 < entries; v0 += kPlanThreads) {
         const int v = v0 + tid;
@@ -381,14 +406,15 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
             const int g = s == tid ? my_group : group_of(s), L = length(s);
             const int start = g >= 0 && L > 0 ? tokens[g] : 0;
             const int at = start > 0 ? where[g] : -1;
-            const int nth = start > 0 ? s - starts[g] : 0, fit = shared_fit(a.group);
-            sh.seq[s] = at <= -2 ? make_int4(-1, -2 - at + nth / fit, nth % fit * a.group, 0)
+            const int nth = start > 0 ? s - starts[g] : 0;
+            sh.seq[s] = at <= -2 ? make_int4(-1, -2 - at + (nth >> fit_log2), (nth & (fit - 1)) * a.group, 0)
                                  : make_int4(at, -1, 0, 0);
             sh.entries[v] = SharedUnit{s, s, start, L, a.group, start > 0 ? 1 : 0, {0, 0}};
             // an empty unit owns one (empty) tile
             n[0] = (L > start ? (L - start + kTileTokens - 1) / kTileTokens : 1) + kUnitTiles;
         } else if (v < entries) {
-            n[0] = sh.entries[v].len / kTileTokens + kUnitTiles;
+            const int p = v - covered;
+            n[0] = (p < kPlanThreads ? s_packed[p] : sh.entries[v].len) / kTileTokens + kUnitTiles;
         }
         block_scan(n, total, s_sums);
         if (v < entries) sh.scan[v] = own + n[0];
@@ -396,10 +422,17 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
     }
     own *= Hkv;
     const int sms = sh.max_workers, per_sm = a.num_workers / sms;
-    const int workers = base > 0 ? prefix_sms(sms, (float)base, (float)units, (float)own) : 0;
+    int workers = 0, tiles = 0, shares = 0;     // tiles and shares of a lane
+    if (base > 0) {
+        workers = prefix_sms(sms, (float)base, (float)units, (float)own, lanes);
+        if (workers % lanes != 0) lanes = 1;    // fewer SMs than lanes
+        tiles = base / lanes;
+        shares = workers / lanes;
+    }
     if (tid == 0) {
         SharedHeader h;
-        h.tiles = base;
+        h.tiles = tiles;
+        h.lanes = lanes;
         h.own_tiles = own;
         h.s_lo = s_lo;
         h.s_hi = s_hi;
@@ -414,20 +447,24 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
     // before it)
     for (int w = tid; w < workers; w += kPlanThreads) {
         SharedWalk k{};
-        const int q = base / workers, r = base - q * workers;      // floor(w base / workers) in 32 bits
-        k.T = w * q + w * r / workers;
-        k.T1 = (w + 1) * q + (w + 1) * r / workers;
+        k.lane = w % lanes;
+        k.lanes = lanes;
+        const int i = w / lanes;
+        const int q = tiles / shares, r = tiles - q * shares;      // floor(i tiles / shares) in 32 bits
+        k.T = i * q + i * r / shares;
+        k.T1 = (i + 1) * q + (i + 1) * r / shares;
+        const int at = (int)k.T * lanes;        // as if all lanes were one
         int lo = 0, hi = G;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (bases[mid] <= k.T) lo = mid; else hi = mid;
+            if (bases[mid] <= at) lo = mid; else hi = mid;
         }
         k.act = where[lo];
         k.gr = sh.groups[k.act];
-        const int rem = (int)(k.T - k.gr.base), unit = rem / k.gr.nt;
+        const int rem = (at - bases[lo]) / lanes, unit = rem / k.gr.nt, per_head = k.gr.pairs / lanes;
         k.j0 = rem - unit * k.gr.nt;
-        k.kvh = unit / k.gr.pairs;
-        k.pair = unit - k.kvh * k.gr.pairs;
+        k.kvh = unit / per_head;
+        k.pair = k.lane + lanes * (unit - k.kvh * per_head);
         piece_end(k);
         sh.walks[w] = k;
     }
@@ -448,8 +485,9 @@ __device__ __forceinline__ bool walk_next(volatile Walk &place, const SharedArgs
         Walk &w = const_cast<Walk &>(place);
         w.T += w.j1 - w.j0;
         w.j0 = 0;
-        if (++w.pair == w.gr.pairs) {
-            w.pair = 0;
+        w.pair += w.lanes;
+        if (w.pair >= w.gr.pairs) {
+            w.pair = w.lane;
             if (++w.kvh == num_kv_heads) {
                 w.kvh = 0;
                 w.gr = sh.groups[++w.act];
@@ -483,7 +521,10 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
     constexpr int BT = kRows / G;               // sequences per query tile
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int w_id = blockIdx.x;
+    // The SMs work in pairs that share a way to L2: a CTA whose neighbour streams own
+    // tokens ended 13 us after the others (of 135). The first CTA starts beside the
+    // plan's SM, which is still taken, and the next ones two by two: so it goes last.
+    const int w_id = blockIdx.x == 0 ? (int)gridDim.x - 1 : (int)blockIdx.x - 1;
     if (tid == 0) {
         tc::prefetch_map(&tmap_k);
         tc::prefetch_map(&tmap_v);
@@ -529,10 +570,12 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     volatile Walk &w = reinterpret_cast<Walk *>(smem + kOffWalk)[warp];
-    const bool works = w_id < sh.hdr->workers;
-    if (works && (tid & 31) < (int)(sizeof(Walk) / 16))
+    // the share's first piece together with the count of shares (a CTA without a
+    // share reads what an earlier call left, and does not use it)
+    if ((tid & 31) < (int)(sizeof(Walk) / 16))
         reinterpret_cast<int4 *>(smem + kOffWalk + warp * kWalkBytes)[tid & 31] =
-            reinterpret_cast<const int4 *>(sh.walks + w_id)[tid & 31];
+            __ldcg(reinterpret_cast<const int4 *>(sh.walks + w_id) + (tid & 31));
+    const bool works = w_id < __ldcg(&sh.hdr->workers);
     __syncwarp();
     if (!works) {
         // more CTAs than tiles

@@ -14,8 +14,12 @@ constexpr int kSharedMinSeqs = 2;       // a prefix is computed apart for at lea
 // result), in tiles. Without it the shares of many short units ended up to 9 us
 // after the others (60 sequences of 1 .. 500 own tokens).
 constexpr int kUnitTiles = 4;
-// Sequences whose heads fit the 8 columns of one unit of decode_shared_kernel.
-__host__ __device__ constexpr int shared_fit(int group) { return group <= 8 ? 8 / group : 1; }
+// Sequences whose heads fit the 8 columns of one unit of decode_shared_kernel: a
+// power of two.
+__host__ __device__ constexpr int shared_fit_log2(int group) {
+    return group == 1 ? 3 : group == 2 ? 2 : group <= 4 ? 1 : 0;
+}
+__host__ __device__ constexpr int shared_fit(int group) { return 1 << shared_fit_log2(group); }
 constexpr int kPairRows = 256;      // rows of a prefix unit: two query tiles of 128
 
 // A group whose prefix is computed once. Its tile space: (KV head, pair of
@@ -30,19 +34,24 @@ struct alignas(16) SharedGroup {
 static_assert(sizeof(SharedGroup) == 32, "one 32-byte sector");
 
 // A share's walk over the tile space: its pieces are runs of key tiles
-// [j0, j1) of one unit, a unit being 256 query rows of one (group, KV head).
+// [j0, j1) of one unit, a unit being 256 query rows of one (group, KV head). Where
+// all groups have the same number of pairs, the pairs are lanes: a share stays in one
+// lane, the lanes are cut alike, and T counts the tiles of a lane. Otherwise there
+// is one lane, of all pairs.
 struct alignas(16) SharedWalk {
     int64_t T, T1;          // next tile, end of the share
     SharedGroup gr;
     int act, kvh, pair, j0, j1;
+    int lane, lanes;
 };
 
 struct SharedHeader {
-    int64_t tiles;          // prefix: key tiles of all active groups
+    int64_t tiles;          // prefix: key tiles of a lane
     int64_t own_tiles;      // decode.cu: 16-token tiles of all units, and kUnitTiles for each
     int s_lo, s_hi;         // sequences the call covers
     int entries;            // of SharedArgs::entries
     int workers;            // CTAs the prefix tiles are shared among
+    int lanes;              // share w is in lane w % lanes
     int own_workers;        // warps the own tiles are shared among
 };
 

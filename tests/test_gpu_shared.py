@@ -194,6 +194,17 @@ def test_many_key_tiles_per_share(n, blocks):
         Batch([n], [blocks], [3, 40], 16, 1).check()
 
 
+# pairs of 128-row query tiles: 3 with the last half empty, 4 and 38 of one group; 2 of
+# every group on the prefix kernel, with others between; 2 and 1
+@pytest.mark.parametrize("sizes,blocks,Hq,Hkv,own", [
+    ([80], [600], 24, 3, [60, 5]), ([256], [300], 32, 8, [400, 16]), ([256], [1100], 32, 8, [16, 700, 0]),
+    ([1200], [40], 8, 1, [3, 20]), ([64, 60], [200, 333], 16, 2, [300, 1]),
+    ([64, 1, 3, 60], [200, 9, 4, 333], 16, 2, [300, 1]), ([64, 20], [200, 333], 16, 2, [90, 1]),
+])
+def test_pairs_of_query_tiles(sizes, blocks, Hq, Hkv, own):
+    Batch(sizes, blocks, own, Hq, Hkv).check()
+
+
 # parts of a row spread over groups of threads and over CTAs: few rows with many
 # parts, some, and many rows; prefixes packed into one unit and on the prefix kernel
 @pytest.mark.parametrize("sizes,blocks,Hq,Hkv,own", [
