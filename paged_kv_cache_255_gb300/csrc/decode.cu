@@ -1092,11 +1092,6 @@ struct Merge {
     }
 };
 
-// n / d, in 32 bits where both fit.
-__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
-    return ((n | d) >> 32) == 0 ? (int64_t)((uint32_t)n / (uint32_t)d) : n / d;
-}
-
 // With shared prefixes: the parts of an output row's prefix, then its own. The
 // prefix is left either by decode_shared_kernel, like the own part (a row of
 // whole_o, or a column of a slot per share), or by shared.cu (a row of unit_o,
@@ -1115,14 +1110,7 @@ __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
 template <int GP, int COLS, int GROUPS, int WORDS>
 __global__ void __launch_bounds__(8 * WORDS * GROUPS, GROUPS == 1 ? 8 : 2)
 combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
-    constexpr int kPairSeqs = kPairRows / GP, kBatch = 3, kThreads = 8 * WORDS;
-    struct Row {
-        int parts;                      // of shared.cu: 0 none, 1 whole in unit_o, else pieces
-        int slot;                       // of the first piece; the next ones are at even slots
-        int place;                      // row | 2 lanes << 8: the row in a piece, the slots between pieces
-        int packed, col;                // entry and column of the prefix in decode_shared_kernel, or -1
-    };
-    __shared__ Row s_row[8];
+    constexpr int kBatch = 3, kThreads = 8 * WORDS;
     __shared__ Merge s_merge[GROUPS == 1 ? 1 : GROUPS - 1][GROUPS == 1 ? 1 : kThreads];
     const int group = threadIdx.x / kThreads, tid = threadIdx.x % kThreads;
     const int word = blockIdx.z * WORDS + (tid >> 3);   // dims [4 word, 4 word + 4), and 64 further on
@@ -1130,39 +1118,17 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x & 7);
     const int kvh = blockIdx.y, Hkv = a.num_kv_heads;
     const int s = (int)(row / GP), h = (int)(row % GP);
-    const int s_lo = __ldcg(&sh.hdr->s_lo);
     auto out_row = [&]() { return (int64_t)s * a.num_q_heads + kvh * a.group + h; };
-    const bool mine = row < rows && h < a.cols && s >= s_lo && s < __ldcg(&sh.hdr->s_hi);
-    if (threadIdx.x < 8 && !mine) s_row[threadIdx.x] = Row{0, 0, 0, -1, 0};
-    if (threadIdx.x < 8 && mine) {
-        const int4 q = __ldcg(sh.seq + s);
-        Row r{0, 0, 0, q.y, q.z + h};
-        if (q.x >= 0) {
-            const int64_t tiles = __ldcg(&sh.hdr->tiles);
-            const int lanes = __ldcg(&sh.hdr->lanes), shares = __ldcg(&sh.hdr->workers) / lanes;
-            const SharedGroup *g = sh.groups + q.x;
-            const int tok = s - __ldcg(&g->s0), pair = tok / kPairSeqs, nt = __ldcg(&g->nt);
-            const int lane = pair % lanes;
-            const int64_t U0 = quotient(__ldcg(&g->base), lanes) +
-                               ((int64_t)kvh * (__ldcg(&g->pairs) / lanes) + pair / lanes) * nt;
-            // share i of a lane is [i tiles / shares, (i + 1) tiles / shares), worker i lanes + lane
-            const int i0 = (int)quotient((U0 + 1) * shares - 1, tiles);
-            const int i1 = (int)quotient((U0 + nt) * shares - 1, tiles);
-            r.parts = 1 + i1 - i0;
-            // worker w's slot 2 w holds its first piece, 2 w + 1 its last; only
-            // the first share may have begun before the unit
-            r.slot = 2 * (i0 * lanes + lane) + (quotient(i0 * tiles, shares) < U0 ? 1 : 0);
-            r.place = (tok - pair * kPairSeqs) * GP + h + (2 * lanes << 8);
-        }
-        s_row[threadIdx.x] = r;
-    }
-    __syncthreads();
+    const int s_lo = __ldcg(&sh.hdr->s_lo), s_hi = __ldcg(&sh.hdr->s_hi);
+    const int4 q = row < rows ? __ldcg(sh.seq + s) : make_int4(-1, -1, 0, 0);
+    const bool mine = row < rows && h < a.cols && s >= s_lo && s < s_hi;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const Row r = s_row[threadIdx.x & 7];
-    int4 u = make_int4(-2, 0, 0, 0), x = make_int4(0, -1, 0, 0);
+    // where the own part is, the prefix's in decode_shared_kernel, and in shared.cu
+    int4 u = make_int4(-2, 0, 0, 0), x = make_int4(0, -1, 0, 0), y = make_int4(0, 0, 0, 0);
     if (mine) {
         u = sh.units[(int64_t)(s - s_lo) * Hkv + kvh];
-        if (r.packed >= 0) x = sh.units[(int64_t)r.packed * Hkv + kvh];
+        if (q.y >= 0) x = sh.units[(int64_t)q.y * Hkv + kvh];
+        if (q.x >= 0) y = sh.parts[q.x + kvh * q.w];
     }
     // A record is not there when the share that owed it gave up waiting for its
     // tiles (the launch's outputs are undefined then): never an address from one.
@@ -1170,11 +1136,13 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
         return v.x >= -2 && v.x < 2 * a.num_workers && v.z >= 0 && v.z <= v.y && v.y < a.num_workers &&
                (v.x < 0 || v.x >> 1 == v.z);
     };
+    const bool sane_y = y.x >= 0 && y.y >= 0 && y.y <= sh.max_workers && y.z >= 0 && y.z <= 2 * sh.max_workers &&
+                        (y.x | 1) + (int64_t)(y.y - 1) * y.z < 2 * sh.max_workers;
     // else not covered, or written by the share that computed it
-    const bool todo = u.x != -2 && sane(u) && (r.packed < 0 || sane(x));
+    const bool todo = u.x != -2 && sane(u) && sane_y && (q.y < 0 || sane(x));
     // the parts in the order of their keys; a batch's loads are all in flight
     // before its merge
-    const int n_packed = 1 + x.y - x.z, n_prefix = n_packed + r.parts;
+    const int n_packed = 1 + x.y - x.z, n_prefix = n_packed + y.y;
     const int parts = todo ? n_prefix + 1 + u.y - u.z : 0;
     const int n = parts * (group + 1) / GROUPS;
     const float4 *slots = reinterpret_cast<const float4 *>(a.part_o);
@@ -1195,15 +1163,15 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
                 return (int64_t)(at == 0 ? first : (first & ~1) + at * apart);
             };
             if (i >= n_packed && i < n_prefix) {
-                if (r.parts == 1) {
+                if (y.y == 1) {
                     from = sh.unit_o + ((int64_t)kvh * 32 + word) * rows + row;
                     step = 16 * rows;
                     e[k] = sh.unit_ml[kvh * rows + row];
                 } else {
-                    const int64_t slot = slot_of(r.slot, i - n_packed, r.place >> 8);
-                    from = sh.part_o + (slot * 32 + word) * kPairRows + (r.place & 255);
+                    const int64_t slot = slot_of(y.x, i - n_packed, y.z);
+                    from = sh.part_o + (slot * 32 + word) * kPairRows + q.z + h;
                     step = 16 * kPairRows;
-                    e[k] = sh.part_ml[slot * kPairRows + (r.place & 255)];
+                    e[k] = sh.part_ml[slot * kPairRows + q.z + h];
                 }
             } else {
                 const bool own = i >= n_prefix;
@@ -1213,7 +1181,7 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
                     from = sh.whole_o + whole * 32 + word;
                     e[k] = sh.whole_ml[whole];
                 } else {
-                    const int64_t slot = slot_of(first, own ? i - n_prefix : i, 2) * COLS + (own ? h : r.col);
+                    const int64_t slot = slot_of(first, own ? i - n_prefix : i, 2) * COLS + (own ? h : q.z + h);
                     from = slots + slot * 32 + word;
                     e[k] = slots_ml[slot];
                 }

@@ -279,7 +279,7 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
     int *bases = plan_smem;             // [G] flat index of the group's first tile
     int *starts = bases + G;            // [G + 1]
     int *tokens = starts + G + 1;       // [G] shortest non-empty length, then tokens computed together
-    int *first = tokens + G;            // [G] first non-empty sequence
+    int *first = tokens + G;            // [G] first non-empty sequence, then first unit
     int *where = first + G;             // [G] non-empty sequences, then index of the active group or
                                         //     -2 - first entry of the packed prefix, or -1
     // programmatic dependent of whatever precedes the call
@@ -367,7 +367,9 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
         block_scan(v, total, s_counts);
         if (g < G) {
             gr.base = base + v[0] - tiles;
+            gr.unit = units + v[1] - u;
             bases[g] = gr.base;
+            first[g] = gr.unit;
             tokens[g] = kind == kAlone ? 0 : gr.tokens;
             where[g] = -1;
             if (tensor) {
@@ -407,8 +409,10 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
             const int start = g >= 0 && L > 0 ? tokens[g] : 0;
             const int at = start > 0 ? where[g] : -1;
             const int nth = start > 0 ? s - starts[g] : 0;
+            const int nth_row = nth * sh.group_pad;     // of the group's query rows
             sh.seq[s] = at <= -2 ? make_int4(-1, -2 - at + (nth >> fit_log2), (nth & (fit - 1)) * a.group, 0)
-                                 : make_int4(at, -1, 0, 0);
+                        : at < 0 ? make_int4(-1, -1, 0, 0)
+                                 : make_int4(first[g] + nth_row / kPairRows, -1, nth_row % kPairRows, pairs_of(g));
             sh.entries[v] = SharedUnit{s, s, start, L, a.group, start > 0 ? 1 : 0, {0, 0}};
             // an empty unit owns one (empty) tile
             n[0] = (L > start ? (L - start + kTileTokens - 1) / kTileTokens : 1) + kUnitTiles;
@@ -433,6 +437,7 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
         SharedHeader h;
         h.tiles = tiles;
         h.lanes = lanes;
+        h.shares = shares;
         h.own_tiles = own;
         h.s_lo = s_lo;
         h.s_hi = s_hi;
@@ -729,6 +734,16 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
                                             w.kvh * a.group, w.gr.s0 + w.pair * 2 * BT + t * BT, bar(kBarQFull));
                 }
                 warp_arrive(bar(kBarQFull));
+                if (lane == 0 && w.j0 == 0) {
+                    // how the combine finds the unit: the shares from this one to the
+                    // one of the unit's last key tile
+                    const int64_t end = w.T + w.gr.nt;
+                    const int parts = w.j1 == w.gr.nt ? 1
+                                      : (int)((end * sh.hdr->shares - 1) / sh.hdr->tiles) - w_id / w.lanes + 1;
+                    sh.parts[w.gr.unit + w.kvh * w.gr.pairs + w.pair] =
+                        make_int4(2 * w_id + (piece > 0 ? 1 : 0), parts, 2 * w.lanes, 0);
+                }
+                __syncwarp();
             }
             // coordinates (dim 1, dim 2) of this lane's box of tile j; dim 1 (or
             // 2) at -kKeys reads zeros, for a block id outside the pool; x =
@@ -929,7 +944,7 @@ cudaError_t launch_g(const DecodeArgs &a, const SharedArgs &sh, cudaStream_t st)
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct Carve {
-    size_t hdr, seq, entries, scan, groups, walks, part_o, part_ml, unit_o, unit_ml, units, whole_o, whole_ml, end;
+    size_t hdr, seq, entries, scan, groups, walks, parts, part_o, part_ml, unit_o, unit_ml, units, whole_o, whole_ml, end;
     Carve(int S, int G, int hq, int hkv, int gp, int workers) {
         const size_t rows = (size_t)S * gp * hkv, own = (size_t)S * hq, slots = 2 * (size_t)workers;
         hdr = 0;
@@ -938,7 +953,8 @@ struct Carve {
         scan = entries + round256(2 * (size_t)S * sizeof(SharedUnit));
         groups = scan + round256(2 * (size_t)S * sizeof(long long));
         walks = groups + round256((size_t)G * sizeof(SharedGroup));
-        part_o = walks + round256((size_t)workers * sizeof(SharedWalk));
+        parts = walks + round256((size_t)workers * sizeof(SharedWalk));
+        part_o = parts + round256((size_t)S * hkv * sizeof(int4));
         part_ml = part_o + slots * 32 * kPairRows * sizeof(float4);
         unit_o = part_ml + slots * kPairRows * sizeof(float2);
         unit_ml = unit_o + rows * 32 * sizeof(float4);
@@ -969,6 +985,7 @@ void shared_carve_workspace(SharedArgs &sh, void *workspace, const DecodeArgs &a
     sh.scan = reinterpret_cast<long long *>(p + c.scan);
     sh.groups = reinterpret_cast<SharedGroup *>(p + c.groups);
     sh.walks = reinterpret_cast<SharedWalk *>(p + c.walks);
+    sh.parts = reinterpret_cast<int4 *>(p + c.parts);
     sh.part_o = reinterpret_cast<float4 *>(p + c.part_o);
     sh.part_ml = reinterpret_cast<float2 *>(p + c.part_ml);
     sh.unit_o = reinterpret_cast<float4 *>(p + c.unit_o);

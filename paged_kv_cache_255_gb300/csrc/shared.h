@@ -25,7 +25,8 @@ constexpr int kPairRows = 256;      // rows of a prefix unit: two query tiles of
 // A group whose prefix is computed once. Its tile space: (KV head, pair of
 // query tiles, key tile), the key tile fastest, from `base` on.
 struct alignas(16) SharedGroup {
-    int64_t base;       // flat index of the group's first key tile
+    int base;           // flat index of the group's first key tile
+    int unit;           // index of its first unit in SharedArgs::parts
     int row;            // table row the prefix is read through
     int s0, n;          // its sequences
     int tokens;         // prefix tokens computed together, a multiple of 16
@@ -51,7 +52,7 @@ struct SharedHeader {
     int s_lo, s_hi;         // sequences the call covers
     int entries;            // of SharedArgs::entries
     int workers;            // CTAs the prefix tiles are shared among
-    int lanes;              // share w is in lane w % lanes
+    int lanes, shares;      // worker w has share w / lanes of lane w % lanes, of `shares`
     int own_workers;        // warps the own tiles are shared among
 };
 
@@ -77,11 +78,14 @@ struct SharedArgs {
     int tensor;                     // whether the prefix kernel is launched
     // in the workspace
     SharedHeader *hdr;
-    int4 *seq;                      // [S] {active group or -1, entry of its packed prefix or -1, column there}
+    int4 *seq;                      // [S] {unit of KV head 0 or -1, entry of its packed prefix or -1,
+                                    //      row of the unit or column of the entry, units of a KV head}
     SharedUnit *entries;            // [2 S] own tokens of every covered sequence, then packed prefixes
     long long *scan;                // [2 S] the same of one KV head, through an entry
     SharedGroup *groups;            // [num_groups] the active ones
     SharedWalk *walks;              // [max_workers] first piece of every share
+    int4 *parts;                    // [S Hkv] a prefix unit's {first slot, parts, slots between them};
+                                    // slot 2 w is worker w's first piece, 2 w + 1 its last
     float4 *part_o;                 // [2 max_workers][32][256] pieces of units that several workers share
     float2 *part_ml;                // [2 max_workers][256] (running max in log2 units, sum)
     float4 *unit_o;                 // [Hkv][32][S G] units one worker computed whole
