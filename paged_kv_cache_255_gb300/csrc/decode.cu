@@ -1100,8 +1100,9 @@ struct Merge {
 // a row: a warp's 8 rows x 4 words are whole 128-byte lines of shared.cu's
 // arrays, and whole sectors of the others and of `out`. (One warp per row, each
 // lane in a line of its own, took 17 us for 8192 rows of 6 parts; one word per
-// thread needed two waves of CTAs and 7 us.) What does not depend on the two
-// kernels before is looked up while they run. GP: heads of a group, padded;
+// thread needed two waves of CTAs and 7 us.) Where the parts are, the two
+// kernels before have recorded: looked up from the split here, 2 us of a call
+// whose last CTAs are the prefix kernel's. GP: heads of a group, padded;
 // COLS: columns of a slot. With few rows every one has many parts (8 units over
 // all warps of the GPU have 228 each): GROUPS groups of threads take contiguous
 // runs of them, their results merged pairwise, and a CTA takes only 2 WORDS of a

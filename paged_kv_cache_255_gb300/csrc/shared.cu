@@ -39,9 +39,9 @@
 // time on SMs of their own: one is bound by the tensor pipe and by the softmax
 // between its products, the other by memory, and neither leaves room for the other
 // on an SM. 128 sequences x 64 heads over 2048 shared and 256 own tokens:
-// 38.5 us (pa_decode 86.5, the bytes alone 21.7), of which about 11 are the plan
-// and the launches up to the first loads and 6 the combine. 256 x 32 over 32768
-// shared and 16 .. 1000 own: 164 us (pa_decode 2178, the bytes alone 99); the 96
+// 39 to 44 us (pa_decode 86.5, the bytes alone 21.7), of which about 10 are the plan
+// and the launches up to the first loads and 5 the combine. 256 x 32 over 32768
+// shared and 16 .. 1000 own: 146 us (pa_decode 2198, the bytes alone 99); the 104
 // SMs of the prefix keep their tensor pipes 68 % busy, a pair of 128-key
 // products of both kinds taking 3230 cycles, the softmax of a tile 1275.
 //
@@ -222,16 +222,17 @@ __device__ __forceinline__ Kind cheapest(int live, int n, int tokens, int group,
 
 // How many of the SMs compute the `tiles` prefix tiles of `units` units, while
 // the others work through `own` 16-token tiles. Measured: a prefix tile pair
-// takes about 2 us on an SM beside the other reads, a piece of a unit (its
-// queries, first keys, last product and rows) 3 us more, and an SM reads about
-// 70 GB/s of K and V, all together 6.4 TB/s. SMs go to both in the proportion of
+// takes about 1.6 us on an SM beside the other reads, a piece of a unit (its
+// queries, first keys, last product and rows) 3 us more, and an SM reads up to
+// 95 GB/s of K and V, all together 5.6 TB/s. SMs go to both in the proportion of
 // the work, so that both end together. The pairs of a (group, KV head) should
 // read the same keys at the same time, or the keys come from memory once for each:
 // so the count is a multiple of the lanes, or with one lane a multiple of the units
-// where the estimate is not a tenth worse; a multiple of the units also gives
-// every SM one piece instead of two. (SMs for the prefix and measured us, with one
-// lane: 256 sequences x 32 heads over 32768 and 16 .. 1000 tokens, 32 units of 4
-// pairs: 96 165.7, 100 185.6, 106 169.9; 128 x 64 over 2048 and 256: 49 51.5, 64 44.8.)
+// where the estimate is not a tenth worse. A multiple of the units also gives
+// every SM one piece instead of two, and is taken where it is no worse. (SMs for
+// the prefix and measured us: 256 sequences x 32 heads over 32768 and 16 .. 1000
+// tokens, 4 lanes, 32 units: 96 158.8, 100 152.4, 104 146.1, 108 152.8, and in one lane 96 159,
+// 100 185.6; 128 x 64 over 2048 and 256 tokens: 32 52.7, 52 45.5, 64 39.9, 72 42.3, 96 49.1.)
 __device__ __forceinline__ int prefix_sms(int sm_count, float tiles, float units, float own, int lanes) {
     constexpr float kTile = 1.6f, kPiece = 3.f, kRate = 95e3f, kRateAll = 5.6e6f;
     const float sms = (float)sm_count, bytes = own * (2.f * kTileBytes);
@@ -243,26 +244,26 @@ __device__ __forceinline__ int prefix_sms(int sm_count, float tiles, float units
     const float a = tiles * kTile + units * kPiece, b = bytes * (1.f / kRate) + 1.f;
     float best = fmaxf(1.f, fminf(floorf(__fdividef(sms * a, a + b) + 0.5f), sms - 1.f));
     best = fminf(best, tiles);
-    auto pieces = [&](float x) { return x >= tiles ? 1.f : 2.f + __fdividef(units, x); };
-    float t = 1.1f * time(best, pieces(best)), from = best;
-    auto consider = [&](float step, float each) {       // multiples of `step` next to `from`
-        const float k = floorf(__fdividef(from, step));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float x = (k + (float)i) * step;
-            const float u = x >= 1.f && x < sms && x <= tiles ? time(x, each > 0.f ? each : pieces(x)) : INFINITY;
-            if (u <= t) {
-                t = u;
-                best = x;
-            }
+    float t = 1.1f;
+    if (lanes > 1) {        // any multiple of the lanes will do
+        const float step = (float)lanes;
+        const float x = fminf(fmaxf(1.f, floorf(__fdividef(best, step) + 0.5f)), floorf(__fdividef(sms - 1.f, step))) * step;
+        if (x >= 1.f && x <= tiles) {
+            best = x;
+            t = 1.f;
         }
-    };
-    if (lanes > 1) {
-        t = INFINITY;       // and no tenth: any multiple of the lanes will do
-        consider((float)lanes, 0.f);
-        if (t == INFINITY) t = 1.1f * time(best, pieces(best));
     }
-    consider(units, 1.f);
+    t *= time(best, best >= tiles ? 1.f : 2.f + __fdividef(units, best));
+    const float k = floorf(__fdividef(best, units));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float x = (k + (float)i) * units;
+        const float u = x >= 1.f && x < sms && x <= tiles ? time(x, 1.f) : INFINITY;
+        if (u <= t) {
+            t = u;
+            best = x;
+        }
+    }
     return (int)best;
 }
 
@@ -275,6 +276,7 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
     const int Hkv = a.num_kv_heads;
     const int fit_log2 = shared_fit_log2(a.group), fit = 1 << fit_log2;
     __shared__ int s_pairs;             // pairs of the first active group
+    __shared__ bool s_differ;           // whether another has more or fewer
     __shared__ int s_packed[kPlanThreads];              // tokens of the first packed prefixes' entries
     int *bases = plan_smem;             // [G] flat index of the group's first tile
     int *starts = bases + G;            // [G + 1]
@@ -292,6 +294,7 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
     const int my_len = tid < S ? clamp(a.context_lens[tid], max_len) : 0;
     const int my_prefix = tid < G ? sh.prefix_blocks[tid] : 0;
     auto length = [&](int s) { return s == tid ? my_len : clamp(a.context_lens[s], max_len); };
+    if (tid == 0) s_differ = false;
     for (int g = tid; g <= G; g += kPlanThreads) {
         starts[g] = clamp(sh.group_starts[g], S);
         if (g < G) {
@@ -393,12 +396,9 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
         entries += total[2] >> 13;
     }
     __syncthreads();
-    int lanes = 1;
-    if (base > 0) {
-        bool differ = false;
-        for (int g = tid; g < G; g += kPlanThreads) differ |= where[g] >= 0 && pairs_of(g) != s_pairs;
-        if (!__syncthreads_or(differ)) lanes = s_pairs;
-    }
+    if (base > 0)
+        for (int g = tid; g < G; g += kPlanThreads)
+            if (where[g] >= 0 && pairs_of(g) != s_pairs) s_differ = true;     // read behind the scans below
     long long own = 0;
     for (int v0 = 0; v0 < entries; v0 += kPlanThreads) {
         const int v = v0 + tid;
@@ -426,8 +426,9 @@ shared_plan_kernel(const DecodeArgs a, const SharedArgs sh) {
     }
     own *= Hkv;
     const int sms = sh.max_workers, per_sm = a.num_workers / sms;
-    int workers = 0, tiles = 0, shares = 0;     // tiles and shares of a lane
+    int workers = 0, lanes = 1, tiles = 0, shares = 0;      // tiles and shares of a lane
     if (base > 0) {
+        if (!s_differ) lanes = s_pairs;
         workers = prefix_sms(sms, (float)base, (float)units, (float)own, lanes);
         if (workers % lanes != 0) lanes = 1;    // fewer SMs than lanes
         tiles = base / lanes;
