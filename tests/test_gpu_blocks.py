@@ -66,6 +66,9 @@ class State:
             assert np.array_equal(bits(d)[pool_ids], p[pool_ids])
 
 
+I32 = dict(dtype=torch.int32, device="cuda")
+
+
 def ints(x):
     return torch.tensor(np.asarray(x, np.int32).reshape(-1), device="cuda")
 
@@ -103,6 +106,38 @@ def test_copy_skips_and_reports():
 def test_copy_to_more_pools_than_one_launch_takes():
     s, _ = drawn(3, 1, 1, 16, 5, Hkv=1, pools=67)
     s.copy([[1, 3], [4, 2]])
+
+
+def test_fork_and_compact_more_pools_than_one_launch_takes():
+    s, _ = drawn(4, 3, 3, 16, 30, lens=[40, 16, 33], spare=4, Hkv=1, pools=67)
+    s.fork([0, 2, 0], [4, 5, 6])
+    s.free([0, 1])
+    s.compact()
+
+
+def test_offsets_past_32_bits():
+    # 4.6 GB a pool: more elements than 32 bits count, the used blocks at its two ends
+    NB, bs, Hkv = 140001, 16, 8
+    pool = torch.empty(NB, bs, Hkv, 128, dtype=torch.bfloat16, device="cuda")
+    handle = pa.CachePools([pool])
+    near, far = (torch.randint(-30000, 30000, (bs, Hkv, 128), dtype=torch.int16, device="cuda") for _ in range(2))
+    pool[3], pool[NB - 1] = near.view(torch.bfloat16), far.view(torch.bfloat16)
+    same = lambda b, x: torch.equal(pool[b].view(torch.int16), x)  # noqa: E731
+    pa.copy_blocks(handle, ints([3, NB - 2, NB - 1, 5]).view(2, 2))
+    assert same(NB - 2, near) and same(5, far)
+    tables, lens, refs = torch.zeros(4, 3, **I32), torch.zeros(4, **I32), torch.zeros(NB, **I32)
+    tables[0, 0], lens[0], refs[NB - 1] = NB - 1, 9, 1
+    refs[1:NB - 1] = 1
+    refs[NB - 3] = 0                                    # the only free block
+    pa.fork_blocks(handle, tables, lens, refs, ints([0]), ints([2]))
+    assert tables[2, 0].item() == NB - 3 and torch.equal(pool[NB - 3, :9].view(torch.int16), far[:9])
+    pool[NB - 3] = near.view(torch.bfloat16)
+    refs[1:NB - 3] = 0
+    refs[NB - 2] = 0
+    remap, live = pa.compact_blocks(handle, tables, lens, refs)
+    assert live.item() == 2 and tables[0, 0].item() == 2 and tables[2, 0].item() == 1
+    assert same(1, near) and same(2, far) and remap[NB - 1].item() == 2
+    assert pa.take_device_error() == 0
 
 
 def test_a_source_may_be_copied_twice():

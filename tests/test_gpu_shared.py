@@ -172,6 +172,46 @@ def test_more_groups_than_plan_threads():
     Batch([2, 1] * 600, [1, 2] * 600, [1, 7, 20], 2, 1).check()
 
 
+def test_as_many_groups_as_allowed():
+    Batch([2] * 4095 + [1], [1] * 4096, [1, 7, 0, 20], 2, 1).check()
+
+
+def test_as_many_sequences_as_allowed():
+    # 65535 sequences with one table row and two queries: two results
+    S = 65535
+    b = Batch([2], [2], [5], 2, 1)
+    _, width = b.tables.shape
+    o, A = reference(b.q, b.k, b.v, b.tables[:1].expand(2, -1), b.lens, b.scale, 16, False)
+    odd = torch.arange(S, device="cuda") % 2
+    i32 = dict(device="cuda", dtype=torch.int32)
+    for starts in ([0, S], [0, 40000, S], [7, S - 9]):
+        prefix = torch.full((len(starts) - 1,), 2, **i32)
+        out = pa.decode_shared(b.q[odd], b.k, b.v, b.tables[:1].expand(S, width).contiguous(),
+                               b.lens[:1].expand(S).contiguous(), torch.tensor(starts, **i32), prefix, b.scale)
+        got = out[starts[0]:starts[-1]].double()
+        want, bound = (x[odd][starts[0]:starts[-1]] for x in (o, 1.1 * 2 ** -8 * (A + 2 * o.abs())))
+        assert ((got - want).abs() <= bound).all()
+    assert pa.take_device_error() == 0
+
+
+def test_offsets_past_32_bits():
+    # 4.6 GB a pool: more elements than 32 bits count, the used blocks at its two ends
+    b = Batch([30, 3], [40, 9], [30, 1, 70], 16, 8)
+    n, NB = b.k.shape[0], 140001
+    far = torch.arange(n, device="cuda") % 2 == 1
+    place = torch.arange(n, device="cuda") + torch.where(far, NB - n, 0)
+    for hm in (False, True):
+        big = []
+        for x in (b.k, b.v):
+            y = torch.empty(NB, *(x.transpose(1, 2) if hm else x).shape[1:], dtype=x.dtype, device="cuda")
+            y[place] = x.transpose(1, 2) if hm else x
+            big.append(y)
+        inside = b.tables < n
+        tables = torch.where(inside, place[b.tables.clamp(max=n - 1).long()], b.tables.long()).int()
+        out = pa.decode_shared(b.q, *big, tables, b.lens, b.starts, b.prefix, b.scale, head_major=hm)
+        b.check(out)
+
+
 def test_rows_outside_the_groups_are_left():
     Batch([5, 3], [3, 7], [4, 18], pad=(2, 6)).check()
     b = Batch([5, 3], [3, 7], [4, 18], pad=(0, 3))
