@@ -71,8 +71,12 @@ PA_API size_t pa_blocks_workspace_size(int num_rows, int64_t num_blocks);
  * The child row must be empty (length 0 or less), and is given to the first
  * fork that lists it; a fork whose child is not empty or was listed before, or
  * that finds no free block, changes nothing and is recorded (code 6). A parent
- * or child of -1 is skipped. Owned entries that are 0 or outside the pool are
- * passed on as they are.
+ * or child of -1 is skipped. Owned entries that are 0, outside the pool or name a
+ * block with count 0 are passed on as they are, the last one too: no block is
+ * taken and no row copied for it. A block with count 0 is free whatever names
+ * it: the same call may hand it to a fork as its new block. Its count is then 1
+ * for that fork and 1 more for each entry passed on, and a full block's entry
+ * that names it is not recorded.
  *
  * num_forks is at most num_rows. Workspace: pa_blocks_workspace_size(num_rows,
  * num_blocks) bytes, 16-byte aligned. `layout` is the pools'.

@@ -255,8 +255,11 @@ fork_plan_kernel(const ForkArgs a) {
                 r.y = row_len(a.context_lens, p, max_len);
                 const int rows = r.y & ((1 << a.block_size_log2) - 1);
                 if (rows > 0) {
+                    // any other entry is passed on as it is: a block with count 0 is free, and
+                    // may be another fork's new block while its rows would be read
                     const int b = a.block_tables[(int64_t)p * a.max_blocks + (r.y >> a.block_size_log2)];
-                    tail = b > 0 && b < a.num_blocks;   // any other entry is passed on as it is
+                    tail = b > 0 && b < a.num_blocks && a.ref_counts[b] > 0;
+                    if (b > 0 && b < a.num_blocks && !tail) set_error(kErrBadEntry);
                 }
             }
             a.forks[i + lane] = r;
@@ -287,7 +290,11 @@ fork_plan_kernel(const ForkArgs a) {
         const bool hit = b > 0 && b < b1 && a.ref_counts[b] <= 0;
         const unsigned m = __ballot_sync(0xffffffffu, hit);
         const int r = rank + __popc(m & lanes_below(lane));
-        if (hit && r < sn.total) a.free_ids[r] = (int)b;
+        if (hit && r < sn.total) {
+            // counted here, before any entry that names it adds to its count
+            a.free_ids[r] = (int)b;
+            a.ref_counts[b] = 1;
+        }
         rank += __popc(m);
     }
     cl.sync();      // no CTA leaves while another may still read its counts
@@ -312,9 +319,7 @@ fork_apply_kernel(const __grid_constant__ PoolSet pools, const ForkArgs a, int w
             int b = a.block_tables[(int64_t)f.x * a.max_blocks + j];
             if (j == full && f.z >= 0) b = a.free_ids[f.z];
             a.block_tables[(int64_t)c * a.max_blocks + j] = b;
-            if (j == full && f.z >= 0) {
-                a.ref_counts[b] = 1;
-            } else if (b != 0) {
+            if (b != 0 && !(j == full && f.z >= 0)) {       // the plan has counted a new block
                 if (b < 0 || b >= a.num_blocks || atomicAdd(a.ref_counts + b, 1) <= 0)
                     set_error(kErrBadEntry);    // passed on all the same
             }
