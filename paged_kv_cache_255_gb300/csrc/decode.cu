@@ -48,6 +48,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "shared.h"
+#include "shared_records.h"
 #include "tcgen05.cuh"
 
 namespace pa {
@@ -917,10 +918,10 @@ __device__ __forceinline__ void decode_body(const DecodeArgs &a, const SharedArg
                 part = cc.u.part != 0;
                 if (piece_j0 == 0 && lane == 0) {
                     // how the combine finds the unit: {first slot, last share,
-                    // first share}; slot -1: whole in whole_o, -2: nothing left
+                    // first share} (shared_records.h)
                     const int64_t unit_end_T = T - cc.j + cc.nt;
                     sh.units[(int64_t)cc.v * a.num_kv_heads + cc.kvh] =
-                        unit_end ? make_int4(part ? -1 : -2, w, w, 0)
+                        unit_end ? make_int4(part ? kRecordWhole : kRecordDone, w, w, 0)
                                  : make_int4(2 * w + (piece == 0 ? 0 : 1),
                                              (int)((unit_end_T * p_eff - 1) / W), w, 0);
                 }
@@ -1125,22 +1126,17 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
     const bool mine = row < rows && h < a.cols && s >= s_lo && s < s_hi;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     // where the own part is, the prefix's in decode_shared_kernel, and in shared.cu
-    int4 u = make_int4(-2, 0, 0, 0), x = make_int4(0, -1, 0, 0), y = make_int4(0, 0, 0, 0);
+    int4 u = make_int4(kRecordDone, 0, 0, 0), x = make_int4(0, -1, 0, 0), y = make_int4(0, 0, 0, 0);
     if (mine) {
         u = sh.units[(int64_t)(s - s_lo) * Hkv + kvh];
         if (q.y >= 0) x = sh.units[(int64_t)q.y * Hkv + kvh];
         if (q.x >= 0) y = sh.parts[q.x + kvh * q.w];
     }
-    // A record is not there when the share that owed it gave up waiting for its
-    // tiles (the launch's outputs are undefined then): never an address from one.
-    auto sane = [&](const int4 v) {
-        return v.x >= -2 && v.x < 2 * a.num_workers && v.z >= 0 && v.z <= v.y && v.y < a.num_workers &&
-               (v.x < 0 || v.x >> 1 == v.z);
-    };
-    const bool sane_y = y.x >= 0 && y.y >= 0 && y.y <= sh.max_workers && y.z >= 0 && y.z <= 2 * sh.max_workers &&
-                        (y.x | 1) + (int64_t)(y.y - 1) * y.z < 2 * sh.max_workers;
-    // else not covered, or written by the share that computed it
-    const bool todo = u.x != -2 && sane(u) && sane_y && (q.y < 0 || sane(x));
+    // else not covered, or written by the share that computed it; a record that a
+    // share still owes is never an address (shared_records.h)
+    const bool todo = u.x != kRecordDone && unit_record_ok(u, a.num_workers, true) &&
+                      prefix_record_ok(y, sh.max_workers) &&
+                      (q.y < 0 || unit_record_ok(x, a.num_workers, false));
     // the parts in the order of their keys; a batch's loads are all in flight
     // before its merge
     const int n_packed = 1 + x.y - x.z, n_prefix = n_packed + y.y;
@@ -1158,18 +1154,13 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
             if (i >= n) break;
             const float4 *from;         // this thread's words: from[0], from[step]
             int64_t step = 16;
-            // a share's first piece is where its record says, the next shares' at
-            // their even slots
-            auto slot_of = [](int first, int at, int apart) {
-                return (int64_t)(at == 0 ? first : (first & ~1) + at * apart);
-            };
             if (i >= n_packed && i < n_prefix) {
                 if (y.y == 1) {
                     from = sh.unit_o + ((int64_t)kvh * 32 + word) * rows + row;
                     step = 16 * rows;
                     e[k] = sh.unit_ml[kvh * rows + row];
                 } else {
-                    const int64_t slot = slot_of(y.x, i - n_packed, y.z);
+                    const int64_t slot = record_slot(y.x, i - n_packed, y.z);
                     from = sh.part_o + (slot * 32 + word) * kPairRows + q.z + h;
                     step = 16 * kPairRows;
                     e[k] = sh.part_ml[slot * kPairRows + q.z + h];
@@ -1177,12 +1168,12 @@ combine_shared_kernel(const DecodeArgs a, const SharedArgs sh) {
             } else {
                 const bool own = i >= n_prefix;
                 const int first = own ? u.x : x.x;
-                if (first == -1) {
+                if (first == kRecordWhole) {
                     const int64_t whole = out_row() + (own ? 0 : (int64_t)a.num_seqs * a.num_q_heads);
                     from = sh.whole_o + whole * 32 + word;
                     e[k] = sh.whole_ml[whole];
                 } else {
-                    const int64_t slot = slot_of(first, own ? i - n_prefix : i, 2) * COLS + (own ? h : q.z + h);
+                    const int64_t slot = record_slot(first, own ? i - n_prefix : i, 2) * COLS + (own ? h : q.z + h);
                     from = slots + slot * 32 + word;
                     e[k] = slots_ml[slot];
                 }
