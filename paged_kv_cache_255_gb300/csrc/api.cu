@@ -540,6 +540,7 @@ pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_c
     const int64_t pairs = (int64_t)num_seqs * gp / pa::kPairRows + num_groups;
     sh.tensor = (num_seqs + pa::shared_fit(a.group) - 1) / pa::shared_fit(a.group) > 1 &&
                 key_tiles <= INT32_MAX / num_kv_heads / pairs && a.scale_log2 > 0.f && sms > 1 ? 1 : 0;
+    sh.fault_hold_v = pa::prefill_fault();
     pa::shared_carve_workspace(sh, static_cast<char *>(workspace) + dec, a);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = pa::launch_shared_prefix(a, sh, st);

@@ -98,10 +98,11 @@ struct PrefillArgs {
     float scale_log2;
 };
 
-// Test hook for the bounded waits of the tcgen05 prefill kernel: with mode 1
-// its V producer leaves the first tile's v_full barrier without its arrival,
-// so the MMA warp's wait for it runs out (about 2 s), the kernel records error
-// 2 and every warp exits. Mode 0 (the default) turns it off.
+// Test hook for the bounded waits of the tcgen05 kernels (prefill, and the prefix
+// kernel of decode over shared prefixes): with mode 1 their V producer leaves
+// the first tile's v_full barrier without its arrival, so the MMA warp's wait
+// for it runs out (about 2 s), the kernel records error 2 and every warp exits.
+// Mode 0 (the default) turns it off.
 void set_prefill_fault(int mode);
 int prefill_fault();
 

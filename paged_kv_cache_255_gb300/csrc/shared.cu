@@ -53,7 +53,8 @@
 //                    queries
 //   warp 10          issues S = Q K^T and O += P V as their inputs arrive
 // Hand-offs are mbarriers; every wait is bounded (about 2 s), and a wait that
-// ran out makes every role skip to the end, where the CTA frees its TMEM.
+// ran out makes every role skip to its end. A role ends when what it has in
+// flight has landed (or 0.1 s later); then the CTA frees its TMEM.
 #include <climits>
 #include <cmath>
 
@@ -98,7 +99,8 @@ constexpr uint32_t kBarSFull = kBarVEmpty + kVStages;    // + query tile (A 0, B
 constexpr uint32_t kBarPReady = kBarSFull + 2;
 constexpr uint32_t kBarPVDone = kBarPReady + 2;
 constexpr uint32_t kBarOFree = kBarPVDone + 2;
-constexpr uint32_t kNumBars = kBarOFree + 2;
+constexpr uint32_t kBarDrain = kBarOFree + 2;            // all products issued are done
+constexpr uint32_t kNumBars = kBarDrain + 1;
 constexpr uint32_t kOffTmemSlot = kOffCtl + 8 * kNumBars;
 constexpr uint32_t kOffAbort = kOffTmemSlot + 4;
 constexpr uint32_t kWalkBytes = 80;
@@ -134,6 +136,21 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
             return false;
         }
     }
+}
+
+// Bounded wait for the last of what a role has in flight, so that nothing lands in
+// the CTA's shared or tensor memory once it is another's. It goes on when the
+// launch has given up: copies and products end by themselves, in microseconds.
+__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
+    if ((threadIdx.x & 31) == 0 && !tc::mbar_try_wait(bar, parity)) {
+        const uint64_t t0 = tc::globaltimer_ns();
+        while (!tc::mbar_try_wait_sleep(bar, parity, 100000u))
+            if (tc::globaltimer_ns() - t0 > 100000000ull) {
+                set_error(kErrTimeout);
+                break;
+            }
+    }
+    __syncwarp();
 }
 
 // One lane waits for the warp; with `spin` the whole warp polls first (a
@@ -562,6 +579,7 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
             tc::mbar_init(bar(kBarPVDone + i), 1);
             tc::mbar_init(bar(kBarOFree + i), kRows / 32);
         }
+        tc::mbar_init(bar(kBarDrain), 1);
         *abort = 0;
         tc::fence_mbar_init();
     }
@@ -719,8 +737,8 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
         const uint32_t bar_full = bar(is_v ? kBarVFull : kBarKFull);
         const uint32_t bar_empty = bar(is_v ? kBarVEmpty : kBarKEmpty);
         const uint32_t base = sbase + (is_v ? kOffV : kOffK);
-        uint32_t gt = 0;
-        int piece = 0;
+        uint32_t gt = 0;                            // tiles issued
+        int piece = 0, queries = 0;                 // pieces begun; pieces whose queries are issued
         bool ok = true;
 #pragma unroll 1
         do {
@@ -735,6 +753,7 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
                                             w.kvh * a.group, w.gr.s0 + w.pair * 2 * BT + t * BT, bar(kBarQFull));
                 }
                 warp_arrive(bar(kBarQFull));
+                ++queries;
                 if (lane == 0 && w.j0 == 0) {
                     // how the combine finds the unit: the shares from this one to the
                     // one of the unit's last key tile
@@ -768,20 +787,24 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
             for (int j = w.j0; j < w.j1; ++j) {
                 const int2 at = box_next;
                 box_next = box_at(j + 1);
-                const uint32_t gj = gt + (j - w.j0);
-                const int st = gj % nst;
-                if (!warp_wait(bar_empty + 8 * st, ((gj / nst) & 1) ^ 1, abort)) { ok = false; break; }
+                const int st = gt % nst;
+                if (!warp_wait(bar_empty + 8 * st, ((gt / nst) & 1) ^ 1, abort)) { ok = false; break; }
                 const uint32_t full = bar_full + 8 * st;
                 const int n = __popc(__ballot_sync(0xffffffffu, at.x != INT_MIN));
                 if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)(n * box * 128));
                 __syncwarp();
                 if (at.x != INT_MIN)
                     tc::tma_load_3d(base + st * kKVBytes + h * kKVHalf + q * box * 128, map, h * 64, at.x, at.y, full);
-                warp_arrive(full);
+                // the test hook holds back one V arrival (set_prefill_fault)
+                if (!(is_v && sh.fault_hold_v && gt == 0)) warp_arrive(full);
+                ++gt;
             }
-            gt += w.j1 - w.j0;
             ++piece;
         } while (ok && walk_next(w, sh, a.num_kv_heads));
+        // the last fill of every stage, and the last queries, have landed
+        for (uint32_t g = gt > (uint32_t)nst ? gt - nst : 0; g < gt; ++g)
+            drain_bar(bar_full + 8 * (g % nst), (g / nst) & 1);
+        if (queries > 0) drain_bar(bar(kBarQFull), (queries - 1) & 1);
     } else if (warp == kMmaWarp) {
         // ---------------- MMA issue ----------------
         const uint64_t dq = tc::sw128_desc(sbase + kOffQ, 16, 1024);        // K-major
@@ -877,16 +900,19 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
                 }
             }
             // the queries' buffers are free once this piece's MMAs are done
-            if (tc::elect_one()) tc::commit(bar(kBarQEmpty));
+            if (ok && tc::elect_one()) tc::commit(bar(kBarQEmpty));
             __syncwarp();
             gt += nt;
             gq0 += nt;
             gq1 += two ? nt : 0;
             ++piece;
         } while (ok && walk_next(w, sh, a.num_kv_heads));
+        if (tc::elect_one()) tc::commit(bar(kBarDrain));
+        __syncwarp();
+        drain_bar(bar(kBarDrain), 0);
     }
 
-    // teardown: every role is done (or has given up); TMEM is freed
+    // teardown: every role is done (or has given up) and has nothing in flight; TMEM is freed
     tc::fence_before_sync();
     __syncthreads();
     if (warp == kMmaWarp) {

@@ -76,6 +76,7 @@ struct SharedArgs {
     int max_workers;                // CTAs of the prefix kernel
     int box_tokens;                 // tokens of a TMA box of the prefix kernel: min(block size, 128)
     int tensor;                     // whether the prefix kernel is launched
+    int fault_hold_v;               // test hook, normally 0: see set_prefill_fault
     // in the workspace
     SharedHeader *hdr;
     int4 *seq;                      // [S] {unit of KV head 0 or -1, entry of its packed prefix or -1,

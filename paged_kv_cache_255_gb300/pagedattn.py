@@ -626,9 +626,9 @@ def take_device_error(stream=None, device=None) -> int:
 
 
 def debug_prefill_fault(mode: int) -> None:
-    """Test hook (off by default): mode 1 makes later prefill launches hold back
-    one barrier arrival so that a bounded wait runs out and code 2 is recorded;
-    mode 0 turns it off."""
+    """Test hook (off by default): mode 1 makes later prefill launches, and the
+    prefix kernel of later decode_shared calls, hold back one barrier arrival so
+    that a bounded wait runs out and code 2 is recorded; mode 0 turns it off."""
     _check("pa_debug_prefill_fault", lib().pa_debug_prefill_fault(int(mode)))
 
 
