@@ -56,7 +56,8 @@
 // k_empty and v_empty; the softmax warps arrive on p_ready once P is in TMEM
 // (and O rescaled), and on o_free once the epilogue has read O. Every wait is
 // bounded (about 2 s) and also gives up once any thread of the CTA has
-// recorded a failed wait; then every role skips to the end, where the CTA
+// recorded a failed wait; then every role skips to its end, waits (0.1 s at most)
+// for what it has in flight, and the CTA
 // frees its TMEM and exits.
 #include <atomic>
 #include <climits>
@@ -109,7 +110,8 @@ constexpr uint32_t kBarOFree = kBarPVDone + 2;
 constexpr uint32_t kBarUnitFull = kBarOFree + 2;         // + unit ring slot
 constexpr uint32_t kBarUnitEmpty = kBarUnitFull + 2;     // + unit ring slot
 constexpr uint32_t kBarClc = kBarUnitEmpty + 2;          // launch-control responses
-constexpr uint32_t kNumBars = kBarClc + 1;
+constexpr uint32_t kBarDrain = kBarClc + 1;              // all products issued are done
+constexpr uint32_t kNumBars = kBarDrain + 1;
 constexpr uint32_t kOffTmemSlot = kOffCtl + 8 * kNumBars;
 constexpr uint32_t kOffAbort = kOffTmemSlot + 4;
 // heavy-first sequence order (up to kRankMaxSeqs sequences): their lengths,
@@ -146,6 +148,11 @@ __device__ __forceinline__ float fmin3(float a, float b, float c) {
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+
+// Nothing a role has issued outlives it.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+    if (!tc::drain_bar(bar, parity)) set_error(kErrTimeout);
 }
 
 // Bounded wait that also gives up once the CTA's abort flag is set.
@@ -435,6 +442,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap tmap_
             tc::mbar_init(bar(kBarUnitEmpty + i), kUnitReaders);
         }
         tc::mbar_init(bar(kBarClc), 1);
+        tc::mbar_init(bar(kBarDrain), 1);
         *abort = 0;
         tc::fence_mbar_init();
         mbar_arrive(bar(kBarUnitFull));         // unit 0 (this CTA's own cell) is published
@@ -627,8 +635,8 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap tmap_
         const uint32_t bar_full = bar(is_v ? kBarVFull : kBarKFull);
         const uint32_t bar_empty = bar(is_v ? kBarVEmpty : kBarKEmpty);
         const uint32_t base = sbase + (is_v ? kOffV : kOffK);
-        uint32_t gt = 0;
-        uint32_t clc_n = 0;                     // launch-control requests made (K warp)
+        uint32_t gt = 0, filled = 0;            // tiles before this item, and issued
+        uint32_t clc_n = 0, clc_asked = 0;      // launch-control requests answered, and made (K warp)
         int qitem = 0;                          // items whose Q the V warp has loaded
         bool clc_done = false;                  // a request found no CTA left to take
         bool ok = true;
@@ -695,6 +703,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap tmap_
                 // (test hook: the first tile's V arrival held back, see
                 // set_prefill_fault)
                 if (!(is_v && a.fault_hold_v && gj == 0)) warp_arrive(full);
+                filled = gj + 1;
             }
             gt += it.nt;
         }
@@ -717,6 +726,7 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap tmap_
                 mbar_arrive_expect_tx(bar(kBarClc), 16);
                 clc_try_cancel(sbase + kOffClcResp, bar(kBarClc));
             }
+            ++clc_asked;
             if (!warp_wait(bar(kBarClc), clc_n & 1, abort)) { ok = false; break; }
             ++clc_n;
             int cx, cy, cz;
@@ -736,6 +746,11 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap tmap_
         if (lane == 0) units[(k + 1) & 1] = nx;
         warp_arrive(bar(kBarUnitFull + ((k + 1) & 1)));
         }
+        // the last fill of every stage, the last queries and the last answer have landed
+        for (uint32_t j = filled > (uint32_t)nst ? filled - nst : 0; j < filled; ++j)
+            drain(bar_full + 8 * (j % nst), (j / nst) & 1);
+        if (qitem > 0) drain(bar(kBarQFull), (qitem - 1) & 1);
+        if (clc_asked > clc_n) drain(bar(kBarClc), clc_n & 1);
     } else if (warp == kMmaWarp) {
         // ---------------- MMA issue ----------------
         // The whole warp runs the issue loop, converged, so that barrier
@@ -884,9 +899,12 @@ prefill_tc_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap tmap_
         }
         if (ok) warp_arrive(bar(kBarUnitEmpty + (k & 1)));
         }
+        if (tc::elect_one()) tc::commit(bar(kBarDrain));
+        __syncwarp();
+        drain(bar(kBarDrain), 0);
     }
 
-    // teardown: every role is done (or has given up); TMEM is freed
+    // teardown: every role is done (or has given up) and has nothing in flight; TMEM is freed
     tc::fence_before_sync();
     __syncthreads();
     if (warp == kMmaWarp) {

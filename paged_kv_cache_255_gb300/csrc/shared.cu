@@ -138,19 +138,9 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
 }
 
-// Bounded wait for the last of what a role has in flight, so that nothing lands in
-// the CTA's shared or tensor memory once it is another's. It goes on when the
-// launch has given up: copies and products end by themselves, in microseconds.
-__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
-    if ((threadIdx.x & 31) == 0 && !tc::mbar_try_wait(bar, parity)) {
-        const uint64_t t0 = tc::globaltimer_ns();
-        while (!tc::mbar_try_wait_sleep(bar, parity, 100000u))
-            if (tc::globaltimer_ns() - t0 > 100000000ull) {
-                set_error(kErrTimeout);
-                break;
-            }
-    }
-    __syncwarp();
+// Nothing a role has issued outlives it.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+    if (!tc::drain_bar(bar, parity)) set_error(kErrTimeout);
 }
 
 // One lane waits for the warp; with `spin` the whole warp polls first (a
@@ -803,8 +793,8 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
         } while (ok && walk_next(w, sh, a.num_kv_heads));
         // the last fill of every stage, and the last queries, have landed
         for (uint32_t g = gt > (uint32_t)nst ? gt - nst : 0; g < gt; ++g)
-            drain_bar(bar_full + 8 * (g % nst), (g / nst) & 1);
-        if (queries > 0) drain_bar(bar(kBarQFull), (queries - 1) & 1);
+            drain(bar_full + 8 * (g % nst), (g / nst) & 1);
+        if (queries > 0) drain(bar(kBarQFull), (queries - 1) & 1);
     } else if (warp == kMmaWarp) {
         // ---------------- MMA issue ----------------
         const uint64_t dq = tc::sw128_desc(sbase + kOffQ, 16, 1024);        // K-major
@@ -909,7 +899,7 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
         } while (ok && walk_next(w, sh, a.num_kv_heads));
         if (tc::elect_one()) tc::commit(bar(kBarDrain));
         __syncwarp();
-        drain_bar(bar(kBarDrain), 0);
+        drain(bar(kBarDrain), 0);
     }
 
     // teardown: every role is done (or has given up) and has nothing in flight; TMEM is freed

@@ -189,6 +189,19 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
     asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(t));
     return t;
 }
+// A warp's bounded wait (0.1 s) for the last of what its role has in flight, so
+// that nothing lands in the CTA's shared or tensor memory once it is another's.
+// It is made also when the launch has given up: copies and products end by
+// themselves, in microseconds. False when it ran out.
+__device__ __forceinline__ bool drain_bar(uint32_t bar, uint32_t parity) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0 && !mbar_try_wait(bar, parity)) {
+        const uint64_t t0 = globaltimer_ns();
+        while (ok && !mbar_try_wait_sleep(bar, parity, 100000u)) ok = globaltimer_ns() - t0 <= 100000000ull;
+    }
+    __syncwarp();
+    return ok;
+}
 // -- TMA ------------------------------------------------------------------------
 // The next phase of `bar` also waits for `bytes` more bytes of asynchronous
 // copies (no arrival).
