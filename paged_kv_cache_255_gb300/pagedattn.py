@@ -361,7 +361,9 @@ def decode_shared(q, k_cache, v_cache, block_tables, context_lens, group_starts,
 def decode_shared_workspace_size(num_seqs: int, num_groups: int, num_q_heads: int, num_kv_heads: int,
                                  head_dim: int = 128, device=None) -> int:
     """Workspace bytes pa_decode_shared needs on ``device`` (default: current)."""
-    index = torch.cuda.current_device() if device is None else torch.device(device).index
+    index = None if device is None else torch.device(device).index
+    if index is None:       # no device, or "cuda": the current one
+        index = torch.cuda.current_device()
     n = _size("pa_decode_shared_workspace_size", index, num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim)
     if n == 0:
         raise ValueError("unsupported head configuration or number of groups")
@@ -507,16 +509,23 @@ def _scratch(kind, nbytes, dev, stream):
 
 
 _sizes = {}
+_MOST_SIZES = 4096
 
 
 def _size(fn, index, *args):
     """The library's answer to a workspace size question, asked once for the
-    same sizes on the same device."""
+    same sizes on the same device (0, for sizes it does not take or after an
+    error of the driver, every time). A serving loop asks for many sizes: the
+    answers kept are thrown away when there are _MOST_SIZES."""
     key = (fn, index, args)
     n = _sizes.get(key)
     if n is None:
         with torch.cuda.device(index):
-            n = _sizes[key] = int(getattr(lib(), fn)(*args))
+            n = int(getattr(lib(), fn)(*args))
+        if n:
+            if len(_sizes) >= _MOST_SIZES:
+                _sizes.clear()
+            _sizes[key] = n
     return n
 
 
