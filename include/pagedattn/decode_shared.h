@@ -36,7 +36,8 @@ extern "C" {
  * Values of group_starts are clamped to [0, num_seqs] and prefixes to the
  * table's width; a group_starts that decreases gives unspecified results within
  * the buffers. Requirements: pa_decode's; num_groups at most 4096, num_seqs and
- * num_kv_heads at most 65535; pools in either layout; a workspace of
+ * num_kv_heads at most 65535; tables of at most 2^31 - 128 tokens
+ * (max_blocks_per_seq * block_size); pools in either layout; a workspace of
  * pa_decode_shared_workspace_size(num_seqs, num_groups, ...) bytes, 16-byte
  * aligned. Results do not depend on timing.
  */

@@ -508,6 +508,8 @@ pa_status_t pa_decode_shared(const void *q, const void *k_cache, const void *v_c
     if (chk != PA_OK) return chk;
     if (num_groups > pa::kSharedMaxGroups || num_seqs > 65535 || num_kv_heads > 65535)
         return PA_ERR_UNSUPPORTED;
+    // tokens are counted in 32 bits, rounded up to tiles of 128
+    if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX - 127) return PA_ERR_UNSUPPORTED;
     if (nothing_to_do || num_groups == 0) return PA_OK;
     if (!group_starts || !prefix_blocks) return PA_ERR_INVALID_ARG;
     const int gp = pa::decode_group_pad(num_q_heads / num_kv_heads);
