@@ -27,11 +27,21 @@ extern "C" {
  * and prefixes of 0 blocks are plain decode. Both arrays lie on the device, so a
  * captured call follows their contents.
  *
- * For every sequence of a group the result is pa_decode's: the same sum over
- * the same tokens t < context_lens[s], in fp32 from the bf16 inputs, rounded to
- * bf16, in another order. Sequences outside all groups (before group_starts[0],
- * or from group_starts[num_groups] on: the padding of a batch of fixed size)
- * are neither read nor written.
+ * What is computed together ends at the shortest non-empty sequence of a group,
+ * rounded down to 16 tokens: one that is much shorter than the prefix makes all
+ * the others read the rest of it by themselves. Give such a sequence a group of
+ * its own. The call plans on the device, which takes a few microseconds: a batch
+ * with few sequences a group and short prefixes is faster through pa_decode.
+ *
+ * For every sequence of a group the result is pa_decode's: the sum over the same
+ * tokens t < context_lens[s], from the bf16 inputs, rounded to bf16, in another
+ * order. Scores, running maxima, sums and outputs are held in fp32; as in
+ * pa_decode the softmax weights are rounded to bf16 for the product with V. The
+ * sum of the weights is of the rounded ones where a sequence reads its tokens by
+ * itself or with a few others, and of the exact ones where a prefix is computed
+ * for many. Sequences outside all groups (before group_starts[0], or from
+ * group_starts[num_groups] on: the padding of a batch of fixed size) are not
+ * written, and nothing of them enters a result.
  *
  * Values of group_starts are clamped to [0, num_seqs] and prefixes to the
  * table's width; a group_starts that decreases gives unspecified results within

@@ -19,11 +19,12 @@
 //          programmatic dependent of the plan and waits for its results.
 // Block data moves in units of 4 KB (16 rows of 256 bytes: every block is a
 // multiple of that), one warp per unit with all eight 16-byte loads of a lane
-// in flight before its stores. Large calls are bound by HBM: 2047 blocks of
-// 32 KB copied in 8 pools take 147 us (7.3 TB/s read and written), a pool of
-// 4096 such blocks, half of them live, compacted in 89 us (6.0 TB/s); small
-// ones by their launches: two blocks copied in 2.2 us, a pool of 128 compacted
-// in 6.7 us.
+// in flight before its stores. Large calls are bound by HBM: 1819 blocks of
+// 32 KB copied in 8 pools (of 2047 pairs, the others unused) take 148 us (6.5 TB/s
+// read and written), a pool of 4096 such blocks, half of them live, is compacted
+// in 89 us (6.0 TB/s); small ones by their launches: two blocks copied in
+// 2.1 us, a pool of 128 compacted in 7.4 us. These and the times below are of a
+// call within a graph of 20: the device's, without the host's.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -162,9 +163,10 @@ copy_blocks_kernel(const __grid_constant__ PoolSet pools, const int2 *pairs, int
 // -- free -----------------------------------------------------------------------
 //
 // Bound by its chain of dependent reads (row, length, entries, counts), and
-// with many rows by the atomics on counts of far-apart blocks: 4 rows of 64 ..
-// 1024 tokens take 3.7 us, 255 rows of 512 .. 16384 tokens (134800 blocks of
-// 16) 11.3 us, both with the copy that restores the tables between passes.
+// with many rows by the atomics on counts of far-apart blocks, one entry a thread
+// in flight: 4 rows of 64 .. 1024 tokens take 3.5 us, 255 rows of 512 .. 16384 tokens
+// (134800 blocks of 16) 12.0 us, both with the copy that restores the tables
+// between passes.
 
 // One reference to block b less. False when there was none to give up: the
 // count is put back, so it ends at 0 however many such calls there were.
@@ -328,7 +330,7 @@ fork_apply_kernel(const __grid_constant__ PoolSet pools, const ForkArgs a, int w
     // The used rows of each parent's last block, into the child's new one: one
     // run in a token-major pool, one per KV head in a head-major one. A CTA
     // takes a slice of kSliceParts parts of up to 4 KB of one fork's block in
-    // one pool. 256 forks of 16 parents, 8 pools, 512 KB blocks: 128.6 us, bound
+    // one pool. 256 forks of 16 parents, 8 pools, 512 KB blocks: 129 us, bound
     // by the writes of the new rows (569 MB at 4.4 TB/s; a parent's rows come from L2
     // after its first fork, 152 us when they were read past it). With a part per
     // warp and task, and a division for each of its chunks, it took 293 us.

@@ -1263,9 +1263,17 @@ struct Launcher {
     }
 };
 
-// The own tokens of a call over shared prefixes, then its combine. Tiles have
-// 8 columns (16 for groups above 8) whatever the group size: the 8 of a matrix instruction,
-// filled by several sequences where they share a prefix.
+// The own tokens of a call over shared prefixes, then its combine.
+//
+// A rule: decode_shared_kernel follows the prefix kernel directly, or behind kernels
+// that wait for what is before them, at their start or by being launched plainly, before
+// they let a dependent start. It reads the plan's results without a wait of its own: it may
+// start only when every CTA of the prefix kernel has waited for the plan (or has ended), and
+// reads them past L1. A kernel between the two that neither waits nor is
+// ordered would break that, and the order of the prefix's results before the combine with it.
+//
+// Tiles have 8 columns (16 for groups above 8) whatever the group size: the 8 of a matrix
+// instruction, filled by several sequences where they share a prefix.
 enum CombineShape { kFew, kSome, kMany };
 
 template <int GP, int COLS>

@@ -41,9 +41,10 @@
 // on an SM. 128 sequences x 64 heads over 2048 shared and 256 own tokens:
 // 39 to 44 us (pa_decode 86.5, the bytes alone 21.7), of which about 10 are the plan
 // and the launches up to the first loads and 5 the combine. 256 x 32 over 32768
-// shared and 16 .. 1000 own: 146 us (pa_decode 2198, the bytes alone 99); the 104
-// SMs of the prefix keep their tensor pipes 68 % busy, a pair of 128-key
-// products of both kinds taking 3230 cycles, the softmax of a tile 1275.
+// shared and 16 .. 1000 own: 144 us (pa_decode 2198, the bytes alone 99); the 104
+// SMs of the prefix keep their tensor pipes 66 % busy, a pair of 128-key products
+// of both kinds taking 3230 cycles, the softmax of a tile 1275. (Times of calls here
+// are of one within a graph of 20: the device's, without the host's.)
 //
 // Inside the prefix kernel (TMEM: S_A 0-127, O_A 128-255, S_B 256-383, O_B
 // 384-511 columns; P_t in bf16 over the first 64 columns of S_t):

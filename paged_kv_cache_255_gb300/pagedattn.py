@@ -321,9 +321,10 @@ def decode_shared(q, k_cache, v_cache, block_tables, context_lens, group_starts,
 
     group_starts: int32 [G + 1]; group g is sequences group_starts[g] ..
     group_starts[g + 1] - 1, whose first prefix_blocks[g] (int32 [G]) table
-    entries are the same. The prefix is read once per group; the results are
-    decode's, but for the order of the sums. Rows of ``out`` outside all groups
-    are left as they were. The other arguments are decode's."""
+    entries are the same. The prefix is read once per group, as far as the group's
+    shortest non-empty sequence reaches; the results are decode's, but for the
+    order of the sums. Rows of ``out`` outside all groups are left as they were.
+    The other arguments are decode's."""
     dev = q.device
     if not _fits(dev.index, torch.bfloat16, q, k_cache, v_cache):
         _explain(dev, torch.bfloat16, q=q, k_cache=k_cache, v_cache=v_cache)
@@ -498,7 +499,9 @@ def _scratch(kind, nbytes, dev, stream):
     stream run one after the other and share a buffer that is kept (an
     allocation costs as much as the rest of a short call); a call on another
     stream, and every captured call, gets one of its own from torch's allocator,
-    so calls that may run at the same time never share."""
+    so calls that may run at the same time never share. The largest of a kind is
+    kept until the thread ends (for decode_shared tens of MB and more:
+    decode_shared_workspace_size); a caller that passes a workspace keeps none here."""
     if stream is not None or torch._C._cuda_isCurrentStreamCapturing():
         return _new(nbytes, torch.uint8, dev, stream)
     key = (kind, dev.index, _raw_stream(dev.index))
