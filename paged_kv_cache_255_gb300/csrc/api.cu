@@ -9,7 +9,9 @@
 #include "../../include/pagedattn.h"
 #include "../../include/pagedattn/blocks.h"
 #include "../../include/pagedattn/decode_shared.h"
+#include "../../include/pagedattn/rotary.h"
 #include "kernels.h"
+#include "rotary.h"
 #include "shared.h"
 
 namespace {
@@ -264,6 +266,67 @@ pa_status_t check_workspace(const void *workspace, size_t workspace_bytes, int n
     const bool ok = workspace && aligned16(workspace) &&
                     workspace_bytes >= pa::blocks_workspace_bytes(num_rows, num_blocks);
     return ok ? PA_OK : PA_ERR_WORKSPACE;
+}
+
+// Rows of `heads` heads of `tokens` tokens: address, and the strides that are used.
+bool rows_ok(const void *p, int64_t tokens, int64_t token, int heads, int64_t head) {
+    auto ok = [](int64_t n, int64_t stride) { return n <= 1 || (stride >= 0 && stride % 8 == 0); };
+    return p && aligned16(p) && ok(tokens, token) && ok(heads, head);
+}
+
+// Whether no two rows of an output overlap.
+bool rows_apart(int64_t tokens, int64_t token, int heads, int64_t head) {
+    const int64_t D = pa::kHeadDimPublic;
+    if (tokens <= 1) return heads <= 1 || head >= D;
+    if (heads <= 1) return token >= D;
+    const bool heads_inside = head <= token;
+    const int64_t in = heads_inside ? head : token, out = heads_inside ? token : head;
+    const int64_t n = heads_inside ? heads : tokens;
+    return in >= D && (out - D) / in >= n - 1;      // out >= (n - 1) in + D
+}
+
+// What pa_rotate and pa_append_kvcache check alike, and the arguments of a launch.
+pa_status_t rotate_args(pa::RotateArgs &a, bool *interleaved, const void *q, int64_t q_token,
+                        int64_t q_head, void *q_out, int64_t qo_token, int64_t qo_head,
+                        int num_q_heads, const void *k, int64_t k_token, int64_t k_head,
+                        int num_kv_heads, int head_dim, const int32_t *positions,
+                        int64_t num_tokens, const pa_rotary_t *rotary, const void *q_weight,
+                        const void *k_weight, float eps) {
+    if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads < 0 || !std::isfinite(eps) || eps < 0.f)
+        return PA_ERR_INVALID_ARG;
+    if (head_dim != pa::kHeadDimPublic) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)num_q_heads + num_kv_heads > (1 << 20)) return PA_ERR_UNSUPPORTED;
+    if (rotary) {
+        if (!std::isfinite(rotary->amplitude)) return PA_ERR_INVALID_ARG;
+        if (rotary->rot_dim < 16 || rotary->rot_dim > head_dim || rotary->rot_dim % 16 != 0)
+            return PA_ERR_UNSUPPORTED;
+    }
+    if (num_tokens == 0) return PA_OK;
+    if (rotary && !positions) return PA_ERR_INVALID_ARG;
+    if (num_q_heads > 0 && (!rows_ok(q, num_tokens, q_token, num_q_heads, q_head) ||
+                            !rows_ok(q_out, num_tokens, qo_token, num_q_heads, qo_head) ||
+                            !rows_apart(num_tokens, qo_token, num_q_heads, qo_head)))
+        return PA_ERR_INVALID_ARG;
+    if (num_kv_heads > 0 && !rows_ok(k, num_tokens, k_token, num_kv_heads, k_head)) return PA_ERR_INVALID_ARG;
+    if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)))
+        return PA_ERR_INVALID_ARG;
+    a.q = {static_cast<const uint4 *>(q), q_token / 8, q_head / 8};
+    a.k = {static_cast<const uint4 *>(k), k_token / 8, k_head / 8};
+    a.q_out = {static_cast<uint4 *>(q_out), qo_token / 8, qo_head / 8};
+    a.positions = rotary ? positions : nullptr;
+    a.q_weight = static_cast<const uint4 *>(q_weight);
+    a.k_weight = static_cast<const uint4 *>(k_weight);
+    a.num_tokens = num_tokens;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.eps = eps;
+    *interleaved = rotary && rotary->interleaved;
+    if (rotary) {
+        a.pairs = rotary->rot_dim / 2;
+        a.amplitude = rotary->amplitude;
+        for (int i = 0; i < a.pairs; ++i) a.turns[i] = rotary->turns[i];
+    }
+    return PA_OK;
 }
 
 }  // namespace
@@ -686,6 +749,95 @@ pa_status_t pa_compact_blocks(void *const *caches, int num_caches, int32_t *bloc
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+pa_status_t pa_rotary_init_frequencies(pa_rotary_t *rotary, int rot_dim, int interleaved,
+                                       const double *frequencies, double amplitude) {
+    if (!rotary || !frequencies || (interleaved != 0 && interleaved != 1)) return PA_ERR_INVALID_ARG;
+    if (rot_dim < 16 || rot_dim > 2 * PA_ROTARY_MAX_PAIRS || rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+    if (!std::isfinite((float)amplitude)) return PA_ERR_INVALID_ARG;
+    for (int i = 0; i < rot_dim / 2; ++i)
+        if (!(std::fabs(frequencies[i]) <= 1048576.0)) return PA_ERR_INVALID_ARG;
+    pa::rotary_fill(rotary, rot_dim, interleaved, frequencies, amplitude);
+    return PA_OK;
+}
+
+pa_status_t pa_rotary_init(pa_rotary_t *rotary, int rot_dim, int interleaved, double base,
+                           pa_rotary_scaling_t scaling, double factor, double original_context,
+                           double low, double high, double amplitude) {
+    if (!(std::isfinite(base) && base > 1) || scaling < PA_ROTARY_PLAIN || scaling > PA_ROTARY_BANDED)
+        return PA_ERR_INVALID_ARG;
+    if (scaling != PA_ROTARY_PLAIN && !(std::isfinite(factor) && factor >= 1)) return PA_ERR_INVALID_ARG;
+    if (scaling == PA_ROTARY_YARN || scaling == PA_ROTARY_BANDED) {
+        if (!(std::isfinite(original_context) && original_context >= 1)) return PA_ERR_INVALID_ARG;
+        if (!(low > 0 && std::isfinite(high) && low < high)) return PA_ERR_INVALID_ARG;
+    }
+    if (rot_dim < 16 || rot_dim > 2 * PA_ROTARY_MAX_PAIRS || rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+    double radians[PA_ROTARY_MAX_PAIRS];
+    pa::rotary_scaled(radians, rot_dim, base, scaling, factor, original_context, low, high);
+    if (amplitude == 0) amplitude = scaling == PA_ROTARY_YARN ? 1 + 0.1 * std::log(factor) : 1;
+    return pa_rotary_init_frequencies(rotary, rot_dim, interleaved, radians, amplitude);
+}
+
+pa_status_t pa_rotate(const void *q, int64_t q_token_stride, int64_t q_head_stride, void *q_out,
+                      int64_t q_out_token_stride, int64_t q_out_head_stride, int num_q_heads,
+                      const void *k, int64_t k_token_stride, int64_t k_head_stride, void *k_out,
+                      int64_t k_out_token_stride, int64_t k_out_head_stride, int num_kv_heads,
+                      int head_dim, const int32_t *positions, int64_t num_tokens,
+                      const pa_rotary_t *rotary, const void *q_weight, const void *k_weight,
+                      float eps, void *stream) {
+    TraceRange r("pa_rotate");
+    pa::RotateArgs a{};
+    bool interleaved = false;
+    const pa_status_t chk = rotate_args(a, &interleaved, q, q_token_stride, q_head_stride, q_out,
+                                        q_out_token_stride, q_out_head_stride, num_q_heads, k,
+                                        k_token_stride, k_head_stride, num_kv_heads, head_dim,
+                                        positions, num_tokens, rotary, q_weight, k_weight, eps);
+    if (chk != PA_OK) return chk;
+    if (num_tokens == 0 || num_q_heads + num_kv_heads == 0) return PA_OK;
+    if (num_kv_heads > 0 && (!rows_ok(k_out, num_tokens, k_out_token_stride, num_kv_heads, k_out_head_stride) ||
+                             !rows_apart(num_tokens, k_out_token_stride, num_kv_heads, k_out_head_stride)))
+        return PA_ERR_INVALID_ARG;
+    a.k_out = {static_cast<uint4 *>(k_out), k_out_token_stride / 8, k_out_head_stride / 8};
+    const int sms = current_sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    const cudaError_t e = pa::launch_rotate(a, false, interleaved, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status_t pa_append_kvcache(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                              void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                              int num_q_heads, const void *k, int64_t k_token_stride,
+                              int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                              int64_t v_head_stride, int num_kv_heads, int head_dim, void *k_cache,
+                              void *v_cache, const int64_t *slot_mapping, int block_size,
+                              int64_t num_blocks, pa_layout_t layout, const int32_t *positions,
+                              int64_t num_tokens, const pa_rotary_t *rotary, const void *q_weight,
+                              const void *k_weight, float eps, void *stream) {
+    TraceRange r("pa_append_kvcache");
+    bool nothing_to_do = false;
+    pa_status_t chk = pa::store_check_args(k, v, k_cache, v_cache, slot_mapping, num_tokens,
+                                           num_kv_heads, head_dim, block_size, num_blocks, layout,
+                                           &nothing_to_do);
+    if (chk != PA_OK) return chk;
+    pa::RotateArgs a{};
+    bool interleaved = false;
+    chk = rotate_args(a, &interleaved, q, q_token_stride, q_head_stride, q_out, q_out_token_stride,
+                      q_out_head_stride, num_q_heads, k, k_token_stride, k_head_stride,
+                      num_kv_heads, head_dim, positions, num_tokens, rotary, q_weight, k_weight, eps);
+    if (chk != PA_OK || nothing_to_do) return chk;
+    if (!rows_ok(v, num_tokens, v_token_stride, num_kv_heads, v_head_stride)) return PA_ERR_INVALID_ARG;
+    a.v = {static_cast<const uint4 *>(v), v_token_stride / 8, v_head_stride / 8};
+    a.k_cache = static_cast<uint4 *>(k_cache);
+    a.v_cache = static_cast<uint4 *>(v_cache);
+    a.slots = slot_mapping;
+    a.num_slots = num_blocks * block_size;
+    a.block_size_log2 = log2_exact(block_size);
+    a.head_major = layout == PA_LAYOUT_HEAD_MAJOR ? 1 : 0;
+    const int sms = current_sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    const cudaError_t e = pa::launch_rotate(a, true, interleaved, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 pa_status_t pa_debug_kernel_variant(int flags) {
     if (flags & ~(PA_VARIANT_DECODE_SIMT | PA_VARIANT_PREFILL_MMA)) return PA_ERR_INVALID_ARG;
     g_kernel_variant.store(flags, std::memory_order_relaxed);
@@ -705,7 +857,7 @@ pa_status_t pa_take_device_error(int32_t *code, void *stream) {
     cudaError_t (*const take[])(cudaStream_t, int *) = {
         pa::take_prefill_error, pa::take_prefill_mma_error, pa::take_decode_error,
         pa::take_store_error,      pa::take_blocks_error,
-        pa::take_shared_error};
+        pa::take_shared_error, pa::take_rotary_error};
     int first = 0;
     for (auto f : take) {   // every word is read and cleared; the smallest code is reported
         int v = 0;

@@ -19,8 +19,8 @@ from . import build as _build
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = range(5)
 
 # every entry point the headers declare, with its ctypes signature
-_P, _I32, _I64, _F32, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
-                             ctypes.c_size_t)
+_P, _I32, _I64, _F32, _F64, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
+                                   ctypes.c_double, ctypes.c_size_t)
 SIGNATURES = {
     "pa_status_string": ([_I32], ctypes.c_char_p),
     "pa_store_kvcache": ([_P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _I64, _P], _I32),
@@ -57,6 +57,12 @@ SIGNATURES = {
     "pa_free_blocks": ([_P, _I32, _P, _I32, _P, _P, _I32, _I32, _I64, _P], _I32),
     "pa_compact_blocks": ([_P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I64, _P,
                            _SZ, _P], _I32),
+    "pa_rotary_init": ([_P, _I32, _I32, _F64, _I32, _F64, _F64, _F64, _F64, _F64], _I32),
+    "pa_rotary_init_frequencies": ([_P, _I32, _I32, _P, _F64], _I32),
+    "pa_rotate": ([_P, _I64, _I64, _P, _I64, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _P, _I64, _P,
+                   _P, _P, _F32, _P], _I32),
+    "pa_append_kvcache": ([_P, _I64, _I64, _P, _I64, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _P, _P,
+                           _P, _I32, _I64, _I32, _P, _I64, _P, _P, _P, _F32, _P], _I32),
     "pa_decode_multi_layout": ([_P, _P, _P, _P, _I32, _P, _I32, _F32, _P, _I32, _I32, _I32, _I32,
                                 _I32, _I64, _I32, _P, _SZ, _P], _I32),
 }
@@ -622,6 +628,159 @@ def compact_blocks(pools: CachePools, block_tables, context_lens, ref_counts, re
           num_live.data_ptr(), *pools._shape, workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
     return remap, num_live
+
+
+class _RotaryStruct(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 64)]
+
+
+class Rotary:
+    """The rotation of a head's first ``rot_dim`` of 128 dims by its position:
+    neighbouring pairs (``interleaved``) or pairs half of ``rot_dim`` apart, at
+    base^(-2 i / rot_dim) radians a token. Made once for a model.
+
+    ``scaling`` for contexts longer than the model was trained on
+    (``original_context`` tokens): "linear", "ntk", "yarn" or "banded", by
+    ``factor``; ``low`` and ``high`` are the turns in original_context between
+    which yarn (1, 32) and banded (1, 4) mix. ``amplitude`` multiplies the result;
+    None is the scaling's own. ``frequencies`` (rot_dim / 2 numbers, radians a
+    token) replace all of these."""
+
+    SCALINGS = (None, "linear", "ntk", "yarn", "banded")
+
+    def __init__(self, rot_dim: int = 128, base: float = 10000.0, interleaved: bool = False, scaling=None,
+                 factor: float = 1.0, original_context: float = 0.0, low=None, high=None, amplitude=None,
+                 frequencies=None):
+        self._struct = _RotaryStruct()
+        self._addr = ctypes.addressof(self._struct)
+        if frequencies is not None:
+            f = [float(x) for x in frequencies]
+            if len(f) != int(rot_dim) // 2:
+                raise ValueError("frequencies must be rot_dim / 2 numbers")
+            data = (ctypes.c_double * max(1, len(f)))(*f)
+            _check("pa_rotary_init_frequencies", lib().pa_rotary_init_frequencies(
+                self._addr, int(rot_dim), int(bool(interleaved)), ctypes.addressof(data),
+                1.0 if amplitude is None else float(amplitude)))
+            return
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"scaling must be one of {self.SCALINGS}")
+        if amplitude is not None and float(amplitude) == 0.0:
+            raise ValueError("amplitude must not be 0")
+        low = 1.0 if low is None else float(low)
+        high = (32.0 if scaling == "yarn" else 4.0) if high is None else float(high)
+        _check("pa_rotary_init", lib().pa_rotary_init(
+            self._addr, int(rot_dim), int(bool(interleaved)), float(base), self.SCALINGS.index(scaling),
+            float(factor), float(original_context), low, high, 0.0 if amplitude is None else float(amplitude)))
+
+    rot_dim = property(lambda self: self._struct.rot_dim)
+    interleaved = property(lambda self: bool(self._struct.interleaved))
+    amplitude = property(lambda self: self._struct.amplitude)
+
+
+def _heads(t, name, index, tokens):
+    """(address, token stride, head stride, heads) of rows [tokens, heads, 128]."""
+    try:
+        shape, (ts, hs, ds) = t.shape, t.stride()
+        if t.dtype is torch.bfloat16 and t.get_device() == index and shape[0] == tokens and shape[2] == 128 \
+                and ds == 1:
+            return t.data_ptr(), ts, hs, shape[1]
+    except (AttributeError, TypeError, ValueError):
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} must be a tensor on CUDA device {index}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    raise ValueError(f"{name} must be [{tokens}, heads, 128] with the dims of a head contiguous, got "
+                     f"{list(t.shape)} with strides {list(t.stride())}")
+
+
+_NO_HEADS = (None, 0, 0, 0)
+
+
+def _weight(w, name, dev):
+    if w is None:
+        return None
+    if not _fits(dev.index, torch.bfloat16, w) or w.shape != (128,):
+        _explain(dev, torch.bfloat16, **{name: w})
+        raise ValueError(f"{name} must be [128]")
+    return w.data_ptr()
+
+
+def _positions(positions, rotary, tokens, dev):
+    """(address of the rotation, address of the positions)"""
+    if rotary is None:
+        return None, None
+    if not _fits(dev.index, torch.int32, positions) or positions.shape != (tokens,):
+        _explain(dev, torch.int32, positions=positions)
+        raise ValueError("positions must be [tokens]")
+    return rotary._addr, positions.data_ptr()
+
+
+def _out_heads(x, out, name, rows, dev, tokens, stream):
+    """An output for the rows x ([T, H, 128], ``rows`` of _heads), and its own."""
+    if out is None:
+        out = _new(x.shape, x.dtype, dev, stream)
+        return out, (out.data_ptr(), rows[3] * 128, 128)
+    o = _heads(out, name, dev.index, tokens)
+    if o[3] != rows[3]:
+        raise ValueError(f"{name} must have its input's shape")
+    return out, o[:3]
+
+
+def rotate(q, k, positions, rotary, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None, k_out=None,
+           stream=None):
+    """The heads of queries and keys (bf16 [T, H, 128], any token and head stride
+    that is a multiple of 8) rotated by their tokens' positions (int32 [T]) after
+    the norm of each head's row where a weight (bf16 [128]) is given. Returns (q_out,
+    k_out); an output may be its input. q or k may be None, and so may ``rotary`` (a
+    Rotary; None: norms only, positions are not read)."""
+    x = q if q is not None else k
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("q or k must be a CUDA tensor")
+    dev, T = x.device, x.shape[0]
+    index = dev.index
+    qr = _heads(q, "q", index, T) if q is not None else _NO_HEADS
+    kr = _heads(k, "k", index, T) if k is not None else _NO_HEADS
+    rot, pos = _positions(positions, rotary, T, dev)
+    qo = ko = _NO_HEADS[:3]
+    if q is not None:
+        q_out, qo = _out_heads(q, q_out, "q_out", qr, dev, T, stream)
+    if k is not None:
+        k_out, ko = _out_heads(k, k_out, "k_out", kr, dev, T, stream)
+    _call("pa_rotate", dev, stream, qr[0], qr[1], qr[2], *qo, qr[3], kr[0], kr[1], kr[2], *ko, kr[3], 128, pos, T, rot,
+          _weight(q_weight, "q_weight", dev), _weight(k_weight, "k_weight", dev), float(eps))
+    return q_out, k_out
+
+
+def append_kvcache(q, k, v, k_cache, v_cache, slot_mapping, positions, rotary, q_weight=None, k_weight=None,
+                   eps: float = 1e-6, q_out=None, stream=None, head_major=False):
+    """A step's keys, rotated and normed as by rotate, and its values as they are,
+    into the slots of the pools (int64 [T], -1 rows skipped) as by store_kvcache; and
+    the queries, rotated and normed, into ``q_out``, which is returned. q, k, v may
+    be strided parts of one projection; q may be None."""
+    dev, T = k_cache.device, slot_mapping.shape[0]
+    index = dev.index
+    if not _fits(index, torch.bfloat16, k_cache, v_cache):
+        _explain(dev, torch.bfloat16, k_cache=k_cache, v_cache=v_cache)
+    if not _fits(index, torch.int64, slot_mapping):
+        _explain(dev, torch.int64, slot_mapping=slot_mapping)
+    qr = _heads(q, "q", index, T) if q is not None else _NO_HEADS
+    kr, vr = _heads(k, "k", index, T), _heads(v, "v", index, T)
+    if head_major:
+        NB, Hkv, bs, D = k_cache.shape
+    else:
+        NB, bs, Hkv, D = k_cache.shape
+    if v_cache.shape != k_cache.shape or kr[3] != Hkv or vr[3] != Hkv or D != 128 or slot_mapping.dim() != 1:
+        raise ValueError("shape mismatch between k, v, caches and slot_mapping")
+    rot, pos = _positions(positions, rotary, T, dev)
+    qo = _NO_HEADS[:3]
+    if q is not None:
+        q_out, qo = _out_heads(q, q_out, "q_out", qr, dev, T, stream)
+    _call("pa_append_kvcache", dev, stream, qr[0], qr[1], qr[2], *qo, qr[3], kr[0], kr[1], kr[2], vr[0], vr[1], vr[2],
+          Hkv, 128, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), bs, NB, 1 if head_major else 0,
+          pos, T, rot, _weight(q_weight, "q_weight", dev), _weight(k_weight, "k_weight", dev), float(eps))
+    return q_out
 
 
 def take_device_error(stream=None, device=None) -> int:
