@@ -9,10 +9,12 @@
 #include "../../include/pagedattn.h"
 #include "../../include/pagedattn/blocks.h"
 #include "../../include/pagedattn/decode_shared.h"
+#include "../../include/pagedattn/decode_tree.h"
 #include "../../include/pagedattn/rotary.h"
 #include "kernels.h"
 #include "rotary.h"
 #include "shared.h"
+#include "tree.h"
 
 namespace {
 
@@ -749,6 +751,101 @@ pa_status_t pa_compact_blocks(void *const *caches, int num_caches, int32_t *bloc
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+size_t pa_decode_tree_workspace_size(int num_q_heads, int num_kv_heads, int head_dim) {
+    if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+        head_dim != pa::kHeadDimPublic || pa::decode_group_pad(num_q_heads / num_kv_heads) == 0)
+        return 0;
+    const int sms = current_sm_count();
+    return sms > 0 ? pa::tree_workspace_bytes(sms) : 0;
+}
+
+pa_status_t pa_decode_tree(const void *q, const void *k_cache, const void *v_cache,
+                           const int32_t *block_tables, int max_blocks_per_seq,
+                           const int32_t *context_lens, const int32_t *query_start_loc,
+                           const uint64_t *tree_mask, int mask_words, float scale, void *out,
+                           int num_seqs, int total_q, int num_q_heads, int num_kv_heads,
+                           int head_dim, int block_size, int64_t num_blocks, pa_layout_t layout,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    TraceRange r("pa_decode_tree");
+    if (total_q < 0 || mask_words < 1) return PA_ERR_INVALID_ARG;
+    if (mask_words > PA_TREE_MAX_WORDS) return PA_ERR_UNSUPPORTED;
+    bool nothing_to_do = false;
+    const pa_status_t chk = pa::decode_check_args(
+        q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, 1, scale, out,
+        total_q > 0 ? num_seqs : 0, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, layout, 0,
+        &nothing_to_do);
+    if (chk != PA_OK) return chk;
+    if (num_seqs < 0) return PA_ERR_INVALID_ARG;
+    if ((int64_t)total_q * num_q_heads > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX - 127) return PA_ERR_UNSUPPORTED;
+    if (nothing_to_do) return PA_OK;
+    if (!query_start_loc || !tree_mask || (reinterpret_cast<uintptr_t>(tree_mask) & 7u)) return PA_ERR_INVALID_ARG;
+    const int sms = current_sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < pa::tree_workspace_bytes(sms))
+        return PA_ERR_WORKSPACE;
+    pa::TreeArgs a{};
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.starts = query_start_loc;
+    a.mask = reinterpret_cast<const uint32_t *>(tree_mask);
+    a.out = out;
+    a.mask_words = 2 * mask_words;
+    a.num_seqs = num_seqs;
+    a.total_q = total_q;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.group = num_q_heads / num_kv_heads;
+    a.block_size_log2 = log2_exact(block_size);
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.head_major = layout == PA_LAYOUT_HEAD_MAJOR ? 1 : 0;
+    a.box_tokens = block_size < 128 ? block_size : 128;
+    a.fault_hold_v = pa::prefill_fault();
+    a.num_blocks = num_blocks;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    a.workers = sms;
+    pa::tree_carve_workspace(a, workspace);
+    const cudaError_t e = pa::launch_decode_tree(a, pa::decode_group_pad(a.group), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status_t pa_keep_tokens(void *const *caches, int num_caches, int32_t *block_tables,
+                           int max_blocks_per_seq, int32_t *context_lens,
+                           const int32_t *query_start_loc, const int32_t *kept, int max_kept,
+                           int num_seqs, int32_t *ref_counts, int num_kv_heads, int head_dim,
+                           int block_size, int64_t num_blocks, pa_layout_t layout, void *stream) {
+    TraceRange r("pa_keep_tokens");
+    if (num_seqs < 0 || max_blocks_per_seq < 0 || max_kept < 1) return PA_ERR_INVALID_ARG;
+    if (layout != PA_LAYOUT_TOKEN_MAJOR && layout != PA_LAYOUT_HEAD_MAJOR) return PA_ERR_INVALID_ARG;
+    const pa_status_t chk = check_pools(caches, num_caches, num_kv_heads, head_dim, block_size, num_blocks);
+    if (chk != PA_OK) return chk;
+    if (max_kept > PA_KEEP_MAX_TOKENS || num_seqs > 65535) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!block_tables || !context_lens || !query_start_loc || !kept || max_blocks_per_seq == 0)
+        return PA_ERR_INVALID_ARG;
+    const int sms = current_sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    pa::KeepArgs a{};
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.starts = query_start_loc;
+    a.kept = kept;
+    a.ref_counts = ref_counts;
+    a.max_blocks = max_blocks_per_seq;
+    a.max_kept = max_kept;
+    a.num_seqs = num_seqs;
+    a.block_size_log2 = log2_exact(block_size);
+    a.num_kv_heads = num_kv_heads;
+    a.head_major = layout == PA_LAYOUT_HEAD_MAJOR ? 1 : 0;
+    a.num_blocks = num_blocks;
+    const cudaError_t e = pa::launch_keep_tokens(caches, num_caches, a, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 pa_status_t pa_rotary_init_frequencies(pa_rotary_t *rotary, int rot_dim, int interleaved,
                                        const double *frequencies, double amplitude) {
     if (!rotary || !frequencies || (interleaved != 0 && interleaved != 1)) return PA_ERR_INVALID_ARG;
@@ -857,7 +954,7 @@ pa_status_t pa_take_device_error(int32_t *code, void *stream) {
     cudaError_t (*const take[])(cudaStream_t, int *) = {
         pa::take_prefill_error, pa::take_prefill_mma_error, pa::take_decode_error,
         pa::take_store_error,      pa::take_blocks_error,
-        pa::take_shared_error, pa::take_rotary_error};
+        pa::take_shared_error, pa::take_rotary_error, pa::take_tree_error, pa::take_keep_error};
     int first = 0;
     for (auto f : take) {   // every word is read and cleared; the smallest code is reported
         int v = 0;

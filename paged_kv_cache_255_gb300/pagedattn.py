@@ -57,6 +57,10 @@ SIGNATURES = {
     "pa_free_blocks": ([_P, _I32, _P, _I32, _P, _P, _I32, _I32, _I64, _P], _I32),
     "pa_compact_blocks": ([_P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I64, _P,
                            _SZ, _P], _I32),
+    "pa_decode_tree_workspace_size": ([_I32, _I32, _I32], _SZ),
+    "pa_decode_tree": ([_P, _P, _P, _P, _I32, _P, _P, _P, _I32, _F32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I64,
+                        _I32, _P, _SZ, _P], _I32),
+    "pa_keep_tokens": ([_P, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _P, _I32, _I32, _I32, _I64, _I32, _P], _I32),
     "pa_rotary_init": ([_P, _I32, _I32, _F64, _I32, _F64, _F64, _F64, _F64, _F64], _I32),
     "pa_rotary_init_frequencies": ([_P, _I32, _I32, _P, _F64], _I32),
     "pa_rotate": ([_P, _I64, _I64, _P, _I64, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, _I32, _I32, _P, _I64, _P,
@@ -628,6 +632,86 @@ def compact_blocks(pools: CachePools, block_tables, context_lens, ref_counts, re
           num_live.data_ptr(), *pools._shape, workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
     return remap, num_live
+
+
+def decode_tree_workspace_size(num_q_heads: int, num_kv_heads: int, head_dim: int = 128, device=None) -> int:
+    """Workspace bytes pa_decode_tree needs on ``device`` (default: current)."""
+    index = None if device is None else torch.device(device).index
+    if index is None:       # no device, or "cuda": the current one
+        index = torch.cuda.current_device()
+    n = _size("pa_decode_tree_workspace_size", index, num_q_heads, num_kv_heads, head_dim)
+    if n == 0:
+        raise ValueError("unsupported head configuration")
+    return n
+
+
+def decode_tree(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, tree_mask, scale, out=None,
+                workspace=None, stream=None, head_major=False):
+    """Decode of a tree of drafted tokens per sequence; returns ``out``. q is bf16
+    [total_q, Hq, D], the nodes packed per sequence by query_start_loc (int32 [S + 1]);
+    a sequence's n nodes are the last n of its context_lens[s] cached tokens. A row sees
+    every token before them, and node j where bit j % 64 of tree_mask[row, j // 64]
+    (int64 [total_q, words], at most 16 words) is set: its ancestors and itself. The other
+    arguments are decode's. Rows of ``out`` outside all sequences are left as they were."""
+    dev = q.device
+    if not _fits(dev.index, torch.bfloat16, q, k_cache, v_cache):
+        _explain(dev, torch.bfloat16, q=q, k_cache=k_cache, v_cache=v_cache)
+    if not _fits(dev.index, torch.int32, block_tables, context_lens, query_start_loc):
+        _explain(dev, torch.int32, block_tables=block_tables, context_lens=context_lens, query_start_loc=query_start_loc)
+    if not _fits(dev.index, torch.int64, tree_mask):
+        _explain(dev, torch.int64, tree_mask=tree_mask)
+    T, Hq, D = q.shape
+    if head_major:
+        NB, Hkv, bs, D2 = k_cache.shape
+    else:
+        NB, bs, Hkv, D2 = k_cache.shape
+    S = context_lens.shape[0]
+    if v_cache.shape != k_cache.shape or D2 != D or block_tables.dim() != 2 or block_tables.shape[0] != S \
+            or context_lens.dim() != 1 or query_start_loc.shape != (S + 1,):
+        raise ValueError("shape mismatch between q, caches, block_tables, context_lens and query_start_loc")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != T:
+        raise ValueError("tree_mask must be [total_q, words]")
+    if out is None:
+        out = _new(q.shape, q.dtype, dev, stream)
+    else:
+        _cuda(out, "out", torch.bfloat16, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if workspace is None:
+        workspace = _scratch("tree", decode_tree_workspace_size(Hq, Hkv, D, dev), dev, stream)
+    else:
+        _cuda(workspace, "workspace", workspace.dtype, dev)
+    _call("pa_decode_tree", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+          block_tables.shape[1], context_lens.data_ptr(), query_start_loc.data_ptr(), tree_mask.data_ptr(),
+          tree_mask.shape[1], float(scale), out.data_ptr(), S, T, Hq, Hkv, D, bs, NB, 1 if head_major else 0,
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out
+
+
+def keep_tokens(pools: CachePools, block_tables, context_lens, query_start_loc, kept, ref_counts=None, stream=None):
+    """Keep the accepted nodes of every sequence's draft (the last n of its tokens, n from
+    query_start_loc, int32 [S + 1]): kept is int32 [S, m], a row's nodes in ascending order
+    up to the first -1. Their rows move to consecutive places behind the context in every
+    pool and context_lens becomes the shorter length, in place; with ref_counts
+    (fork_blocks) the blocks no longer needed are given back."""
+    dev = pools.device
+    if not _fits(dev.index, torch.int32, block_tables, context_lens, query_start_loc, kept):
+        _explain(dev, torch.int32, block_tables=block_tables, context_lens=context_lens,
+                 query_start_loc=query_start_loc, kept=kept)
+    S = context_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.dim() != 1 \
+            or query_start_loc.shape != (S + 1,) or kept.dim() != 2 or kept.shape[0] != S:
+        raise ValueError("shape mismatch between block_tables, context_lens, query_start_loc and kept")
+    refs = None
+    if ref_counts is not None:
+        if not _fits(dev.index, torch.int32, ref_counts):
+            _explain(dev, torch.int32, ref_counts=ref_counts)
+        if ref_counts.shape != (pools.num_blocks,):
+            raise ValueError("ref_counts must have one entry per block")
+        refs = ref_counts.data_ptr()
+    _call("pa_keep_tokens", dev, stream, *pools._args, block_tables.data_ptr(), block_tables.shape[1],
+          context_lens.data_ptr(), query_start_loc.data_ptr(), kept.data_ptr(), kept.shape[1], S, refs, *pools._shape,
+          1 if pools.head_major else 0)
 
 
 class _RotaryStruct(ctypes.Structure):
