@@ -20,15 +20,19 @@
 //
 // Inside a CTA (TMEM: S_A 0-127, O_A 128-255, S_B 256-383, O_B 384-511 columns;
 // P_t in bf16 over the first 64 columns of S_t):
-//   warps 0-3, 4-7   softmax of query tile A, B: thread t owns row t (TMEM lane t);
-//                    the mask's bits are read only on tiles that reach the nodes
+//   warps 0-3, 4-7   softmax of stream A, B. Two query tiles are a stream each; the even
+//                    and the odd key tiles of one query tile otherwise. Of more than 64
+//                    rows thread t owns row t (TMEM lane t); up to 64 rows (32) stand 16
+//                    (8) to a warp, a quad of lanes owning two rows (one), so that all four
+//                    schedulers work and each for a half (a quarter) of the time.
+//                    The mask's bits are read only on tiles that reach the nodes, and the V
+//                    of those is cleaned by the same warps before its product: rows past
+//                    the last token become 0, and so do infinities and NaN in nodes' rows (a
+//                    weight of 0 times them is not 0). The rows that do see such a node add
+//                    what was taken out after their result is written.
 //   warps 8, 9       K and V producers: TMA boxes of a block's tokens (16 .. 128) x 64
 //                    dims; the V warp also loads the queries
 //   warp 10          issues S = Q K^T and O += P V as their inputs arrive
-//   warp 11          cleans V tiles that reach the nodes between their landing and their
-//                    product: rows past the last token become 0, and so do infinities and
-//                    NaN in nodes' rows (a weight of 0 times them is not 0). The rows that do see
-//                    such a node add what was taken out after their result is written.
 // Hand-offs are mbarriers; every wait is bounded (about 2 s), and a wait that ran out
 // makes every role skip to its end. A role ends when what it has in flight has landed
 // (or 0.1 s later); then the CTA frees its TMEM.
@@ -55,14 +59,12 @@ constexpr int kSoftmaxThreads = 256;
 constexpr int kKWarp = kSoftmaxThreads / 32;            // 8
 constexpr int kVWarp = kKWarp + 1;                      // 9
 constexpr int kMmaWarp = kKWarp + 2;                    // 10
-constexpr int kCleanWarp = kKWarp + 3;                  // 11
-constexpr int kThreads = kSoftmaxThreads + 4 * 32;
+constexpr int kThreads = kSoftmaxThreads + 3 * 32;
 constexpr int kWarpsAll = kThreads / 32;
 constexpr int kGroup = 16;                              // tokens per MMA of P V
 constexpr int kGroups = kKeys / kGroup;                 // 8
 constexpr int kUnitPlaces = 2;                          // places of a unit besides its tiles
 constexpr int kMinPlaces = 3;                           // fewest places of a share
-constexpr int kMaskWords = 2 * 16;                      // 32-bit words of a mask row, at most
 constexpr uint32_t kQBytes = kRows * kRowBytes;         // 32 KB: 2 halves of [128][128 B]
 constexpr uint32_t kQHalf = kRows * 128;
 constexpr uint32_t kKVBytes = kKeys * kRowBytes;
@@ -71,31 +73,33 @@ constexpr uint32_t kOffQ = 0;                           // Q_A, Q_B
 constexpr uint32_t kOffK = kOffQ + 2 * kQBytes;
 constexpr uint32_t kOffV = kOffK + kKStages * kKVBytes;
 constexpr uint32_t kOffCtl = kOffV + kVStages * kKVBytes;
-constexpr uint32_t kBarQFull = 0;
-constexpr uint32_t kBarQEmpty = 1;
-constexpr uint32_t kBarKFull = 2;                        // + stage
+constexpr uint32_t kBarQFull = 0;                        // + buffer
+constexpr uint32_t kBarQEmpty = 2;                       // + buffer
+constexpr uint32_t kBarKFull = 4;                        // + stage
 constexpr uint32_t kBarKEmpty = kBarKFull + kKStages;
 constexpr uint32_t kBarVFull = kBarKEmpty + kKStages;
 constexpr uint32_t kBarVEmpty = kBarVFull + kVStages;
-constexpr uint32_t kBarSFull = kBarVEmpty + kVStages;    // + query tile (A 0, B 1)
+constexpr uint32_t kBarSFull = kBarVEmpty + kVStages;    // + stream (A 0, B 1)
 constexpr uint32_t kBarPReady = kBarSFull + 2;
 constexpr uint32_t kBarPVDone = kBarPReady + 2;
-constexpr uint32_t kBarOFree = kBarPVDone + 2;
-constexpr uint32_t kBarDrain = kBarOFree + 2;            // all products issued are done
-constexpr uint32_t kBarVLanded = kBarDrain + 1;          // + stage: a V tile that is to be cleaned
-constexpr uint32_t kNumBars = kBarVLanded + kVStages;
+constexpr uint32_t kBarOFree = kBarPVDone + 2;           // a piece's results are read
+constexpr uint32_t kBarHalves = kBarOFree + 1;           // both streams' maxima and sums are there
+constexpr uint32_t kBarDrain = kBarHalves + 1;           // all products issued are done
+constexpr uint32_t kNumBars = kBarDrain + 1;
 constexpr uint32_t kOffTmemSlot = kOffCtl + 8 * kNumBars;
 constexpr uint32_t kOffAbort = kOffTmemSlot + 4;
 constexpr uint32_t kWalkBytes = 64;
 constexpr uint32_t kOffWalk = (kOffAbort + 4 + 15) & ~15u;        // one Walk per warp
-constexpr uint32_t kOffSums = kOffWalk + kWalkBytes * kWarpsAll;  // plan: a sum per warp
-constexpr uint32_t kOffOdd = kOffSums + 8 * kWarpsAll;            // by parity of the piece: nodes whose V
-constexpr uint32_t kOddBytes = 4 * (kMaskWords + 1);              // is not all finite, and whether any is
-constexpr uint32_t kSmemBytes = kOffOdd + 2 * kOddBytes;
+constexpr int kOddSets = 4;                                       // of the pieces in flight: bit i, nodes 32 i ..
+constexpr uint32_t kOffOdd = kOffWalk + kWalkBytes * kWarpsAll;   // 32 i + 31 have V that is not finite
+constexpr uint32_t kOffHalves = kOffOdd + 4 * kOddSets;           // [2][128] float2; before that the plan's sums
+constexpr uint32_t kSmemBytes = kOffHalves + 2 * kRows * 8;
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdescS = tc::idesc_bf16(128, kKeys, false);
 constexpr uint32_t kIdescPV = tc::idesc_bf16(128, 128, true);
+constexpr uint32_t kNegateA = 1u << 13;                 // of an instruction descriptor
+constexpr uint32_t kMasked = 0xff800000u;               // -infinity
 constexpr float kRescaleSlack = 8.f;                    // log2 units
 
 __device__ __forceinline__ void set_error(int code) { atomicCAS(&g_tree_error, 0, code); }
@@ -105,17 +109,16 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __forceinline__ float fmin3(float a, float b, float c) {
-    float r;
-    asm("min.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
 
+// The kernel's code has to stay small: at 200 KB every unit's straight-line code came from
+// L2 again (an epilogue of 16 stores took 7000 cycles). What runs once a piece or
+// less is therefore out of line.
+
 // Bounded wait that also gives up once the CTA's abort flag is set.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort) {
+__device__ __noinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort) {
     if (tc::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = tc::globaltimer_ns();
     for (;;) {
@@ -134,22 +137,40 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
     if (!tc::drain_bar(bar, parity)) set_error(kErrTimeout);
 }
 
-// One lane waits for the warp; with `spin` the whole warp polls first (a
-// suspended waiter resumes late).
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort,
-                                          bool spin = false) {
+// The warp polls, converged: the answer to every lane's test (a suspended waiter resumes
+// late), bounded; without `spin` one lane waits for it.
+__device__ __noinline__ bool warp_wait_more(uint32_t bar, uint32_t parity, volatile int *abort, bool spin) {
     if (spin) {
-        for (int i = 0; i < 256; ++i)
-            if (__any_sync(0xffffffffu, tc::mbar_test_wait(bar, parity))) {
-                __syncwarp();
-                return true;
+        const uint64_t t0 = tc::globaltimer_ns();
+#pragma unroll 1
+        for (uint32_t i = 1;; ++i) {
+            if (__any_sync(0xffffffffu, tc::mbar_test_wait(bar, parity))) break;
+            if ((i & 255) == 0) {
+                const bool late = tc::globaltimer_ns() - t0 > 2000000000ull;
+                if (__any_sync(0xffffffffu, late || *abort)) {
+                    if ((threadIdx.x & 31) == 0 && !*abort) {
+                        set_error(kErrTimeout);
+                        *abort = 1;
+                    }
+                    return false;
+                }
             }
+        }
+        __syncwarp();
+        return true;
     }
     bool ok = true;
     if ((threadIdx.x & 31) == 0) ok = wait_bar(bar, parity, abort);
-    const bool r = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
     __syncwarp();
-    return r;
+    return ok;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, bool spin = false) {
+    if (__any_sync(0xffffffffu, tc::mbar_test_wait(bar, parity))) {
+        __syncwarp();
+        return true;
+    }
+    return warp_wait_more(bar, parity, abort, spin);
 }
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
     __syncwarp();
@@ -165,7 +186,7 @@ struct Seq {
 };
 
 template <int G>
-__device__ __forceinline__ Seq load_seq(const TreeArgs &a, int s) {
+__device__ __noinline__ Seq load_seq(const TreeArgs &a, int s) {
     const int64_t max_len = (int64_t)a.max_blocks_per_seq << a.block_size_log2;     // below 2^31
     const int64_t l = __ldg(a.context_lens + s);
     int q0 = __ldg(a.starts + s), q1 = __ldg(a.starts + s + 1);
@@ -180,18 +201,20 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &a, int s) {
     return r;
 }
 
-__device__ __forceinline__ int64_t seq_places(const Seq &q, int num_kv_heads) {
-    return (int64_t)q.pairs * num_kv_heads * (q.nt + kUnitPlaces);
+// Places of a sequence's units in one of `lanes` lanes.
+__device__ __forceinline__ int64_t seq_places(const Seq &q, int num_kv_heads, int lanes) {
+    return (int64_t)(q.pairs / lanes) * num_kv_heads * (q.nt + kUnitPlaces);
 }
 
-// A share's walk over the flat space, sequence by sequence, KV head, pair, key tile: its
-// pieces are runs of key tiles [j0, j1) of one unit. Every warp walks by itself and keeps
-// its place in shared memory, where the fields are read when they are needed: none
-// stays live across the tile loop.
+// A share's walk over the flat space of its lane, sequence by sequence, KV head, pair, key
+// tile: its pieces are runs of key tiles [j0, j1) of one unit. Every warp walks by itself
+// and keeps its place in shared memory, where the fields are read when they are needed:
+// none stays live across the tile loop.
 struct alignas(16) Walk {
     int64_t T, T1;      // place of tile j0, end of the share
     Seq q;
     int s, kvh, pair, j0, j1;
+    int lane, lanes;
 };
 static_assert(sizeof(Walk) == kWalkBytes, "Walk");
 
@@ -206,8 +229,9 @@ __device__ __forceinline__ bool next_unit(Walk &w, const TreeArgs &a) {
     w.T += w.q.nt - w.j0 + kUnitPlaces;
     if (w.T >= w.T1) return false;
     w.j0 = 0;
-    if (++w.pair == w.q.pairs) {
-        w.pair = 0;
+    w.pair += w.lanes;
+    if (w.pair >= w.q.pairs) {
+        w.pair = w.lane;
         if (++w.kvh == a.num_kv_heads) {
             w.kvh = 0;
             do w.q = load_seq<G>(a, ++w.s);         // the places left are some sequence's
@@ -219,7 +243,7 @@ __device__ __forceinline__ bool next_unit(Walk &w, const TreeArgs &a) {
 }
 
 template <int G>
-__device__ __forceinline__ bool walk_next(volatile Walk &place, const TreeArgs &a) {
+__device__ __noinline__ bool walk_next(volatile Walk &place, const TreeArgs &a) {
     bool more = false;
     __syncwarp();
     if ((threadIdx.x & 31) == 0) more = next_unit<G>(const_cast<Walk &>(place), a);
@@ -228,27 +252,53 @@ __device__ __forceinline__ bool walk_next(volatile Walk &place, const TreeArgs &
     return more;
 }
 
-// The total number of places, the shares in use, and this CTA's first piece (in
-// `first`, shared memory); false when it has none. All threads call it.
+// The places of a lane, its shares, and this CTA's first piece (in `first`, shared memory);
+// false when it has none. All threads call it.
 template <int G>
-__device__ __forceinline__ bool plan_share(const TreeArgs &a, Walk *first, volatile long long *sums,
+__device__ __noinline__ bool plan_share(const TreeArgs &a, Walk *first, volatile long long *sums,
                                            int64_t &W, int &shares) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = a.num_seqs, Hkv = a.num_kv_heads;
     Seq mine{};
     if (tid < S) mine = load_seq<G>(a, tid);
-    long long local = tid < S ? seq_places(mine, Hkv) : 0;
-    for (int s = tid + kThreads; s < S; s += kThreads) local += seq_places(load_seq<G>(a, s), Hkv);
+    long long all = 0, one = 0;                 // places of all pairs, and of one pair a unit
+    int most = 0, least = INT_MAX;              // pairs of a sequence
+    for (int s = tid; s < S; s += kThreads) {
+        const Seq q = s == tid ? mine : load_seq<G>(a, s);
+        if (q.pairs == 0) continue;
+        all += seq_places(q, Hkv, 1);
+        one += seq_places(q, Hkv, q.pairs);
+        most = q.pairs > most ? q.pairs : most;
+        least = q.pairs < least ? q.pairs : least;
+    }
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) local += __shfl_xor_sync(0xffffffffu, local, m);
-    if (lane == 0) sums[warp] = local;
+    for (int m = 16; m >= 1; m >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, m);
+        one += __shfl_xor_sync(0xffffffffu, one, m);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) {
+        sums[warp] = all;
+        sums[kWarpsAll + warp] = one;
+        sums[2 * kWarpsAll + warp] = (long long)most << 32 | least;
+    }
     __syncthreads();
-    W = 0;
-    for (int i = 0; i < kWarpsAll; ++i) W += sums[i];
+    all = one = 0;
+    for (int i = 0; i < kWarpsAll; ++i) {
+        all += sums[i];
+        one += sums[kWarpsAll + i];
+        const long long x = sums[2 * kWarpsAll + i];
+        most = (int)(x >> 32) > most ? (int)(x >> 32) : most;
+        least = (int)x < least ? (int)x : least;
+    }
     __syncthreads();
-    int64_t p = W / kMinPlaces;
-    shares = (int)(p < 1 ? 1 : (p > a.workers ? a.workers : p));
-    const int w = blockIdx.x;
+    // where all have the same number of pairs, the pairs are lanes
+    const int lanes = most == least && most <= a.workers ? most : 1;
+    W = lanes > 1 ? one : all;
+    const int64_t p = W / kMinPlaces, cap = a.workers / lanes;
+    shares = (int)(p < 1 ? 1 : (p > cap ? cap : p));
+    const int mine_lane = blockIdx.x % lanes, w = blockIdx.x / lanes;
     if (w >= shares || W == 0) return false;
     const int64_t T0 = (int64_t)w * W / shares, T1 = (int64_t)(w + 1) * W / shares;
     if (tid == 0) first->T1 = -1;               // nothing found yet
@@ -256,7 +306,7 @@ __device__ __forceinline__ bool plan_share(const TreeArgs &a, Walk *first, volat
     for (int c0 = 0; c0 < S && base <= T0; c0 += kThreads) {
         const int s = c0 + tid;
         const Seq q = c0 == 0 ? mine : (s < S ? load_seq<G>(a, s) : Seq{});
-        const long long own = s < S ? seq_places(q, Hkv) : 0;
+        const long long own = s < S ? seq_places(q, Hkv, lanes) : 0;
         long long v = own;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -274,14 +324,16 @@ __device__ __forceinline__ bool plan_share(const TreeArgs &a, Walk *first, volat
         if (own > 0 && T0 >= excl && T0 < excl + own) {
             Walk k;
             const int64_t rem = T0 - excl;
-            const int places = q.nt + kUnitPlaces;
+            const int places = q.nt + kUnitPlaces, per_head = q.pairs / lanes;
             const int64_t unit = rem / places;
             k.T = T0;
             k.T1 = T1;
             k.q = q;
             k.s = s;
-            k.kvh = (int)(unit / q.pairs);
-            k.pair = (int)(unit - (int64_t)k.kvh * q.pairs);
+            k.lane = mine_lane;
+            k.lanes = lanes;
+            k.kvh = (int)(unit / per_head);
+            k.pair = mine_lane + lanes * (int)(unit - (int64_t)k.kvh * per_head);
             k.j0 = (int)(rem - unit * places);
             bool works = true;
             if (k.j0 >= q.nt) works = next_unit<G>(k, a);     // past the unit's tiles
@@ -297,23 +349,40 @@ __device__ __forceinline__ bool plan_share(const TreeArgs &a, Walk *first, volat
 
 // -- masks -----------------------------------------------------------------------
 
-// Bits [32 i, 32 i + 32) of a row of `words` mask words: nodes before the first (the
-// context) are seen, those past the last are not.
-__device__ __forceinline__ uint32_t mask_word(const uint32_t *row, int words, int i) {
-    return i < 0 ? ~0u : (i < words ? row[i] : 0u);
-}
-// Of 32 nodes from node b on, those that exist (below n).
-__device__ __forceinline__ uint32_t below(int n, int b) {
-    const int k = n - b;
-    return k <= 0 ? 0u : (k >= 32 ? ~0u : (1u << k) - 1u);
+// Of the 128 tokens from node b on (negative: before the first, in the context), those that
+// a row of `words` mask words sees: all of the context, and the nodes below n whose bits it
+// has.
+__device__ __noinline__ uint4 seen_nodes(const uint32_t *row, int words, int b, int n) {
+    uint32_t w[5], v[4];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+        const int i = (b >> 5) + k;
+        w[k] = i < 0 ? ~0u : (i < words ? row[i] : 0u);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int left = n - b - 32 * k;
+        const uint32_t real = left <= 0 ? 0u : (left >= 32 ? ~0u : (1u << left) - 1u);
+        v[k] = __funnelshift_r(w[k], w[k + 1], b & 31) & real;
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// Key tiles of a piece that a query tile (0 A, 1 B) computes: all, or none when the
-// rows end before it.
+// Whether a piece's rows reach into query tile B. Its two streams are then the two query
+// tiles over all key tiles; otherwise they are the even and the odd key tiles of query tile
+// A (counted from the piece's first), merged when the piece ends.
 template <int G>
-__device__ __forceinline__ int piece_tiles(const volatile Walk &w, int t) {
-    return w.pair * (kPair / G) + t * (kRows / G) < w.q.n ? w.j1 - w.j0 : 0;
+__device__ __forceinline__ bool two_tiles(const volatile Walk &w) {
+    return w.pair * (kPair / G) + kRows / G < w.q.n;
 }
+// Rows of a warp's 32 TMEM lanes: all, or the first 16 or 8 for up to 64 or 32 rows.
+template <int G>
+__device__ __forceinline__ int rows_per_warp(const volatile Walk &w) {
+    const int tokens = w.q.n - w.pair * (kPair / G);
+    return tokens <= 32 / G && G <= 8 ? 8 : (tokens <= 64 / G ? 16 : 32);
+}
+// Key tiles of a stream.
+__device__ __forceinline__ int stream_tiles(int nt, bool two, int t) { return two ? nt : (nt + 1 - t) / 2; }
 
 // 16-token groups of key tile j that hold keys.
 __device__ __forceinline__ int groups_used(const volatile Walk &w, int j) {
@@ -327,63 +396,65 @@ __device__ __forceinline__ bool reaches_nodes(const volatile Walk &w, int j) {
 }
 
 // A V tile in shared memory whose keys reach the nodes: rows past the last token become
-// zero, and so do the elements of nodes' rows that are not finite; the nodes that had some
-// are marked in `odd`. The 16-byte chunks of a row are permuted within it (128-byte
+// zero, and so do the elements of nodes' rows that are not finite; the words of 32 nodes
+// that had some are marked in `odd`. By the 128 threads of a stream. The 16-byte chunks of a row are permuted within it (128-byte
 // swizzle), which does not matter here.
-__device__ __forceinline__ void clean_v(const volatile Walk &w, int j, uint32_t vtile, uint32_t *odd, int words,
-                                        int lane) {
+__device__ __noinline__ void clean_v(const volatile Walk &w, int j, uint8_t *vtile, uint32_t *odd, int words,
+                                        int thread) {
     const int node0 = j * kKeys - (w.q.L - w.q.n);              // node of the tile's first key
     const int first = node0 < 0 ? -node0 : 0, left = w.q.L - j * kKeys;
     const int rows = groups_used(w, j) * kGroup - first;
-#pragma unroll 4
-    for (int i = lane; i < rows * 16; i += 32) {
-        const int r = first + (i >> 4);
-        const uint32_t at = vtile + ((i >> 3) & 1) * kKVHalf + r * 128 + (i & 7) * 16;
-        uint32_t x[4] = {0u, 0u, 0u, 0u};
-        bool store = true;
-        if (r < left) {
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
-                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                         : "r"(at)
-                         : "memory");
-            store = false;
+    constexpr int kBatch = 4;                                   // chunks a thread has in flight
+    for (int i0 = thread; i0 < rows * 16; i0 += kRows * kBatch) {
+        uint4 *at[kBatch];
+        uint4 x[kBatch];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + kRows * k, r = first + (i >> 4);
+            at[k] = reinterpret_cast<uint4 *>(vtile + ((i >> 3) & 1) * kKVHalf + r * 128 + (i & 7) * 16);
+            if (i < rows * 16 && r < left) x[k] = *at[k];
+            else x[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + kRows * k, r = first + (i >> 4);
+            uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            bool odd_one = false;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
                 // an exponent of all ones: infinity or NaN
-                const bool lo = (x[k] & 0x7f80u) == 0x7f80u, hi = (x[k] & 0x7f800000u) == 0x7f800000u;
-                if (lo) x[k] &= 0xffff0000u;
-                if (hi) x[k] &= 0x0000ffffu;
-                store |= lo | hi;
+                const bool lo = (v[c] & 0x7f80u) == 0x7f80u, hi = (v[c] & 0x7f800000u) == 0x7f800000u;
+                v[c] = lo ? v[c] & 0xffff0000u : v[c];
+                v[c] = hi ? v[c] & 0x0000ffffu : v[c];
+                odd_one |= lo | hi;
             }
-            const int node = node0 + r;
-            if (store && node < 32 * words) {                   // the others nobody sees
-                atomicOr(odd + (node >> 5), 1u << (node & 31));
-                odd[kMaskWords] = 1u;
+            if (i < rows * 16 && (odd_one || r >= left)) {
+                *at[k] = make_uint4(v[0], v[1], v[2], v[3]);
+                const int node = node0 + r;
+                if (odd_one && node < 32 * words) atomicOr(odd, 1u << (node >> 5));     // the others nobody sees
             }
         }
-        if (store)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-                         "r"(x[3])
-                         : "memory");
     }
 }
 
-// What clean_v took out of the nodes that a row sees, added to its written result: the
-// dims of those nodes that are not finite. `out` is the row in bf16, or `part` its words of
-// a part in fp32. Rare.
-__device__ __noinline__ void add_odd(const TreeArgs &a, const uint32_t *odd, int s, int kvh, int first_node,
-                                     const uint32_t *mask_row, uint16_t *out, float4 *part) {
+// What clean_v took out of the nodes that a row sees among tokens [t0, t1), added to its
+// written result: dims [d0, d1) of those that are not finite. `out` is the row in bf16, or
+// `part` its words of a part in fp32. Rare.
+__device__ __noinline__ void add_odd(const TreeArgs &a, uint32_t odd, int s, int kvh, int first_node, int t0, int t1,
+                                     const uint32_t *mask_row, uint16_t *out, float4 *part, int d0, int d1) {
     const int lb = a.block_size_log2;
-    for (int i = 0; i < a.mask_words; ++i)
-        for (uint32_t bits = odd[i] & mask_row[i]; bits; bits &= bits - 1) {
+    for (; odd; odd &= odd - 1) {
+        const int i = __ffs(odd) - 1;
+        for (uint32_t bits = mask_row[i]; bits; bits &= bits - 1) {
             const int t = first_node + 32 * i + __ffs(bits) - 1;
+            if (t < t0 || t >= t1) continue;
             const int64_t bid = __ldg(a.block_tables + (int64_t)s * a.max_blocks_per_seq + (t >> lb));
             const int off = t & ((1 << lb) - 1);
             if (bid < 0 || bid >= a.num_blocks) continue;       // read as zeros
             const int64_t row = a.head_major ? ((bid * a.num_kv_heads + kvh) << lb) + off
                                              : ((bid << lb) + off) * a.num_kv_heads + kvh;
             const uint16_t *v = static_cast<const uint16_t *>(a.v_cache) + row * kHeadDim;
-            for (int d = 0; d < kHeadDim; ++d) {
+            for (int d = d0; d < d1; ++d) {
                 if ((v[d] & 0x7f80) != 0x7f80) continue;
                 const float x = __uint_as_float((uint32_t)v[d] << 16);
                 if (out) {
@@ -394,15 +465,389 @@ __device__ __noinline__ void add_odd(const TreeArgs &a, const uint32_t *odd, int
                 }
             }
         }
+    }
+}
+
+// Rows of a TMA box of queries: whole tokens' G heads, and whole 8-row swizzle atoms.
+__host__ __device__ constexpr int box_rows(int G) { return G > 8 ? G : 8; }
+
+// The two buffers of queries, counted alike by the V warp, which fills them, and the MMA
+// warp: a piece of two query tiles takes both, others take them in turn.
+struct QBuffers {
+    int n0 = 0, n1 = 0, next = 0;
+    // the buffer of query tile A
+    __device__ __forceinline__ int take(bool two) {
+        const int b = two ? 0 : next;
+        if (!two) next ^= 1;
+        n0 += two || b == 0 ? 1 : 0;
+        n1 += two || b == 1 ? 1 : 0;
+        return b;
+    }
+    __device__ __forceinline__ int uses(int b) const { return b == 0 ? n0 : n1; }
+    // one that was taken and not filled
+    __device__ __forceinline__ void drop(int b) {
+        if (b == 0) --n0;
+        else --n1;
+    }
+};
+
+// -- softmax of one key tile ----------------------------------------------------------
+//
+// Scores S from TMEM (of -Q, where the scale is negative, so that sc is positive), the masked
+// ones -infinity; the running max m (log2 units) is raised
+// only when the tile exceeds it by 2^8: weights stay below 2^8, far inside fp32 and bf16
+// range, and O is rescaled rarely. P = 2^(S sc - m), rounded to bf16 for the second product:
+// its error of 2^-9 per weight averages out over the keys, and the output is rounded
+// to bf16 as well. The sum is of the exact weights.
+
+// The new max for a tile whose largest raw score is `most` (-infinity: all masked); the
+// factor on what was summed before (1 when the max stays).
+__device__ __forceinline__ float raise_max(float most, float sc, float &m, float &lsum) {
+    const float mt = most * sc;
+    if (!(mt > m + kRescaleSlack)) return 1.f;
+    const float alpha = m != -INFINITY ? ex2(m - mt) : 1.f;
+    lsum *= alpha;
+    m = mt;
+    return alpha;
+}
+
+// A thread per row: 128 scores of its TMEM lane.
+__device__ __forceinline__ void wide_tile(uint32_t tS, uint32_t tO, float sc, bool nodes,
+                                          const uint32_t (&vis)[4], float &m, float &lsum) {
+    uint32_t sr[4][32];
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) tc::tmem_ld32(tS + ch * 32, sr[ch]);
+    tc::tmem_ld_wait();
+    if (nodes) {
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+                if (!(vis[ch] >> c & 1)) sr[ch][c] = kMasked;
+    }
+    // in four running values
+    float e4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+        for (int c = 0; c < 32; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                e4[k] = fmax3(e4[k], __uint_as_float(sr[ch][c + 2 * k]), __uint_as_float(sr[ch][c + 2 * k + 1]));
+    const float alpha = raise_max(fmax3(fmaxf(e4[0], e4[1]), e4[2], e4[3]), sc, m, lsum);
+    const float mb = m == -INFINITY ? 0.f : m;
+    float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+        uint32_t pw[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const float p0 = ex2(fmaf(__uint_as_float(sr[ch][2 * c]), sc, -mb));
+            const float p1 = ex2(fmaf(__uint_as_float(sr[ch][2 * c + 1]), sc, -mb));
+            l4[c & 3] += p0 + p1;
+            pw[c] = pack_bf16x2(p0, p1);
+        }
+        tc::tmem_st16(tS + ch * 16, pw);
+    }
+    lsum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+            uint32_t o[32];
+            tc::tmem_ld32(tO + ch * 32, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tc::tmem_st32(tO + ch * 32, o);
+        }
+    }
+    tc::tmem_st_wait();
+}
+
+// A quad of lanes per row, or (R = 2) per row and the one 8 further on: lane q of a quad
+// has scores 8 k + 2 q and the next, k = 0 .. 15, of each.
+template <int R>
+__device__ __forceinline__ void narrow_tile(uint32_t tS, uint32_t tO, float sc, bool nodes,
+                                            const uint32_t (&vis)[R][4], float (&m)[R], float (&lsum)[R]) {
+    const int q2 = 2 * (threadIdx.x & 3);
+    uint32_t s[64];
+    tc::tmem_ld_16x256b_x16(tS, s);
+    tc::tmem_ld_wait();
+    float alpha[2] = {1.f, 1.f}, mb[2] = {0.f, 0.f};
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+        if (nodes) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const uint32_t v = vis[x][k >> 2] >> q2;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (!(v >> (8 * (k & 3) + e) & 1)) s[4 * k + 2 * x + e] = kMasked;
+            }
+        }
+        float e2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            e2[k & 1] = fmax3(e2[k & 1], __uint_as_float(s[4 * k + 2 * x]), __uint_as_float(s[4 * k + 2 * x + 1]));
+        float most = fmaxf(e2[0], e2[1]);
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        alpha[x] = raise_max(most, sc, m[x], lsum[x]);
+        mb[x] = m[x] == -INFINITY ? 0.f : m[x];
+    }
+    uint32_t pw[32];
+    float l2[2][2] = {};
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (x >= R) {                       // no row there
+                pw[2 * k + x] = 0u;
+                continue;
+            }
+            const float p0 = ex2(fmaf(__uint_as_float(s[4 * k + 2 * x]), sc, -mb[x]));
+            const float p1 = ex2(fmaf(__uint_as_float(s[4 * k + 2 * x + 1]), sc, -mb[x]));
+            l2[x][k & 1] += p0 + p1;
+            pw[2 * k + x] = pack_bf16x2(p0, p1);
+        }
+    tc::tmem_st_16x128b_x16(tS, pw);
+#pragma unroll
+    for (int x = 0; x < R; ++x) lsum[x] += l2[x][0] + l2[x][1];
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            uint32_t o[32];
+            tc::tmem_ld_16x256b_x8(tO + 64 * h, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[(i >> 1) & 1]);
+            tc::tmem_st_16x256b_x8(tO + 64 * h, o);
+        }
+    }
+    tc::tmem_st_wait();
+}
+
+// What a softmax warp counts over its pieces.
+struct Streams {
+    uint32_t gt = 0, ga = 0;    // key tiles before this piece, of this stream and of all
+    int piece = 0, halves = 0;  // pieces before this one; those whose streams were halves
+};
+
+// A softmax warp's part of one piece: R = 0 a thread per row, 1 and 2 a quad of lanes per one
+// and two rows. False when a wait ran out.
+template <int G, int R>
+__device__ __forceinline__ bool softmax_piece(const TreeArgs &a, const volatile Walk &w, Streams &st, uint8_t *smem,
+                                              uint32_t sbase, uint32_t tmem) {
+    constexpr int NR = R == 2 ? 2 : 1;                  // rows of a thread
+    const int tid = threadIdx.x, wg = tid >> 7, r = tid & 127;
+    const uint32_t lane = (uint32_t)(r & ~31) << 16;
+    const uint32_t tS = tmem + lane + wg * 256, tO = tS + 128;
+    auto bar = [&](uint32_t i) { return sbase + kOffCtl + 8 * i; };
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + kOffAbort);
+    uint32_t *odd_marks = reinterpret_cast<uint32_t *>(smem + kOffOdd);
+    const float sc = fabsf(a.scale_log2);
+    const bool two = R == 0 && two_tiles<G>(w);
+    const int nt = w.j1 - w.j0, ntt = stream_tiles(nt, two, wg);
+    const int tile = two ? wg : 0;                      // query tile
+    // this thread's first row of the query tile, the other is 8 further on
+    const int row0 = R == 0 ? r : (r >> 5) * (8 * R) + ((tid >> 2) & 7);
+    auto token = [&](int row) { return w.pair * (kPair / G) + tile * (kRows / G) + row / G; };
+    auto row_valid = [&](int row) { return token(row) < w.q.n && row % G < a.group; };
+    bool rv[NR];
+#pragma unroll
+    for (int x = 0; x < NR; ++x) rv[x] = row_valid(row0 + 8 * x);
+    // warps past the last row only take part in the hand-offs and the cleaning
+    const bool any = __any_sync(0xffffffffu, rv[0]);
+    float m[NR], lsum[NR];
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+        m[x] = -INFINITY;
+        lsum[x] = 0.f;
+    }
+#pragma unroll 1
+    for (int j = 0; j < ntt; ++j) {
+        const int jj = two ? j : 2 * j + wg;            // key tile, from the piece's first
+        const int b0 = (w.j0 + jj) * kKeys - (w.q.L - w.q.n);       // node of its first key
+        const bool nodes = b0 + kKeys > 0;
+        uint32_t vis[NR][4];
+        if (nodes && any)
+#pragma unroll
+            for (int x = 0; x < NR; ++x) {
+                const uint32_t *row = a.mask + ((int64_t)w.q.q0 + token(row0 + 8 * x)) * a.mask_words;
+                const uint4 v = rv[x] ? seen_nodes(row, a.mask_words, b0, w.q.n) : make_uint4(0u, 0u, 0u, 0u);
+                vis[x][0] = v.x;
+                vis[x][1] = v.y;
+                vis[x][2] = v.z;
+                vis[x][3] = v.w;
+            }
+        // S_t(j) done: also PV_t(j - 1), issued before it, so O is stable (a warp without
+        // rows sleeps until then: its polls would take from the others)
+        if (!warp_wait(bar(kBarSFull + wg), (st.gt + j) & 1, abort, any)) return false;
+        tc::fence_after_sync();
+        if (any) {
+            if constexpr (R == 0) wide_tile(tS, tO, sc, nodes, vis[0], m[0], lsum[0]);
+            else narrow_tile<R>(tS, tO, sc, nodes, vis, m, lsum);
+        }
+        // V has to be there to be cleaned; of two query tiles A's warps do it, whose product
+        // is issued first
+        if (nodes && (!two || wg == 0)) {
+            const uint32_t g = st.ga + jj;
+            if (!warp_wait(bar(kBarVFull + g % kVStages), (g / kVStages) & 1, abort, any)) return false;
+            clean_v(w, w.j0 + jj, smem + kOffV + (g % kVStages) * kKVBytes, odd_marks + st.piece % kOddSets, a.mask_words, r);
+            tc::fence_proxy_async();
+        }
+        tc::fence_before_sync();
+        warp_arrive(bar(kBarPReady + wg));
+    }
+    if (ntt > 0) {
+        if (!warp_wait(bar(kBarPVDone + wg), (st.gt + ntt - 1) & 1, abort, any)) return false;
+        tc::fence_after_sync();
+    }
+    if (R > 0) {
+        // a quad's sums; its maxima are common
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 1);
+            lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 2);
+        }
+    }
+    // Streams that are halves of the same rows: both know both maxima and sums, stream A
+    // takes dims 0-63 of both O, stream B the others (both warps of a row have its TMEM lane).
+    const bool first = R == 0 || (tid & 3) == 0;        // of the row's lanes
+    float fa[NR], fb[NR];                               // factors on the O of A, B (own: fa)
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+        fa[x] = 1.f;
+        fb[x] = 0.f;
+    }
+    if (!two) {
+        // (a stream without tiles has not waited for the last piece's to be read)
+        if (ntt == 0 && st.piece > 0 && !warp_wait(bar(kBarOFree), (st.piece - 1) & 1, abort)) return false;
+        float2 *ml = reinterpret_cast<float2 *>(smem + kOffHalves);
+#pragma unroll
+        for (int x = 0; x < NR; ++x)
+            if (first) ml[wg * kRows + row0 + 8 * x] = make_float2(m[x], lsum[x]);
+        tc::fence_before_sync();
+        warp_arrive(bar(kBarHalves));
+        if (!warp_wait(bar(kBarHalves), st.halves & 1, abort, any)) return false;
+        tc::fence_after_sync();
+        ++st.halves;
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            const float2 ea = ml[row0 + 8 * x], eb = ml[kRows + row0 + 8 * x];
+            m[x] = fmaxf(ea.x, eb.x);
+            fa[x] = ea.y == 0.f ? 0.f : ex2(ea.x - m[x]);
+            fb[x] = eb.y == 0.f ? 0.f : ex2(eb.x - m[x]);
+            lsum[x] = (ea.y == 0.f ? 0.f : ea.y * fa[x]) + (eb.y == 0.f ? 0.f : eb.y * fb[x]);
+        }
+    }
+    if (any) {
+        const bool whole = w.j0 == 0 && w.j1 == w.q.nt, b_too = !two && nt > 1;
+        // a row's place in the output (16-byte words), and among the parts
+        auto out_row = [&](int row) {
+            return reinterpret_cast<uint4 *>(a.out) +
+                   (((int64_t)w.q.q0 + token(row)) * a.num_q_heads + (int64_t)w.kvh * a.group + row % G) * (kHeadDim / 8);
+        };
+        const int slot = 2 * (int)blockIdx.x + (w.j0 == 0 ? 1 : 0);
+        float4 *po = a.part_o + (int64_t)slot * 32 * kPair + tile * kRows;
+        const int d0 = two ? 0 : 64 * wg, d1 = two ? kHeadDim : d0 + 64;
+        // a row that saw nothing outputs zero, whatever its O
+        float inv[NR];
+#pragma unroll
+        for (int x = 0; x < NR; ++x) {
+            inv[x] = whole ? 1.f / lsum[x] : 1.f;
+            if (!whole && rv[x] && first && (two || wg == 0))
+                a.part_ml[(int64_t)slot * kPair + tile * kRows + row0 + 8 * x] = make_float2(m[x], lsum[x]);
+        }
+        if constexpr (R == 0) {
+            uint4 *orow = out_row(row0);
+#pragma unroll 1
+            for (int d = d0; d < d1; d += 32) {
+                uint32_t o[32], o2[32];
+                tc::tmem_ld32((two ? tO : tmem + lane + 128) + d, o);
+                if (b_too) tc::tmem_ld32(tmem + lane + 384 + d, o2);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    float x = __uint_as_float(o[c]) * fa[0];
+                    if (b_too) x = fmaf(__uint_as_float(o2[c]), fb[0], x);
+                    o[c] = lsum[0] == 0.f ? 0u : __float_as_uint(x * inv[0]);
+                }
+                if (rv[0] && whole) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t *x = o + 8 * c;
+                        auto f = [&](int i) { return __uint_as_float(x[i]); };
+                        orow[d / 8 + c] = make_uint4(pack_bf16x2(f(0), f(1)), pack_bf16x2(f(2), f(3)),
+                                                     pack_bf16x2(f(4), f(5)), pack_bf16x2(f(6), f(7)));
+                    }
+                } else if (rv[0]) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        po[(d / 4 + c) * kPair + row0] =
+                            make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                        __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+                }
+            }
+        } else {
+            // (halves) dims 8 k + 2 (lane % 4) and the next
+            uint32_t o[32], o2[32];
+            tc::tmem_ld_16x256b_x8(tmem + lane + 128 + d0, o);
+            if (b_too) tc::tmem_ld_16x256b_x8(tmem + lane + 384 + d0, o2);
+            tc::tmem_ld_wait();
+            const int pairs = (tid & 3) + d0 / 2;
+#pragma unroll
+            for (int x = 0; x < NR; ++x) {
+                const int row = row0 + 8 * x;
+                uint32_t *orow = reinterpret_cast<uint32_t *>(out_row(row)) + pairs;
+                float2 *prow = reinterpret_cast<float2 *>(po + (pairs >> 1) * kPair + row) + (pairs & 1);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float y[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        y[e] = __uint_as_float(o[4 * k + 2 * x + e]) * fa[x];
+                        if (b_too) y[e] = fmaf(__uint_as_float(o2[4 * k + 2 * x + e]), fb[x], y[e]);
+                        y[e] = lsum[x] == 0.f ? 0.f : y[e] * inv[x];
+                    }
+                    if (rv[x] && whole) orow[4 * k] = pack_bf16x2(y[0], y[1]);
+                    else if (rv[x]) prow[4 * k * kPair] = make_float2(y[0], y[1]);
+                }
+            }
+        }
+        const uint32_t odd = reaches_nodes(w, w.j1 - 1)
+            ? reinterpret_cast<volatile uint32_t *>(odd_marks)[st.piece % kOddSets] : 0u;
+        if (odd) {
+            __syncwarp();               // the row's lanes have written
+#pragma unroll 1
+            for (int x = 0; x < NR; ++x) {
+                const int row = row0 + 8 * x;
+                if (!first || !row_valid(row)) continue;
+                add_odd(a, odd, w.s, w.kvh, w.q.L - w.q.n, w.j0 * kKeys, min(w.j1 * kKeys, w.q.L),
+                        a.mask + ((int64_t)w.q.q0 + token(row)) * a.mask_words,
+                        whole ? reinterpret_cast<uint16_t *>(out_row(row)) : nullptr, po + row, d0, d1);
+            }
+        }
+    }
+    // the marks of the piece after the next: everybody has read those of the piece before the
+    // last, and nobody is there yet
+    if (tid == 0) reinterpret_cast<volatile uint32_t *>(odd_marks)[(st.piece + 2) % kOddSets] = 0u;
+    tc::fence_before_sync();
+    warp_arrive(bar(kBarOFree));
+    st.gt += ntt;
+    st.ga += nt;
+    ++st.piece;
+    return true;
 }
 
 // -- attention ---------------------------------------------------------------------
 
 template <int G>
 __global__ void __launch_bounds__(kThreads, 1)
-tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
+tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
             const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_q) {
     constexpr int BT = kRows / G;               // tokens per query tile
+    constexpr int BR = box_rows(G);
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
@@ -421,8 +866,10 @@ tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
     auto bar = [&](uint32_t i) { return ctl + 8 * i; };
     volatile int *abort = reinterpret_cast<volatile int *>(smem + kOffAbort);
     if (tid == 0) {
-        tc::mbar_init(bar(kBarQFull), 1);
-        tc::mbar_init(bar(kBarQEmpty), 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar(kBarQFull + i), 1);
+            tc::mbar_init(bar(kBarQEmpty + i), 1);
+        }
         for (int i = 0; i < kKStages; ++i) {
             tc::mbar_init(bar(kBarKFull + i), 1);
             tc::mbar_init(bar(kBarKEmpty + i), 1);
@@ -430,16 +877,17 @@ tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
         for (int i = 0; i < kVStages; ++i) {
             tc::mbar_init(bar(kBarVFull + i), 1);
             tc::mbar_init(bar(kBarVEmpty + i), 1);
-            tc::mbar_init(bar(kBarVLanded + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar(kBarSFull + i), 1);
             tc::mbar_init(bar(kBarPReady + i), kRows / 32);
             tc::mbar_init(bar(kBarPVDone + i), 1);
-            tc::mbar_init(bar(kBarOFree + i), kRows / 32);
         }
+        tc::mbar_init(bar(kBarOFree), kSoftmaxThreads / 32);
+        tc::mbar_init(bar(kBarHalves), kSoftmaxThreads / 32);
         tc::mbar_init(bar(kBarDrain), 1);
         *abort = 0;
+        for (int i = 0; i < kOddSets; ++i) reinterpret_cast<uint32_t *>(smem + kOffOdd)[i] = 0u;
         tc::fence_mbar_init();
     }
     if (warp == kMmaWarp) tc::tmem_alloc(sbase + kOffTmemSlot, kTmemCols);
@@ -454,7 +902,7 @@ tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
     int64_t W;
     int shares;
     Walk *walks = reinterpret_cast<Walk *>(smem + kOffWalk);
-    const bool works = plan_share<G>(a, walks, reinterpret_cast<volatile long long *>(smem + kOffSums), W, shares);
+    const bool works = plan_share<G>(a, walks, reinterpret_cast<volatile long long *>(smem + kOffHalves), W, shares);
     // the place of the first piece, for each warp its own
     {
         const Walk first = walks[0];
@@ -469,182 +917,16 @@ tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
         // more CTAs than shares, or a share of no tiles
     } else if (tid < kSoftmaxThreads) {
         // ---------------- softmax warpgroups ----------------
-        const int wg = tid >> 7, r = tid & 127;
-        const uint32_t lane = (uint32_t)(r & ~31) << 16;
-        const uint32_t tS = tmem + lane + wg * 256, tO = tS + 128;
-        const float sc = a.scale_log2;
-        // a masked score for the max: the value that loses whatever the scale's sign (masked
-        // keys then get p = 0 directly)
-        const float masked = sc >= 0.f ? -INFINITY : INFINITY;
-        uint32_t gt = 0;                        // this query tile's key tiles before this piece
-        int piece = 0;
+        Streams st;
         bool ok = true;
 #pragma unroll 1
         do {
-            const int ntt = piece_tiles<G>(w, wg);
-            const int tok = w.pair * 2 * BT + wg * BT + r / G;
-            const bool rv = tok < w.q.n && r % G < a.group;
-            // warps past the last row only take part in the hand-offs
-            const bool any = __any_sync(0xffffffffu, rv);
-            float m = -INFINITY, lsum = 0.f;
-#pragma unroll 1
-            for (int j = 0; j < ntt; ++j) {
-                const uint32_t gj = gt + j;
-                const int kb = (w.j0 + j) * kKeys;
-                const int b0 = kb - (w.q.L - w.q.n);            // node of the tile's first key
-                const bool need_mask = any && b0 + kKeys > 0;
-                uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-                if (need_mask) {
-                    uint32_t mw[5] = {};
-                    if (rv) {
-                        const uint32_t *row = a.mask + ((int64_t)w.q.q0 + tok) * a.mask_words;
-#pragma unroll
-                        for (int k = 0; k < 5; ++k) mw[k] = mask_word(row, a.mask_words, (b0 >> 5) + k);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        vis[k] = __funnelshift_r(mw[k], mw[k + 1], b0 & 31) & below(w.q.n, b0 + 32 * k);
-                }
-                // S_t(j) done: also PV_t(j - 1), issued before it, so O is stable
-                if (!warp_wait(bar(kBarSFull + wg), gj & 1, abort, true)) { ok = false; break; }
-                tc::fence_after_sync();
-                if (any) {
-                    uint32_t sr[4][32];
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) tc::tmem_ld32(tS + ch * 32, sr[ch]);
-                    tc::tmem_ld_wait();
-                    if (need_mask) {
-#pragma unroll
-                        for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!(vis[ch] >> c & 1)) sr[ch][c] = __float_as_uint(masked);
-                    }
-                    // the extreme raw score of the row, in four running values
-                    float e4[4] = {masked, masked, masked, masked};
-                    if (sc >= 0.f) {
-#pragma unroll
-                        for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-                            for (int c = 0; c < 32; c += 8)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    e4[k] = fmax3(e4[k], __uint_as_float(sr[ch][c + 2 * k]),
-                                                  __uint_as_float(sr[ch][c + 2 * k + 1]));
-                    } else {
-#pragma unroll
-                        for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-                            for (int c = 0; c < 32; c += 8)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    e4[k] = fmin3(e4[k], __uint_as_float(sr[ch][c + 2 * k]),
-                                                  __uint_as_float(sr[ch][c + 2 * k + 1]));
-                    }
-                    const float ext = sc >= 0.f ? fmax3(fmaxf(e4[0], e4[1]), e4[2], e4[3])
-                                                : fmin3(fminf(e4[0], e4[1]), e4[2], e4[3]);
-                    // every score of the row masked: no new max (also for scale 0)
-                    const float mt = ext == masked ? -INFINITY : ext * sc;
-                    // the max is raised only when a tile exceeds it by 2^8: weights stay below
-                    // 2^8, far inside fp32 and bf16 range, and O is rescaled rarely
-                    bool rescale = false;
-                    float alpha = 1.f;
-                    if (mt > m + kRescaleSlack) {
-                        rescale = m != -INFINITY;
-                        alpha = rescale ? ex2(m - mt) : 1.f;
-                        lsum *= alpha;
-                        m = mt;
-                    }
-                    const float mb = m == -INFINITY ? 0.f : m;
-                    // P = 2^(S sc - m), rounded to bf16 for the second product: its error of
-                    // 2^-9 per weight averages out over the keys, and the output is rounded
-                    // to bf16 as well
-                    float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t pw[16];
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            float p0 = ex2(fmaf(__uint_as_float(sr[ch][2 * c]), sc, -mb));
-                            float p1 = ex2(fmaf(__uint_as_float(sr[ch][2 * c + 1]), sc, -mb));
-                            if (need_mask) {
-                                p0 = vis[ch] >> (2 * c) & 1 ? p0 : 0.f;
-                                p1 = vis[ch] >> (2 * c + 1) & 1 ? p1 : 0.f;
-                            }
-                            l4[c & 3] += p0 + p1;
-                            pw[c] = pack_bf16x2(p0, p1);
-                        }
-                        tc::tmem_st16(tS + ch * 16, pw);
-                    }
-                    lsum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-                    if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll 1
-                        for (int ch = 0; ch < 4; ++ch) {
-                            uint32_t o[32];
-                            tc::tmem_ld32(tO + ch * 32, o);
-                            tc::tmem_ld_wait();
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-                            tc::tmem_st32(tO + ch * 32, o);
-                        }
-                    }
-                    tc::tmem_st_wait();
-                }
-                tc::fence_before_sync();
-                warp_arrive(bar(kBarPReady + wg));
+            switch (rows_per_warp<G>(w)) {
+                case 8: ok = softmax_piece<G, 1>(a, w, st, smem, sbase, tmem); break;
+                case 16: ok = softmax_piece<G, 2>(a, w, st, smem, sbase, tmem); break;
+                default: ok = softmax_piece<G, 0>(a, w, st, smem, sbase, tmem);
             }
-            if (!ok) break;
-            if (ntt > 0) {
-                if (!warp_wait(bar(kBarPVDone + wg), (gt + ntt - 1) & 1, abort, true)) { ok = false; break; }
-                tc::fence_after_sync();
-                if (any) {
-                    const bool whole = w.j0 == 0 && w.j1 == w.q.nt;
-                    // a row that saw nothing outputs zero, whatever its O
-                    const float inv = whole ? 1.f / lsum : 1.f;
-                    const int slot = 2 * w_id + (w.j0 == 0 ? 1 : 0);
-                    float4 *po = a.part_o + (int64_t)slot * 32 * kPair + wg * kRows + r;
-                    uint4 *orow = reinterpret_cast<uint4 *>(a.out) +
-                                  (((int64_t)w.q.q0 + tok) * a.num_q_heads + (int64_t)w.kvh * a.group + r % G) * (kHeadDim / 8);
-                    if (!whole && rv) a.part_ml[(int64_t)slot * kPair + wg * kRows + r] = make_float2(m, lsum);
-#pragma unroll 1
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t o[32];
-                        tc::tmem_ld32(tO + ch * 32, o);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            o[c] = lsum == 0.f ? 0u : __float_as_uint(__uint_as_float(o[c]) * inv);
-                        if (rv && whole) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint32_t *x = o + 8 * c;
-                                auto f = [&](int i) { return __uint_as_float(x[i]); };
-                                orow[ch * 4 + c] = make_uint4(pack_bf16x2(f(0), f(1)), pack_bf16x2(f(2), f(3)),
-                                                              pack_bf16x2(f(4), f(5)), pack_bf16x2(f(6), f(7)));
-                            }
-                        } else if (rv) {
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                po[(ch * 8 + c) * kPair] =
-                                    make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                                                __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
-                        }
-                    }
-                    const uint32_t *odd = reinterpret_cast<const uint32_t *>(smem + kOffOdd + (piece & 1) * kOddBytes);
-                    if (rv && reaches_nodes(w, w.j1 - 1) && odd[kMaskWords])
-                        add_odd(a, odd, w.s, w.kvh, w.q.L - w.q.n, a.mask + ((int64_t)w.q.q0 + tok) * a.mask_words,
-                                whole ? reinterpret_cast<uint16_t *>(orow) : nullptr, po);
-                }
-            }
-            // (only after a piece that the tile took part in: nobody waits for the others)
-            if (ntt > 0) {
-                tc::fence_before_sync();
-                warp_arrive(bar(kBarOFree + wg));
-            }
-            gt += ntt;
-            ++piece;
-        } while (walk_next<G>(w, a));
+        } while (ok && walk_next<G>(w, a));
     } else if (warp == kKWarp || warp == kVWarp) {
         // ---------------- K and V producers ----------------
         const bool is_v = warp == kVWarp;
@@ -657,26 +939,38 @@ tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
         const void *map = is_v ? static_cast<const void *>(&tmap_v) : static_cast<const void *>(&tmap_k);
         const int box = a.box_tokens, boxes = kKeys / box;
         uint32_t gt = 0;                            // tiles issued
-        int piece = 0, queries = 0;                 // pieces begun; pieces whose queries are issued
+        QBuffers qb;
         bool ok = true;
 #pragma unroll 1
         do {
             if (is_v) {
-                // the queries, once the previous piece's MMAs are done with the buffers
-                if (piece > 0 && !warp_wait(bar(kBarQEmpty), (piece - 1) & 1, abort)) { ok = false; break; }
-                if (lane == 0) {
-                    tc::mbar_expect_tx(bar(kBarQFull), 2 * kQBytes);
-                    for (int t = 0; t < 2; ++t)
-                        for (int hh = 0; hh < 2; ++hh)
-                            tc::tma_load_3d(sbase + kOffQ + t * kQBytes + hh * kQHalf, &tmap_q, hh * 64,
-                                            w.kvh * a.group, w.q.q0 + w.pair * 2 * BT + t * BT, bar(kBarQFull));
+                // the queries, once the products of the piece that had the buffer are done
+                const bool two = two_tiles<G>(w);
+                const int b0 = qb.take(two);
+                for (int t = 0; t <= (two ? 1 : 0) && ok; ++t) {
+                    const int b = b0 + t;
+                    if (qb.uses(b) > 1) ok = warp_wait(bar(kBarQEmpty + b), qb.uses(b) & 1, abort);
+                    if (!ok) {
+                        qb.drop(b);
+                        break;
+                    }
+                    // box q: rows BR q .. of the tile, in the first rq rows of every 32
+                    const int rq = rows_per_warp<G>(w), nq = 4 * rq / BR;
+                    if (lane == 0) tc::mbar_expect_tx(bar(kBarQFull + b), (uint32_t)(nq * 2 * BR * 128));
+                    __syncwarp();
+                    if (q < nq)
+                        tc::tma_load_3d(sbase + kOffQ + b * kQBytes + h * kQHalf +
+                                            (BR * q / rq * 32 + BR * q % rq) * 128,
+                                        &tmap_q, h * 64, w.kvh * a.group,
+                                        w.q.q0 + w.pair * 2 * BT + t * BT + BR * q / G, bar(kBarQFull + b));
+                    warp_arrive(bar(kBarQFull + b));
                 }
-                warp_arrive(bar(kBarQFull));
-                ++queries;
+                if (!ok) break;
                 // a unit that begins here and ends in another share: the combine's task
                 if (lane == 0 && w.j0 == 0 && w.j1 < w.q.nt) {
                     const int64_t end = w.T + w.q.nt;           // past the unit's last tile
-                    a.tasks[w_id] = make_int4(w.s, w.kvh, w.pair, (int)((end * shares - 1) / W));
+                    const int parts = (int)((end * shares - 1) / W) - w_id / w.lanes + 1;
+                    a.tasks[w_id] = make_int4(w.s, w.kvh, w.pair, parts | w.lanes << 16);
                 }
                 __syncwarp();
             }
@@ -704,8 +998,7 @@ tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
                 box_next = box_at(j + 1);
                 const int st = gt % nst;
                 if (!warp_wait(bar_empty + 8 * st, ((gt / nst) & 1) ^ 1, abort)) { ok = false; break; }
-                // a V tile that reaches the nodes is cleaned before it counts as there
-                const uint32_t full = is_v && reaches_nodes(w, j) ? bar(kBarVLanded + st) : bar_full + 8 * st;
+                const uint32_t full = bar_full + 8 * st;
                 const int n = __popc(__ballot_sync(0xffffffffu, at.x != INT_MIN));
                 if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)(n * box * 128));
                 __syncwarp();
@@ -715,12 +1008,12 @@ tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
                 if (!(is_v && a.fault_hold_v && gt == 0)) warp_arrive(full);
                 ++gt;
             }
-            ++piece;
         } while (ok && walk_next<G>(w, a));
         // the last fill of every stage, and the last queries, have landed
         for (uint32_t g = gt > (uint32_t)nst ? gt - nst : 0; g < gt; ++g)
             drain(bar_full + 8 * (g % nst), (g / nst) & 1);
-        if (queries > 0) drain(bar(kBarQFull), (queries - 1) & 1);
+        for (int b = 0; b < 2; ++b)
+            if (qb.uses(b) > 0) drain(bar(kBarQFull + b), (qb.uses(b) - 1) & 1);
     } else if (warp == kMmaWarp) {
         // ---------------- MMA issue ----------------
         const uint64_t dq = tc::sw128_desc(sbase + kOffQ, 16, 1024);        // K-major
@@ -729,8 +1022,10 @@ tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
         const uint32_t hi = (uint32_t)(dq >> 32);                           // same for all three
         const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, v_lo = (uint32_t)dv;
         auto desc = [hi](uint32_t lo) { return ((uint64_t)hi << 32) | lo; };
-        auto issue_s = [&](int t, int st, uint32_t release) {
-            const uint32_t qd = q_lo + t * (kQBytes >> 4);
+        const uint32_t idesc_s = kIdescS | (a.scale_log2 < 0.f ? kNegateA : 0u);
+        // S of stream t from query buffer b and K stage st
+        auto issue_s = [&](int t, int b, int st, uint32_t release) {
+            const uint32_t qd = q_lo + b * (kQBytes >> 4);
             const uint32_t kd = k_lo + st * (kKVBytes >> 4);
             const uint32_t d = tmem + t * 256;
             tc::fence_after_sync();
@@ -738,7 +1033,7 @@ tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
                 for (int kk = 0; kk < kHeadDim / 16; ++kk)
                     tc::mma_ss(d, desc(qd + (((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4)),
-                               desc(kd + (((kk >> 2) * kKVHalf + (kk & 3) * 32) >> 4)), kIdescS, kk > 0);
+                               desc(kd + (((kk >> 2) * kKVHalf + (kk & 3) * 32) >> 4)), idesc_s, kk > 0);
                 tc::commit(bar(kBarSFull + t));
                 if (release) tc::commit(release);
             }
@@ -758,111 +1053,53 @@ tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmap_k,
                 if (release) tc::commit(release);
             }
         };
-        // the warp polls, converged: the answer to every lane's test, bounded
-        auto await = [&](uint32_t b, uint32_t parity) {
-            uint64_t t0 = 0;
-            for (uint32_t i = 0;; ++i) {
-                if (__any_sync(0xffffffffu, tc::mbar_test_wait(b, parity))) {
-                    __syncwarp();
-                    return true;
-                }
-                if (i == 0) t0 = tc::globaltimer_ns();
-                if ((i & 255) == 255) {
-                    const bool stop = __shfl_sync(0xffffffffu,
-                                                  (*abort || tc::globaltimer_ns() - t0 > 2000000000ull) ? 1 : 0, 0) != 0;
-                    if (stop) {
-                        if ((threadIdx.x & 31) == 0 && !*abort) {
-                            set_error(kErrTimeout);
-                            *abort = 1;
-                        }
-                        return false;
-                    }
-                }
-            }
-        };
-        // In turn: PV_A(j), S_A(j + 1), PV_B(j), S_B(j + 1). PV_t(j) once P_t(j) is in TMEM
-        // (and, for the first of a piece, the previous piece's O has been read); the tiles it
-        // and S need have been waited for before, off the chain from P to S. A stage is
-        // released after its last reader.
-        uint32_t gt = 0, gq0 = 0, gq1 = 0;
-        int piece = 0, pieces_b = 0;            // pieces before this one; those that had a tile B
+        auto await = [&](uint32_t b, uint32_t parity) { return warp_wait(b, parity, abort, true); };
+        // Step i is of stream i % 2: of two query tiles over key tile i / 2, of halves over key
+        // tile i. In turn: PV of step i once its P is in TMEM (and, for the first of a piece,
+        // the previous piece's results have been read), then S of step i + 2. The tiles they
+        // need have been waited for before, off the chain from P to S. A stage is released
+        // after its last reader.
+        uint32_t gt = 0, gq0 = 0, gq1 = 0;      // key tiles before this piece, of all and of each stream
+        int piece = 0;
+        QBuffers qb;
         bool ok = true;
 #pragma unroll 1
         do {
             const int nt = w.j1 - w.j0;
-            const bool two = piece_tiles<G>(w, 1) > 0;
-            ok = await(bar(kBarQFull), piece & 1) && await(bar(kBarKFull + gt % kKStages), (gt / kKStages) & 1);
-            if (ok) {
-                issue_s(0, gt % kKStages, two ? 0u : bar(kBarKEmpty + gt % kKStages));
-                if (two) issue_s(1, gt % kKStages, bar(kBarKEmpty + gt % kKStages));
-            }
+            const bool two = two_tiles<G>(w);
+            const int shift = two ? 1 : 0, steps = nt << shift;
+            const int b0 = qb.take(two);
+            ok = await(bar(kBarQFull + b0), (qb.uses(b0) - 1) & 1);
+            if (ok && two) ok = await(bar(kBarQFull + 1), (qb.uses(1) - 1) & 1);
 #pragma unroll 1
-            for (int j = 0; ok && j < nt; ++j) {
-                const uint32_t gp = gt + j, gs = gp + 1;
+            for (int i = -2; ok && i < steps; ++i) {
+                const int t = i & 1, j = i >> shift;
+                const bool last = !two || t == 1;               // reader of its tiles
+                const uint32_t gp = gt + j, gs = gt + ((i + 2) >> shift);
                 const int vs = gp % kVStages, ks = gs % kKStages;
-                const bool more = j + 1 < nt;
-                const int nv = groups_used(w, w.j0 + j);
-                ok = await(bar(kBarVFull + vs), (gp / kVStages) & 1);
+                const bool more = i + 2 < steps;
+                if (i >= 0) ok = await(bar(kBarVFull + vs), (gp / kVStages) & 1);
                 if (ok && more) ok = await(bar(kBarKFull + ks), (gs / kKStages) & 1);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (t == 1 && !two) break;
-                    const bool last = t == 1 || !two;
-                    if (ok && j == 0 && t == 0) {
-                        // the results of the last piece of either tile are read (of B's also where
-                        // this piece has no B: the marks of clean_v are free with them)
-                        if (piece > 0) ok = await(bar(kBarOFree), (piece - 1) & 1);
-                        if (ok && pieces_b > 0) ok = await(bar(kBarOFree + 1), (pieces_b - 1) & 1);
-                    }
-                    if (ok) ok = await(bar(kBarPReady + t), ((t == 0 ? gq0 : gq1) + j) & 1);
-                    if (!ok) break;
-                    issue_pv(t, vs, j > 0, nv, last ? bar(kBarVEmpty + vs) : 0u);
-                    if (more) issue_s(t, ks, last ? bar(kBarKEmpty + ks) : 0u);
-                }
+                if (ok && i == 0 && piece > 0) ok = await(bar(kBarOFree), (piece - 1) & 1);
+                if (ok && i >= 0) ok = await(bar(kBarPReady + t), ((t == 0 ? gq0 : gq1) + (i >> 1)) & 1);
+                if (!ok) break;
+                if (i >= 0) issue_pv(t, vs, i > 1, groups_used(w, w.j0 + j), last ? bar(kBarVEmpty + vs) : 0u);
+                if (more) issue_s(t, two ? t : b0, ks, last ? bar(kBarKEmpty + ks) : 0u);
             }
             // the queries' buffers are free once this piece's MMAs are done
-            if (ok && tc::elect_one()) tc::commit(bar(kBarQEmpty));
+            if (ok && tc::elect_one()) {
+                tc::commit(bar(kBarQEmpty + b0));
+                if (two) tc::commit(bar(kBarQEmpty + 1));
+            }
             __syncwarp();
             gt += nt;
-            gq0 += nt;
-            gq1 += two ? nt : 0;
-            pieces_b += two ? 1 : 0;
+            gq0 += stream_tiles(nt, two, 0);
+            gq1 += stream_tiles(nt, two, 1);
             ++piece;
         } while (ok && walk_next<G>(w, a));
         if (tc::elect_one()) tc::commit(bar(kBarDrain));
         __syncwarp();
         drain(bar(kBarDrain), 0);
-    }
-
-    if (works && warp == kCleanWarp) {
-        // ---------------- cleaning of V tiles ----------------
-        uint32_t gt = 0, landed = 0;                // tiles before this piece; bit i: parity of stage i's next phase
-        int piece = 0;
-        bool ok = true;
-#pragma unroll 1
-        do {
-            bool fresh = true;
-            uint32_t *odd = reinterpret_cast<uint32_t *>(smem + kOffOdd + (piece & 1) * kOddBytes);
-#pragma unroll 1
-            for (int j = w.j0; j < w.j1; ++j) {
-                if (!reaches_nodes(w, j)) continue;
-                const int st = (gt + (j - w.j0)) % kVStages;
-                if (!warp_wait(bar(kBarVLanded + st), landed >> st & 1, abort)) { ok = false; break; }
-                landed ^= 1u << st;
-                if (fresh) {
-                    // the V warp begins a piece once the products of the one before are done,
-                    // and those wait for the results of the one before that: its marks are read
-                    fresh = false;
-                    for (int i = tid & 31; i <= kMaskWords; i += 32) odd[i] = 0u;
-                    __syncwarp();
-                }
-                clean_v(w, j, sbase + kOffV + st * kKVBytes, odd, a.mask_words, tid & 31);
-                tc::fence_proxy_async();
-                warp_arrive(bar(kBarVFull + st));
-            }
-            gt += w.j1 - w.j0;
-            ++piece;
-        } while (ok && walk_next<G>(w, a));
     }
 
     // teardown: every role is done (or has given up) and has nothing in flight; TMEM is freed
@@ -885,12 +1122,13 @@ __global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const T
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int w = blockIdx.x, r = blockIdx.y * kCombineRows + (threadIdx.x & 7), c = threadIdx.x >> 3;
     const int4 task = a.tasks[w];
-    // after a wait that ran out the task may be of shares that wrote nothing; what is read lies in the workspace
-    if (task.x < 0 || task.w <= w || task.w >= a.workers) return;
+    if (task.x < 0) return;
+    // share by share of the lane; what is read lies in the workspace
+    const int parts = task.w & 0xffff, lanes = task.w >> 16;
+    if (w + (parts - 1) * lanes >= a.workers) return;
     const Seq q = load_seq<G>(a, task.x);
     const int tok = task.z * (kPair / G) + r / G, head = r % G;
     if (tok >= q.n || head >= a.group) return;
-    const int parts = task.w - w + 1;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < parts; i0 += kCombineBatch) {
@@ -900,7 +1138,7 @@ __global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const T
         for (int k = 0; k < kCombineBatch; ++k) {
             const int i = i0 + k;
             if (i < parts) {
-                const int64_t slot = i == 0 ? 2 * w + 1 : 2 * (w + i);
+                const int64_t slot = i == 0 ? 2 * w + 1 : 2 * (w + i * lanes);
                 e[k] = a.part_ml[slot * kPair + r];
                 x[k] = a.part_o[(slot * 32 + c) * kPair + r];
             }
@@ -924,14 +1162,14 @@ __global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const T
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
-// q [total_q, Hq, 128] as (128, Hq, total_q) with boxes of 64 dims x G heads x 128 / G
-// tokens: one half of a 128-row query tile.
+// q [total_q, Hq, 128] as (128, Hq, total_q) with boxes of 64 dims x G heads x
+// box_rows(G) / G tokens.
 bool make_q_map(CUtensorMap *m, const void *q, int total_q, int num_q_heads, int G) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)num_q_heads, (cuuint64_t)total_q};
     const cuuint64_t strides[2] = {(cuuint64_t)kRowBytes, (cuuint64_t)num_q_heads * kRowBytes};
-    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(kRows / G)};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(box_rows(G) / G)};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
