@@ -49,7 +49,9 @@ extern "C" {
  *
  * Requirements: pa_decode's for heads, blocks, pools and alignment (either layout);
  * 1 <= mask_words <= PA_TREE_MAX_WORDS; tree_mask 8-byte aligned; total_q * num_q_heads
- * below 2^31; tables of at most 2^31 - 128 tokens; a workspace of
+ * below 2^31; tables of at most 2^31 - 128 tokens, and (num_seqs + total_q * g / 256) *
+ * num_kv_heads * (tokens of a table / 128 + 8) below 2^31, with g the group size rounded
+ * up to a power of two; a workspace of
  * pa_decode_tree_workspace_size(...) bytes, 16-byte aligned.
  */
 PA_API size_t pa_decode_tree_workspace_size(int num_q_heads, int num_kv_heads, int head_dim);

@@ -88,7 +88,7 @@ constexpr uint32_t kBarDrain = kBarHalves + 1;           // all products issued 
 constexpr uint32_t kNumBars = kBarDrain + 1;
 constexpr uint32_t kOffTmemSlot = kOffCtl + 8 * kNumBars;
 constexpr uint32_t kOffAbort = kOffTmemSlot + 4;
-constexpr uint32_t kWalkBytes = 64;
+constexpr uint32_t kWalkBytes = 56;
 constexpr uint32_t kOffWalk = (kOffAbort + 4 + 15) & ~15u;        // one Walk per warp
 constexpr int kOddSets = 4;                                       // of the pieces in flight: bit i, nodes 32 i ..
 constexpr uint32_t kOffOdd = kOffWalk + kWalkBytes * kWarpsAll;   // 32 i + 31 have V that is not finite
@@ -133,7 +133,7 @@ __device__ __noinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile in
 }
 
 // Nothing a role has issued outlives it.
-__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+__device__ __noinline__ void drain(uint32_t bar, uint32_t parity) {
     if (!tc::drain_bar(bar, parity)) set_error(kErrTimeout);
 }
 
@@ -201,17 +201,17 @@ __device__ __noinline__ Seq load_seq(const TreeArgs &a, int s) {
     return r;
 }
 
-// Places of a sequence's units in one of `lanes` lanes.
-__device__ __forceinline__ int64_t seq_places(const Seq &q, int num_kv_heads, int lanes) {
-    return (int64_t)(q.pairs / lanes) * num_kv_heads * (q.nt + kUnitPlaces);
+// Places of a sequence's units in one of `lanes` lanes. (The host has ruled out 2^31 places.)
+__device__ __forceinline__ int seq_places(const Seq &q, int num_kv_heads, int lanes) {
+    return q.pairs / lanes * num_kv_heads * (q.nt + kUnitPlaces);
 }
 
 // A share's walk over the flat space of its lane, sequence by sequence, KV head, pair, key
 // tile: its pieces are runs of key tiles [j0, j1) of one unit. Every warp walks by itself
 // and keeps its place in shared memory, where the fields are read when they are needed:
 // none stays live across the tile loop.
-struct alignas(16) Walk {
-    int64_t T, T1;      // place of tile j0, end of the share
+struct Walk {
+    int T, T1;          // place of tile j0, end of the share
     Seq q;
     int s, kvh, pair, j0, j1;
     int lane, lanes;
@@ -219,13 +219,13 @@ struct alignas(16) Walk {
 static_assert(sizeof(Walk) == kWalkBytes, "Walk");
 
 __device__ __forceinline__ void piece_end(Walk &w) {
-    const int64_t left = w.T1 - w.T;
-    w.j1 = w.q.nt - w.j0 < left ? w.q.nt : w.j0 + (int)left;
+    const int left = w.T1 - w.T;
+    w.j1 = w.q.nt - w.j0 < left ? w.q.nt : w.j0 + left;
 }
 
 // On to the next unit; false at the end of the share.
 template <int G>
-__device__ __forceinline__ bool next_unit(Walk &w, const TreeArgs &a) {
+__device__ __noinline__ bool next_unit(Walk &w, const TreeArgs &a) {
     w.T += w.q.nt - w.j0 + kUnitPlaces;
     if (w.T >= w.T1) return false;
     w.j0 = 0;
@@ -252,98 +252,99 @@ __device__ __noinline__ bool walk_next(volatile Walk &place, const TreeArgs &a) 
     return more;
 }
 
+// Where share i of `shares` begins among W places: floor(i W / shares).
+__device__ __forceinline__ int share_begin(int i, int W, int shares) {
+    const int each = W / shares;
+    return i * each + i * (W - each * shares) / shares;
+}
+
+// The share that place T is in: a guess, which is off by one at most.
+__device__ __forceinline__ int share_of(int T, int W, int shares) {
+    int i = (int)(__fdividef((float)T, (float)W) * (float)shares);
+    while (share_begin(i, W, shares) > T) --i;
+    while (share_begin(i + 1, W, shares) <= T) ++i;
+    return i;
+}
+
 // The places of a lane, its shares, and this CTA's first piece (in `first`, shared memory);
-// false when it has none. All threads call it.
+// false when it has none. All threads call it; `sums` is scratch.
 template <int G>
-__device__ __noinline__ bool plan_share(const TreeArgs &a, Walk *first, volatile long long *sums,
-                                           int64_t &W, int &shares) {
+__device__ __noinline__ bool plan_share(const TreeArgs &a, Walk *first, volatile int *sums, int &W, int &shares) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = a.num_seqs, Hkv = a.num_kv_heads;
     Seq mine{};
-    if (tid < S) mine = load_seq<G>(a, tid);
-    long long all = 0, one = 0;                 // places of all pairs, and of one pair a unit
-    int most = 0, least = INT_MAX;              // pairs of a sequence
+    unsigned all = 0, one = 0;                  // places of all pairs, and of one pair a unit
+    unsigned most = 0, least = INT_MAX;         // pairs of a sequence
+#pragma unroll 1
     for (int s = tid; s < S; s += kThreads) {
-        const Seq q = s == tid ? mine : load_seq<G>(a, s);
+        const Seq q = load_seq<G>(a, s);
+        if (s == tid) mine = q;
         if (q.pairs == 0) continue;
         all += seq_places(q, Hkv, 1);
         one += seq_places(q, Hkv, q.pairs);
-        most = q.pairs > most ? q.pairs : most;
-        least = q.pairs < least ? q.pairs : least;
+        most = max(most, q.pairs);
+        least = min(least, q.pairs);
     }
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, m);
-        one += __shfl_xor_sync(0xffffffffu, one, m);
-    }
+    all = __reduce_add_sync(0xffffffffu, all);
+    one = __reduce_add_sync(0xffffffffu, one);
     most = __reduce_max_sync(0xffffffffu, most);
     least = __reduce_min_sync(0xffffffffu, least);
     if (lane == 0) {
         sums[warp] = all;
-        sums[kWarpsAll + warp] = one;
-        sums[2 * kWarpsAll + warp] = (long long)most << 32 | least;
+        sums[32 + warp] = one;
+        sums[64 + warp] = most;
+        sums[96 + warp] = least;
     }
-    __syncthreads();
-    all = one = 0;
-    for (int i = 0; i < kWarpsAll; ++i) {
-        all += sums[i];
-        one += sums[kWarpsAll + i];
-        const long long x = sums[2 * kWarpsAll + i];
-        most = (int)(x >> 32) > most ? (int)(x >> 32) : most;
-        least = (int)x < least ? (int)x : least;
-    }
-    __syncthreads();
-    // where all have the same number of pairs, the pairs are lanes
-    const int lanes = most == least && most <= a.workers ? most : 1;
-    W = lanes > 1 ? one : all;
-    const int64_t p = W / kMinPlaces, cap = a.workers / lanes;
-    shares = (int)(p < 1 ? 1 : (p > cap ? cap : p));
-    const int mine_lane = blockIdx.x % lanes, w = blockIdx.x / lanes;
-    if (w >= shares || W == 0) return false;
-    const int64_t T0 = (int64_t)w * W / shares, T1 = (int64_t)(w + 1) * W / shares;
     if (tid == 0) first->T1 = -1;               // nothing found yet
-    int64_t base = 0;
+    __syncthreads();
+    // every warp adds up all warps' sums
+    const bool mine_too = lane < kWarpsAll;
+    all = __reduce_add_sync(0xffffffffu, mine_too ? sums[lane] : 0);
+    one = __reduce_add_sync(0xffffffffu, mine_too ? sums[32 + lane] : 0);
+    most = __reduce_max_sync(0xffffffffu, mine_too ? sums[64 + lane] : 0);
+    least = __reduce_min_sync(0xffffffffu, mine_too ? sums[96 + lane] : INT_MAX);
+    // where all have the same number of pairs, the pairs are lanes
+    const int lanes = most == least && (int)most <= a.workers ? most : 1;
+    W = lanes > 1 ? one : all;
+    shares = max(1, min(W / kMinPlaces, a.workers / lanes));
+    const int w = blockIdx.x / lanes;
+    if (w >= shares || W == 0) return false;
+    const int T0 = share_begin(w, W, shares);
+    int base = 0;
+#pragma unroll 1
     for (int c0 = 0; c0 < S && base <= T0; c0 += kThreads) {
         const int s = c0 + tid;
-        const Seq q = c0 == 0 ? mine : (s < S ? load_seq<G>(a, s) : Seq{});
-        const long long own = s < S ? seq_places(q, Hkv, lanes) : 0;
-        long long v = own;
+        if (c0 > 0 && s < S) mine = load_seq<G>(a, s);
+        const int own = s < S ? seq_places(mine, Hkv, lanes) : 0;
+        int v = own;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const long long n = __shfl_up_sync(0xffffffffu, v, off);
+            const int n = __shfl_up_sync(0xffffffffu, v, off);
             if (lane >= off) v += n;
         }
+        __syncthreads();                        // the sums before have been read
         if (lane == 31) sums[warp] = v;
         __syncthreads();
-        long long before = base, end = base;
-        for (int i = 0; i < kWarpsAll; ++i) {
-            if (i < warp) before += sums[i];
-            end += sums[i];
-        }
-        const long long excl = before + v - own;
+        const int x = mine_too ? sums[lane] : 0;
+        const int excl = base + v - own + __reduce_add_sync(0xffffffffu, (unsigned)(lane < warp ? x : 0));
         if (own > 0 && T0 >= excl && T0 < excl + own) {
-            Walk k;
-            const int64_t rem = T0 - excl;
-            const int places = q.nt + kUnitPlaces, per_head = q.pairs / lanes;
-            const int64_t unit = rem / places;
-            k.T = T0;
-            k.T1 = T1;
-            k.q = q;
-            k.s = s;
-            k.lane = mine_lane;
-            k.lanes = lanes;
-            k.kvh = (int)(unit / per_head);
-            k.pair = mine_lane + lanes * (int)(unit - (int64_t)k.kvh * per_head);
-            k.j0 = (int)(rem - unit * places);
-            bool works = true;
-            if (k.j0 >= q.nt) works = next_unit<G>(k, a);     // past the unit's tiles
-            else piece_end(k);
-            if (!works) k.T1 = -1;
-            *first = k;
+            const int rem = T0 - excl, places = mine.nt + kUnitPlaces, per_head = mine.pairs / lanes;
+            const int unit = rem / places;
+            first->T = T0;
+            first->T1 = share_begin(w + 1, W, shares);
+            first->q = mine;
+            first->s = s;
+            first->lane = blockIdx.x % lanes;
+            first->lanes = lanes;
+            first->kvh = unit / per_head;
+            first->pair = first->lane + lanes * (unit % per_head);
+            first->j0 = rem - unit * places;
+            if (first->j0 < mine.nt) piece_end(*first);
+            else if (!next_unit<G>(*first, a)) first->T1 = -1;      // past the unit's tiles
         }
-        base = end;
-        __syncthreads();
+        base += __reduce_add_sync(0xffffffffu, (unsigned)x);
     }
+    __syncthreads();
     return first->T1 >= 0;
 }
 
@@ -511,43 +512,66 @@ __device__ __forceinline__ float raise_max(float most, float sc, float &m, float
     return alpha;
 }
 
-// A thread per row: 128 scores of its TMEM lane.
+// A thread per row: 128 scores of its TMEM lane, 32 at a time, once for the maximum and
+// again for the weights: held all at once they take four times the code.
 __device__ __forceinline__ void wide_tile(uint32_t tS, uint32_t tO, float sc, bool nodes,
                                           const uint32_t (&vis)[4], float &m, float &lsum) {
-    uint32_t sr[4][32];
-#pragma unroll
-    for (int ch = 0; ch < 4; ++ch) tc::tmem_ld32(tS + ch * 32, sr[ch]);
-    tc::tmem_ld_wait();
+    float e[2] = {-INFINITY, -INFINITY};
+    uint32_t sr[2][32];
+    tc::tmem_ld32(tS, sr[0]);
     if (nodes) {
+        uint32_t v0 = vis[0], v1 = vis[1], v2 = vis[2], v3 = vis[3];
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+            tc::tmem_ld32(tS + 32 * ch, sr[0]);
+            tc::tmem_ld_wait();
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch)
+            for (int c = 0; c < 32; ++c) {
+                if (!(v0 >> c & 1)) sr[0][c] = kMasked;
+                e[c & 1] = fmaxf(e[c & 1], __uint_as_float(sr[0][c]));
+            }
+            tc::tmem_st32(tS + 32 * ch, sr[0]);
+            v0 = v1;
+            v1 = v2;
+            v2 = v3;
+        }
+        tc::tmem_st_wait();
+    } else {
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ch += 2) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-                if (!(vis[ch] >> c & 1)) sr[ch][c] = kMasked;
+            for (int h = 0; h < 2; ++h) {
+                tc::tmem_ld_wait();
+                if (ch + h < 3) tc::tmem_ld32(tS + 32 * (ch + h + 1), sr[h ^ 1]);
+#pragma unroll
+                for (int c = 0; c < 32; c += 4)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        e[k] = fmax3(e[k], __uint_as_float(sr[h][c + 2 * k]), __uint_as_float(sr[h][c + 2 * k + 1]));
+            }
+        }
     }
-    // in four running values
-    float e4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-    for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-        for (int c = 0; c < 32; c += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                e4[k] = fmax3(e4[k], __uint_as_float(sr[ch][c + 2 * k]), __uint_as_float(sr[ch][c + 2 * k + 1]));
-    const float alpha = raise_max(fmax3(fmaxf(e4[0], e4[1]), e4[2], e4[3]), sc, m, lsum);
+    tc::tmem_ld32(tS, sr[0]);
+    const float alpha = raise_max(fmaxf(e[0], e[1]), sc, m, lsum);
     const float mb = m == -INFINITY ? 0.f : m;
     float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ch += 2) {
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch) {
-        uint32_t pw[16];
+        for (int h = 0; h < 2; ++h) {
+            tc::tmem_ld_wait();
+            if (ch + h < 3) tc::tmem_ld32(tS + 32 * (ch + h + 1), sr[h ^ 1]);
+            uint32_t pw[16];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            const float p0 = ex2(fmaf(__uint_as_float(sr[ch][2 * c]), sc, -mb));
-            const float p1 = ex2(fmaf(__uint_as_float(sr[ch][2 * c + 1]), sc, -mb));
-            l4[c & 3] += p0 + p1;
-            pw[c] = pack_bf16x2(p0, p1);
+            for (int c = 0; c < 16; ++c) {
+                const float p0 = ex2(fmaf(__uint_as_float(sr[h][2 * c]), sc, -mb));
+                const float p1 = ex2(fmaf(__uint_as_float(sr[h][2 * c + 1]), sc, -mb));
+                l4[c & 3] += p0 + p1;
+                pw[c] = pack_bf16x2(p0, p1);
+            }
+            // over columns that have been read
+            tc::tmem_st16(tS + (ch + h) * 16, pw);
         }
-        tc::tmem_st16(tS + ch * 16, pw);
     }
     lsum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
     if (__any_sync(0xffffffffu, alpha != 1.f)) {
@@ -625,6 +649,16 @@ __device__ __forceinline__ void narrow_tile(uint32_t tS, uint32_t tO, float sc, 
         }
     }
     tc::tmem_st_wait();
+}
+
+// An element of a result from those of both streams; a row that saw nothing outputs zero,
+// whatever its O. (A second O that is not there may be anything.)
+__device__ __forceinline__ float merged(uint32_t o, uint32_t o2, float fa, bool b_too, float fb, float lsum, float inv) {
+    const float x = __uint_as_float(o) * fa, y = fmaf(__uint_as_float(o2), fb, x);
+    return lsum == 0.f ? 0.f : (b_too ? y : x) * inv;
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
 // What a softmax warp counts over its pieces.
@@ -751,7 +785,6 @@ __device__ __forceinline__ bool softmax_piece(const TreeArgs &a, const volatile 
         const int slot = 2 * (int)blockIdx.x + (w.j0 == 0 ? 1 : 0);
         float4 *po = a.part_o + (int64_t)slot * 32 * kPair + tile * kRows;
         const int d0 = two ? 0 : 64 * wg, d1 = two ? kHeadDim : d0 + 64;
-        // a row that saw nothing outputs zero, whatever its O
         float inv[NR];
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
@@ -762,56 +795,43 @@ __device__ __forceinline__ bool softmax_piece(const TreeArgs &a, const volatile 
         if constexpr (R == 0) {
             uint4 *orow = out_row(row0);
 #pragma unroll 1
-            for (int d = d0; d < d1; d += 32) {
-                uint32_t o[32], o2[32];
-                tc::tmem_ld32((two ? tO : tmem + lane + 128) + d, o);
-                if (b_too) tc::tmem_ld32(tmem + lane + 384 + d, o2);
+            for (int d = d0; d < d1; d += 8) {
+                uint32_t o[8], o2[8];
+                tc::tmem_ld8((two ? tO : tmem + lane + 128) + d, o);
+                tc::tmem_ld8(tmem + lane + 384 + d, o2);
                 tc::tmem_ld_wait();
+                float y[8];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    float x = __uint_as_float(o[c]) * fa[0];
-                    if (b_too) x = fmaf(__uint_as_float(o2[c]), fb[0], x);
-                    o[c] = lsum[0] == 0.f ? 0u : __float_as_uint(x * inv[0]);
-                }
+                for (int c = 0; c < 8; ++c) y[c] = merged(o[c], o2[c], fa[0], b_too, fb[0], lsum[0], inv[0]);
                 if (rv[0] && whole) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t *x = o + 8 * c;
-                        auto f = [&](int i) { return __uint_as_float(x[i]); };
-                        orow[d / 8 + c] = make_uint4(pack_bf16x2(f(0), f(1)), pack_bf16x2(f(2), f(3)),
-                                                     pack_bf16x2(f(4), f(5)), pack_bf16x2(f(6), f(7)));
-                    }
+                    orow[d / 8] = pack(y);
                 } else if (rv[0]) {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        po[(d / 4 + c) * kPair + row0] =
-                            make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                                        __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+                    po[(d / 4) * kPair + row0] = make_float4(y[0], y[1], y[2], y[3]);
+                    po[(d / 4 + 1) * kPair + row0] = make_float4(y[4], y[5], y[6], y[7]);
                 }
             }
         } else {
-            // (halves) dims 8 k + 2 (lane % 4) and the next
-            uint32_t o[32], o2[32];
-            tc::tmem_ld_16x256b_x8(tmem + lane + 128 + d0, o);
-            if (b_too) tc::tmem_ld_16x256b_x8(tmem + lane + 384 + d0, o2);
-            tc::tmem_ld_wait();
-            const int pairs = (tid & 3) + d0 / 2;
+            // (halves) dims d + 2 (lane % 4) and the next
+            uint32_t *orow[NR];
+            float2 *prow[NR];
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
-                const int row = row0 + 8 * x;
-                uint32_t *orow = reinterpret_cast<uint32_t *>(out_row(row)) + pairs;
-                float2 *prow = reinterpret_cast<float2 *>(po + (pairs >> 1) * kPair + row) + (pairs & 1);
+                const int pairs = (tid & 3) + d0 / 2;
+                orow[x] = reinterpret_cast<uint32_t *>(out_row(row0 + 8 * x)) + pairs;
+                prow[x] = reinterpret_cast<float2 *>(po + (pairs >> 1) * kPair + row0 + 8 * x) + (pairs & 1);
+            }
+#pragma unroll 1
+            for (int d = 0; d < 64; d += 8) {
+                uint32_t o[4], o2[4];
+                tc::tmem_ld_16x256b_x1(tmem + lane + 128 + d0 + d, o);
+                tc::tmem_ld_16x256b_x1(tmem + lane + 384 + d0 + d, o2);
+                tc::tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float y[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        y[e] = __uint_as_float(o[4 * k + 2 * x + e]) * fa[x];
-                        if (b_too) y[e] = fmaf(__uint_as_float(o2[4 * k + 2 * x + e]), fb[x], y[e]);
-                        y[e] = lsum[x] == 0.f ? 0.f : y[e] * inv[x];
-                    }
-                    if (rv[x] && whole) orow[4 * k] = pack_bf16x2(y[0], y[1]);
-                    else if (rv[x]) prow[4 * k * kPair] = make_float2(y[0], y[1]);
+                for (int x = 0; x < NR; ++x) {
+                    const float y0 = merged(o[2 * x], o2[2 * x], fa[x], b_too, fb[x], lsum[x], inv[x]);
+                    const float y1 = merged(o[2 * x + 1], o2[2 * x + 1], fa[x], b_too, fb[x], lsum[x], inv[x]);
+                    if (rv[x] && whole) orow[x][d / 2] = pack_bf16x2(y0, y1);
+                    else if (rv[x]) prow[x][d / 2 * kPair] = make_float2(y0, y1);
                 }
             }
         }
@@ -899,10 +919,9 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
     // programmatic dependent of whatever precedes the call
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    int64_t W;
-    int shares;
+    int W, shares;
     Walk *walks = reinterpret_cast<Walk *>(smem + kOffWalk);
-    const bool works = plan_share<G>(a, walks, reinterpret_cast<volatile long long *>(smem + kOffHalves), W, shares);
+    const bool works = plan_share<G>(a, walks, reinterpret_cast<volatile int *>(smem + kOffHalves), W, shares);
     // the place of the first piece, for each warp its own
     {
         const Walk first = walks[0];
@@ -968,8 +987,7 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
                 if (!ok) break;
                 // a unit that begins here and ends in another share: the combine's task
                 if (lane == 0 && w.j0 == 0 && w.j1 < w.q.nt) {
-                    const int64_t end = w.T + w.q.nt;           // past the unit's last tile
-                    const int parts = (int)((end * shares - 1) / W) - w_id / w.lanes + 1;
+                    const int parts = share_of(w.T + w.q.nt - 1, W, shares) - w_id / w.lanes + 1;
                     a.tasks[w_id] = make_int4(w.s, w.kvh, w.pair, parts | w.lanes << 16);
                 }
                 __syncwarp();
@@ -1010,8 +1028,10 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
             }
         } while (ok && walk_next<G>(w, a));
         // the last fill of every stage, and the last queries, have landed
+#pragma unroll 1
         for (uint32_t g = gt > (uint32_t)nst ? gt - nst : 0; g < gt; ++g)
             drain(bar_full + 8 * (g % nst), (g / nst) & 1);
+#pragma unroll 1
         for (int b = 0; b < 2; ++b)
             if (qb.uses(b) > 0) drain(bar(kBarQFull + b), (qb.uses(b) - 1) & 1);
     } else if (warp == kMmaWarp) {
