@@ -297,7 +297,7 @@ pa_status_t rotate_args(pa::RotateArgs &a, bool *interleaved, const void *q, int
     if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads < 0 || !std::isfinite(eps) || eps < 0.f)
         return PA_ERR_INVALID_ARG;
     if (head_dim != pa::kHeadDimPublic) return PA_ERR_UNSUPPORTED;
-    if ((int64_t)num_q_heads + num_kv_heads > (1 << 20)) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)num_q_heads + num_kv_heads > (1 << 20) || num_tokens > INT32_MAX) return PA_ERR_UNSUPPORTED;
     if (rotary) {
         if (!std::isfinite(rotary->amplitude)) return PA_ERR_INVALID_ARG;
         if (rotary->rot_dim < 16 || rotary->rot_dim > head_dim || rotary->rot_dim % 16 != 0)

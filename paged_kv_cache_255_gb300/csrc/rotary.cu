@@ -18,6 +18,7 @@
 // and cosines of a token are computed once per warp, two pairs a lane, handed round
 // by shuffles, and used for all heads the warp takes.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstring>
 
@@ -33,153 +34,215 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kChunks = kHeadDim / 8;       // 16-byte chunks of a row
-constexpr int kBatch = 2;                   // quads of heads whose loads are in flight together
+constexpr int kCtasPerSm = 6;
+constexpr int kDepth = 4;                   // quads of rows a warp has on their way
 
-__device__ __forceinline__ void unpack(const uint4 &w, float (&f)[8]) {
-    f[0] = bf16_lo(w.x);
-    f[1] = bf16_hi(w.x);
-    f[2] = bf16_lo(w.y);
-    f[3] = bf16_hi(w.y);
-    f[4] = bf16_lo(w.z);
-    f[5] = bf16_hi(w.z);
-    f[6] = bf16_lo(w.w);
-    f[7] = bf16_hi(w.w);
+// Two floats that one instruction works on (the kernel is bound by its issue slots before
+// it is by memory: with scalar arithmetic 16384 prompt rows of 40 heads took
+// 57.8 us, of which the bytes alone are 49).
+struct Two {
+    float x, y;
+};
+__device__ __forceinline__ uint64_t bits(Two v) {
+    return (uint64_t)__float_as_uint(v.x) | (uint64_t)__float_as_uint(v.y) << 32;
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ Two two(uint64_t b) {
+    return Two{__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32))};
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return two(r);
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return two(r);
 }
 
-enum Kind { kQuery, kKey, kValue };
+// The 8 pairs (a, b) of a lane's two chunks, two pairs to a Two, and back. Interleaved pairs
+// are the words of the chunks; otherwise a is the first chunk and b the second.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void unpack(const uint4 (&w)[2], Two (&a)[4], Two (&b)[4]) {
+    const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (INTERLEAVED) {
+            a[i] = Two{bf16_lo(u[2 * i]), bf16_lo(u[2 * i + 1])};
+            b[i] = Two{bf16_hi(u[2 * i]), bf16_hi(u[2 * i + 1])};
+        } else {
+            a[i] = Two{bf16_lo(u[i]), bf16_hi(u[i])};
+            b[i] = Two{bf16_lo(u[i + 4]), bf16_hi(u[i + 4])};
+        }
+    }
+}
+template <bool INTERLEAVED>
+__device__ __forceinline__ void pack(const Two (&a)[4], const Two (&b)[4], uint4 (&w)[2]) {
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (INTERLEAVED) {
+            u[2 * i] = pack_bf16x2(a[i].x, b[i].x);
+            u[2 * i + 1] = pack_bf16x2(a[i].y, b[i].y);
+        } else {
+            u[i] = pack_bf16x2(a[i].x, a[i].y);
+            u[i + 4] = pack_bf16x2(b[i].x, b[i].y);
+        }
+    }
+    w[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    w[1] = make_uint4(u[4], u[5], u[6], u[7]);
+}
 
 template <bool APPEND, bool INTERLEAVED>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
 rotate_kernel(const __grid_constant__ RotateArgs a) {
+    __shared__ uint4 s_ring[kWarps][kDepth * 64];
     __shared__ uint64_t s_turns[kRotaryPairs];
+    // weights in fp32, as the lanes hold a row: of q, of k; a and b; lane % 8
+    __shared__ float4 s_weight[2][2][2][8];
     const int lane = threadIdx.x & 31, sub = lane & 7;
-    for (int i = threadIdx.x; i < kRotaryPairs; i += kWarps * 32) s_turns[i] = a.turns[i];
     // this lane's chunks of a row, and whether its pairs are rotated
     const bool rotated = sub * 8 < a.pairs;
     const bool apart = !INTERLEAVED && rotated;
     const int c0 = apart ? sub : 2 * sub, c1 = apart ? sub + a.pairs / 8 : 2 * sub + 1;
+    const int hq = a.num_q_heads, hk = a.num_kv_heads, rows = hq + hk + (APPEND ? hk : 0);
+    const unsigned items = a.num_tokens * a.slices, stride = gridDim.x * kWarps, slices = a.slices;
+    const int quad_rows = a.quads * 4;
     // programmatic dependent of whatever precedes the call
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    uint4 qw[2] = {}, kw[2] = {};
-    if (a.q_weight) {
-        qw[0] = __ldg(a.q_weight + c0);
-        qw[1] = __ldg(a.q_weight + c1);
-    }
-    if (a.k_weight) {
-        kw[0] = __ldg(a.k_weight + c0);
-        kw[1] = __ldg(a.k_weight + c1);
+    // The warp's quads in order, kDepth - 1 of them on their way to shared memory while one is
+    // worked on (held in registers, two of them, 24 warps kept the memory 60 % busy). A
+    // lane copies what it reads itself.
+    uint4 *ring = s_ring[threadIdx.x >> 5] + lane;
+    unsigned item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    unsigned item_ahead = item, t_ahead = item / slices;
+    int h_ahead = (int)(item - t_ahead * slices) * quad_rows, end_ahead = min(h_ahead + quad_rows, rows), put = 0;
+    auto fetch = [&]() {
+        if (item_ahead < items) {
+            const int h = h_ahead + (lane >> 3);
+            if (h < end_ahead) {
+                const HeadRows &r = h < hq ? a.q : (!APPEND || h < hq + hk ? a.k : a.v);
+                const int64_t head = h < hq ? h : (!APPEND || h < hq + hk ? h - hq : h - hq - hk);
+                const uint4 *src = r.p + t_ahead * r.token + head * r.head;
+                const uint32_t dst = smem_u32(ring + put * 64);
+                cp_async_16(dst, src + c0, 16);
+                cp_async_16(dst + 512, src + c1, 16);
+            }
+            h_ahead += 4;
+            if (h_ahead >= end_ahead) {
+                item_ahead += stride;
+                t_ahead = item_ahead / slices;
+                h_ahead = (int)(item_ahead - t_ahead * slices) * quad_rows;
+                end_ahead = min(h_ahead + quad_rows, rows);
+            }
+        }
+        put = put + 1 == kDepth ? 0 : put + 1;
+        cp_async_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < kDepth - 1; ++i) fetch();
+    for (int i = threadIdx.x; i < kRotaryPairs; i += kWarps * 32) s_turns[i] = a.turns[i];
+    if (threadIdx.x < 16) {
+        const int key = threadIdx.x >> 3;
+        const uint4 *w = key ? a.k_weight : a.q_weight;
+        if (w) {
+            const uint4 x[2] = {__ldg(w + c0), __ldg(w + c1)};
+            Two f[2][4];
+            unpack<INTERLEAVED>(x, f[0], f[1]);
+#pragma unroll
+            for (int ab = 0; ab < 2; ++ab)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    s_weight[key][ab][i][sub] = make_float4(f[ab][2 * i].x, f[ab][2 * i].y, f[ab][2 * i + 1].x, f[ab][2 * i + 1].y);
+        }
     }
     __syncthreads();
-    const int hq = a.num_q_heads, hk = a.num_kv_heads, rows = hq + hk + (APPEND ? hk : 0);
-    const int64_t items = a.num_tokens * a.slices;
-    const int64_t stride = (int64_t)gridDim.x * kWarps;
-    for (int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); item < items; item += stride) {
-        const int64_t t = item / a.slices;
-        const int first = (int)(item - t * a.slices) * a.quads * 4;
-        const int last = first + a.quads * 4 < rows ? first + a.quads * 4 : rows;
-        int64_t slot = 0;
-        bool stored = false;
+    int get = 0;
+#pragma unroll 1
+    for (; item < items; item += stride) {
+        const int64_t t = item / slices;
+        const int first = (int)(item - (unsigned)t * slices) * quad_rows, last = min(first + quad_rows, rows);
+        // where the rows of q, k and v would begin if all were one's: row h of the token is
+        // the h-th of its own from there on
+        uint4 *const to_q = a.q_out.p + t * a.q_out.token;
+        uint4 *to_k = a.k_out.p + t * a.k_out.token - hq * a.k_out.head, *to_v = nullptr;
+        int64_t k_step = a.k_out.head;          // from a head's row to the next
+        bool stored = true;
         if (APPEND) {
-            slot = __ldg(a.slots + t);
+            const int64_t slot = __ldg(a.slots + t);
             stored = slot >= 0 && slot < a.num_slots;
             if (!stored && slot != -1 && lane == 0) atomicCAS(&g_rotary_error, 0, kErrBadSlot);
+            const int lb = a.block_size_log2;
+            const int64_t row = a.head_major ? ((slot >> lb) * hk << lb) + (slot & ((1 << lb) - 1)) : slot * hk;
+            k_step = a.head_major ? kChunks << lb : kChunks;
+            to_k = a.k_cache + row * kChunks - hq * k_step;
+            to_v = a.v_cache + row * kChunks - (hq + hk) * k_step;
         }
-        const int p = a.positions ? __ldg(a.positions + t) : 0;
-        float cs[8], sn[8];
-        bool have = false;
-        for (int h0 = first; h0 < last; h0 += 4 * kBatch) {
-            uint4 x[kBatch][2];
-            uint4 *out[kBatch];
-            Kind kind[kBatch];
+        Two cs[4], sn[4];
+        if (a.positions) {
+            // pairs 2 lane and 2 lane + 1, then each lane the 8 of its own
+            const int p = __ldg(a.positions + t);
+            float c2[2], s2[2];
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                const int h = h0 + 4 * b + (lane >> 3);
-                const uint4 *src = nullptr;
-                out[b] = nullptr;
-                kind[b] = h < hq ? kQuery : (h < hq + hk ? kKey : kValue);
-                if (h < last) {
-                    const HeadRows &r = kind[b] == kQuery ? a.q : (kind[b] == kKey ? a.k : a.v);
-                    const int head = kind[b] == kQuery ? h : (kind[b] == kKey ? h - hq : h - hq - hk);
-                    src = r.p + t * r.token + head * r.head;
-                    if (kind[b] == kQuery) {
-                        out[b] = a.q_out.p + t * a.q_out.token + head * a.q_out.head;
-                    } else if (!APPEND) {
-                        out[b] = a.k_out.p + t * a.k_out.token + head * a.k_out.head;
-                    } else if (stored) {
-                        const int lb = a.block_size_log2;
-                        const int64_t row = a.head_major
-                            ? (((slot >> lb) * hk + head) << lb) + (slot & ((1 << lb) - 1))
-                            : slot * hk + head;
-                        out[b] = (kind[b] == kKey ? a.k_cache : a.v_cache) + row * kChunks;
-                    }
-                }
-                if (out[b]) {
-                    x[b][0] = src[c0];
-                    x[b][1] = src[c1];
-                } else {
-                    x[b][0] = x[b][1] = make_uint4(0u, 0u, 0u, 0u);
-                }
-            }
-            if (a.positions && !have) {
-                // pairs 2 lane and 2 lane + 1, then each lane the 8 of its own
-                have = true;
-                float c2[2], s2[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint64_t turn = (uint64_t)(int64_t)p * s_turns[2 * lane + k];
-                    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s2[k], &c2[k]);
-                    s2[k] *= a.amplitude;
-                    c2[k] *= a.amplitude;
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    cs[j] = __shfl_sync(0xffffffffu, c2[j & 1], 4 * sub + (j >> 1));
-                    sn[j] = __shfl_sync(0xffffffffu, s2[j & 1], 4 * sub + (j >> 1));
-                }
+            for (int k = 0; k < 2; ++k) {
+                const uint64_t turn = (uint64_t)(int64_t)p * s_turns[2 * lane + k];
+                sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s2[k], &c2[k]);
+                s2[k] *= a.amplitude;
+                c2[k] *= a.amplitude;
             }
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                const bool key = kind[b] == kKey;
-                const bool norm = kind[b] != kValue && (key ? a.k_weight : a.q_weight) != nullptr;
-                const bool turn = kind[b] != kValue && rotated;
-                float f[2][8];
-                unpack(x[b][0], f[0]);
-                unpack(x[b][1], f[1]);
-                float sq = 0.f;
+            for (int j = 0; j < 4; ++j) {
+                cs[j] = Two{__shfl_sync(0xffffffffu, c2[0], 4 * sub + j), __shfl_sync(0xffffffffu, c2[1], 4 * sub + j)};
+                sn[j] = Two{__shfl_sync(0xffffffffu, s2[0], 4 * sub + j), __shfl_sync(0xffffffffu, s2[1], 4 * sub + j)};
+            }
+        }
+#pragma unroll 1
+        for (int h0 = first; h0 < last; h0 += 4) {
+            fetch();
+            cp_async_wait<kDepth - 1>();
+            uint4 x[2] = {ring[get * 64], ring[get * 64 + 32]};
+            get = get + 1 == kDepth ? 0 : get + 1;
+            const int h = h0 + (lane >> 3);
+            const bool key = h >= hq, value = APPEND && h >= hq + hk;
+            const bool norm = !value && (key ? a.k_weight : a.q_weight) != nullptr;
+            const bool turn = !value && rotated;
+            Two f[4], g[4];
+            unpack<INTERLEAVED>(x, f, g);
+            Two sq = mul(f[0], f[0]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sq = fmaf(f[0][i], f[0][i], fmaf(f[1][i], f[1][i], sq));
+            for (int i = 1; i < 4; ++i) sq = fma2(f[i], f[i], sq);
 #pragma unroll
-                for (int m = 1; m < 8; m <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, m);
-                if (norm) {
-                    const float inv = rsqrtf(fmaf(sq, 1.f / kHeadDim, a.eps));
+            for (int i = 0; i < 4; ++i) sq = fma2(g[i], g[i], sq);
+            float sum = sq.x + sq.y;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float w[8];
-                        unpack(key ? kw[k] : qw[k], w);
+            for (int m = 1; m < 8; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+            if (norm) {
+                const float inv = rsqrtf(fmaf(sum, 1.f / kHeadDim, a.eps));
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) f[k][i] *= inv * w[i];
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    const float4 wa = s_weight[key][0][i][sub], wb = s_weight[key][1][i][sub];
+                    f[2 * i] = mul(f[2 * i], mul(Two{wa.x, wa.y}, Two{inv, inv}));
+                    f[2 * i + 1] = mul(f[2 * i + 1], mul(Two{wa.z, wa.w}, Two{inv, inv}));
+                    g[2 * i] = mul(g[2 * i], mul(Two{wb.x, wb.y}, Two{inv, inv}));
+                    g[2 * i + 1] = mul(g[2 * i + 1], mul(Two{wb.z, wb.w}, Two{inv, inv}));
                 }
-                if (turn) {
+            }
+            if (turn) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float &u = INTERLEAVED ? f[j >> 2][2 * (j & 3)] : f[0][j];
-                        float &v = INTERLEAVED ? f[j >> 2][2 * (j & 3) + 1] : f[1][j];
-                        const float n = u * cs[j] - v * sn[j];
-                        v = v * cs[j] + u * sn[j];
-                        u = n;
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const Two u = fma2(g[j], Two{-sn[j].x, -sn[j].y}, mul(f[j], cs[j]));
+                    g[j] = fma2(f[j], sn[j], mul(g[j], cs[j]));
+                    f[j] = u;
                 }
-                if (out[b]) {
-                    // neither normed nor rotated: the bits as they are
-                    out[b][c0] = norm || turn ? pack(f[0]) : x[b][0];
-                    out[b][c1] = norm || turn ? pack(f[1]) : x[b][1];
-                }
+            }
+            // neither normed nor rotated: the bits as they are
+            if (norm || turn) pack<INTERLEAVED>(f, g, x);
+            if (h < last && (!key || stored)) {
+                uint4 *out = !key ? to_q : (value ? to_v : to_k);
+                out += h * (!key ? a.q_out.head : k_step);
+                out[c0] = x[0];
+                out[c1] = x[1];
             }
         }
     }
@@ -245,15 +308,17 @@ cudaError_t take_rotary_error(cudaStream_t stream, int *code) {
 cudaError_t launch_rotate(RotateArgs a, bool append, bool interleaved, int sm_count, cudaStream_t stream) {
     const int rows = a.num_q_heads + a.num_kv_heads * (append ? 2 : 1);
     const int all = (rows + 3) / 4;             // quads of a token
-    // A warp takes as many of a token's quads as leave the GPU full of warps: the
-    // sines are then computed once for all of them.
-    const int64_t full = (int64_t)sm_count * 32;
-    int64_t quads = a.num_tokens * all / full;
+    // A warp takes as many of a token's quads as leave the GPU full of warps: the sines are
+    // then computed once for all of them. (One wave of 24 warps an SM, each going from token
+    // to token, instead of CTAs in turn: 16384 tokens of 40 heads 58.9 us against 52.5, of
+    // 2047 x 48 19.1 against 14.5.)
+    const int64_t quads = a.num_tokens * all / ((int64_t)sm_count * 32);
     a.quads = (int)(quads < 1 ? 1 : (quads > all ? all : quads));
     a.slices = (all + a.quads - 1) / a.quads;
+    while (a.num_tokens * a.slices > INT32_MAX) --a.slices;     // items are counted in 32 bits
+    a.quads = (all + a.slices - 1) / a.slices;      // alike
     int64_t grid = (a.num_tokens * a.slices + kWarps - 1) / kWarps;
-    const int64_t most = (int64_t)sm_count * 16;
-    if (grid > most) grid = most;
+    if (grid > (int64_t)sm_count * kCtasPerSm * 3) grid = (int64_t)sm_count * kCtasPerSm * 3;
     if (append)
         return interleaved ? launch<true, true>(a, (unsigned)grid, stream)
                            : launch<true, false>(a, (unsigned)grid, stream);

@@ -804,7 +804,8 @@ def _positions(positions, rotary, tokens, dev):
 def _out_heads(x, out, name, rows, dev, tokens, stream):
     """An output for the rows x ([T, H, 128], ``rows`` of _heads), and its own."""
     if out is None:
-        out = _new(x.shape, x.dtype, dev, stream)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format) if stream is None \
+            else _new(x.shape, x.dtype, dev, stream)
         return out, (out.data_ptr(), rows[3] * 128, 128)
     o = _heads(out, name, dev.index, tokens)
     if o[3] != rows[3]:

@@ -84,6 +84,7 @@ SHARED = [
     (dict(T=-1), pa.PA_ERR_INVALID_ARG),
     (dict(Hq=-1), pa.PA_ERR_INVALID_ARG),
     (dict(Hq=1 << 20), pa.PA_ERR_UNSUPPORTED),
+    (dict(T=1 << 31), pa.PA_ERR_UNSUPPORTED),
     (dict(q=None), pa.PA_ERR_INVALID_ARG),
     (dict(q=24), pa.PA_ERR_INVALID_ARG),
     (dict(qts=-1024), pa.PA_ERR_INVALID_ARG),
