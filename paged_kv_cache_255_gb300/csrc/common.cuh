@@ -81,6 +81,32 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return r;
 }
 
+// Two floats that one instruction works on.
+struct Two {
+    float x, y;
+};
+__device__ __forceinline__ uint64_t bits(Two v) {
+    return (uint64_t)__float_as_uint(v.x) | (uint64_t)__float_as_uint(v.y) << 32;
+}
+__device__ __forceinline__ Two two(uint64_t b) {
+    return Two{__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32))};
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return two(r);
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return two(r);
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return two(r);
+}
+
 // ldmatrix: four 8x8 b16 matrices from shared memory; lane i supplies the
 // address of row (i % 8) of matrix (i / 8). Lane l receives, of matrix j,
 // row l / 4, columns 2 (l % 4) and 2 (l % 4) + 1 (transposed with .trans).

@@ -37,29 +37,6 @@ constexpr int kChunks = kHeadDim / 8;       // 16-byte chunks of a row
 constexpr int kCtasPerSm = 6;
 constexpr int kDepth = 4;                   // quads of rows a warp has on their way
 
-// Two floats that one instruction works on (the kernel is bound by its issue slots before
-// it is by memory: with scalar arithmetic 16384 prompt rows of 40 heads took
-// 57.8 us, of which the bytes alone are 49).
-struct Two {
-    float x, y;
-};
-__device__ __forceinline__ uint64_t bits(Two v) {
-    return (uint64_t)__float_as_uint(v.x) | (uint64_t)__float_as_uint(v.y) << 32;
-}
-__device__ __forceinline__ Two two(uint64_t b) {
-    return Two{__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32))};
-}
-__device__ __forceinline__ Two mul(Two a, Two b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-    return two(r);
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-    return two(r);
-}
-
 // The 8 pairs (a, b) of a lane's two chunks, two pairs to a Two, and back. Interleaved pairs
 // are the words of the chunks; otherwise a is the first chunk and b the second.
 template <bool INTERLEAVED>

@@ -554,7 +554,8 @@ __device__ __forceinline__ void wide_tile(uint32_t tS, uint32_t tO, float sc, bo
     tc::tmem_ld32(tS, sr[0]);
     const float alpha = raise_max(fmaxf(e[0], e[1]), sc, m, lsum);
     const float mb = m == -INFINITY ? 0.f : m;
-    float l4[4] = {0.f, 0.f, 0.f, 0.f};
+    const Two sc2{sc, sc}, mb2{-mb, -mb};
+    Two l2[2] = {};
 #pragma unroll 1
     for (int ch = 0; ch < 4; ch += 2) {
 #pragma unroll
@@ -564,16 +565,16 @@ __device__ __forceinline__ void wide_tile(uint32_t tS, uint32_t tO, float sc, bo
             uint32_t pw[16];
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-                const float p0 = ex2(fmaf(__uint_as_float(sr[h][2 * c]), sc, -mb));
-                const float p1 = ex2(fmaf(__uint_as_float(sr[h][2 * c + 1]), sc, -mb));
-                l4[c & 3] += p0 + p1;
-                pw[c] = pack_bf16x2(p0, p1);
+                const Two x = fma2(Two{__uint_as_float(sr[h][2 * c]), __uint_as_float(sr[h][2 * c + 1])}, sc2, mb2);
+                const Two p{ex2(x.x), ex2(x.y)};
+                l2[c & 1] = add(l2[c & 1], p);
+                pw[c] = pack_bf16x2(p.x, p.y);
             }
             // over columns that have been read
             tc::tmem_st16(tS + (ch + h) * 16, pw);
         }
     }
-    lsum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+    lsum += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
     if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
         for (int ch = 0; ch < 4; ++ch) {
@@ -1074,12 +1075,16 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
             }
         };
         auto await = [&](uint32_t b, uint32_t parity) { return warp_wait(b, parity, abort, true); };
+        static_assert(kVStages == 2, "V stages are counted on in turn");
         // Step i is of stream i % 2: of two query tiles over key tile i / 2, of halves over key
         // tile i. In turn: PV of step i once its P is in TMEM (and, for the first of a piece,
         // the previous piece's results have been read), then S of step i + 2. The tiles they
         // need have been waited for before, off the chain from P to S. A stage is released
         // after its last reader.
-        uint32_t gt = 0, gq0 = 0, gq1 = 0;      // key tiles before this piece, of all and of each stream
+        // (A wait costs 130 cycles also where nothing is to wait for, and a step's products take
+        // 1024: a second reader does not wait for its tiles, and the rings' places are counted on.)
+        int vs = 0, ks = 0;                     // next V and K stage, and their phases
+        uint32_t v_phase = 0, k_phase = 0, p_phase = 0;         // (p_phase: bit t, of stream t)
         int piece = 0;
         QBuffers qb;
         bool ok = true;
@@ -1087,24 +1092,38 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
         do {
             const int nt = w.j1 - w.j0;
             const bool two = two_tiles<G>(w);
-            const int shift = two ? 1 : 0, steps = nt << shift;
+            const int steps = nt << (two ? 1 : 0);
+            const int tail = groups_used(w, w.j1 - 1);          // 16-key groups of the last tile
             const int b0 = qb.take(two);
             ok = await(bar(kBarQFull + b0), (qb.uses(b0) - 1) & 1);
             if (ok && two) ok = await(bar(kBarQFull + 1), (qb.uses(1) - 1) & 1);
 #pragma unroll 1
             for (int i = -2; ok && i < steps; ++i) {
-                const int t = i & 1, j = i >> shift;
-                const bool last = !two || t == 1;               // reader of its tiles
-                const uint32_t gp = gt + j, gs = gt + ((i + 2) >> shift);
-                const int vs = gp % kVStages, ks = gs % kKStages;
+                const int t = i & 1;
+                const bool first = !two || t == 0, last = !two || t == 1;       // reader of its tiles
                 const bool more = i + 2 < steps;
-                if (i >= 0) ok = await(bar(kBarVFull + vs), (gp / kVStages) & 1);
-                if (ok && more) ok = await(bar(kBarKFull + ks), (gs / kKStages) & 1);
-                if (ok && i == 0 && piece > 0) ok = await(bar(kBarOFree), (piece - 1) & 1);
-                if (ok && i >= 0) ok = await(bar(kBarPReady + t), ((t == 0 ? gq0 : gq1) + (i >> 1)) & 1);
+                if (first) {
+                    if (i >= 0) ok = await(bar(kBarVFull + vs), v_phase);
+                    if (ok && more) ok = await(bar(kBarKFull + ks), k_phase);
+                    if (ok && i == 0 && piece > 0) ok = await(bar(kBarOFree), (piece - 1) & 1);
+                }
+                if (ok && i >= 0) ok = await(bar(kBarPReady + t), p_phase >> t & 1);
                 if (!ok) break;
-                if (i >= 0) issue_pv(t, vs, i > 1, groups_used(w, w.j0 + j), last ? bar(kBarVEmpty + vs) : 0u);
-                if (more) issue_s(t, two ? t : b0, ks, last ? bar(kBarKEmpty + ks) : 0u);
+                if (i >= 0) {
+                    issue_pv(t, vs, i > 1, i + (two ? 2 : 1) < steps ? kGroups : tail, last ? bar(kBarVEmpty + vs) : 0u);
+                    p_phase ^= 1u << t;
+                    if (last) {
+                        vs ^= 1;
+                        v_phase ^= vs == 0 ? 1u : 0u;
+                    }
+                }
+                if (more) {
+                    issue_s(t, two ? t : b0, ks, last ? bar(kBarKEmpty + ks) : 0u);
+                    if (last) {
+                        ks = ks == kKStages - 1 ? 0 : ks + 1;
+                        k_phase ^= ks == 0 ? 1u : 0u;
+                    }
+                }
             }
             // the queries' buffers are free once this piece's MMAs are done
             if (ok && tc::elect_one()) {
@@ -1112,9 +1131,6 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
                 if (two) tc::commit(bar(kBarQEmpty + 1));
             }
             __syncwarp();
-            gt += nt;
-            gq0 += stream_tiles(nt, two, 0);
-            gq1 += stream_tiles(nt, two, 1);
             ++piece;
         } while (ok && walk_next<G>(w, a));
         if (tc::elect_one()) tc::commit(bar(kBarDrain));
