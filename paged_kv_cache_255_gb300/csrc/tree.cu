@@ -407,32 +407,35 @@ __device__ __noinline__ void clean_v(const volatile Walk &w, int j, uint8_t *vti
     const int rows = groups_used(w, j) * kGroup - first;
     constexpr int kBatch = 4;                                   // chunks a thread has in flight
     for (int i0 = thread; i0 < rows * 16; i0 += kRows * kBatch) {
-        uint4 *at[kBatch];
         uint4 x[kBatch];
+        auto place = [&](int k) {
+            const int i = i0 + kRows * k;
+            return reinterpret_cast<uint4 *>(vtile + ((i >> 3) & 1) * kKVHalf + (first + (i >> 4)) * 128 + (i & 7) * 16);
+        };
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int i = i0 + kRows * k, r = first + (i >> 4);
-            at[k] = reinterpret_cast<uint4 *>(vtile + ((i >> 3) & 1) * kKVHalf + r * 128 + (i & 7) * 16);
-            if (i < rows * 16 && r < left) x[k] = *at[k];
-            else x[k] = make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int k = 0; k < kBatch; ++k)
+            x[k] = i0 + kRows * k < rows * 16 ? *place(k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int i = i0 + kRows * k, r = first + (i >> 4);
             uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            bool odd_one = false;
+            // an exponent of all ones is an infinity or NaN: one more carries into the sign's place
+            uint32_t found = 0;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                // an exponent of all ones: infinity or NaN
-                const bool lo = (v[c] & 0x7f80u) == 0x7f80u, hi = (v[c] & 0x7f800000u) == 0x7f800000u;
-                v[c] = lo ? v[c] & 0xffff0000u : v[c];
-                v[c] = hi ? v[c] & 0x0000ffffu : v[c];
-                odd_one |= lo | hi;
-            }
-            if (i < rows * 16 && (odd_one || r >= left)) {
-                *at[k] = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int c = 0; c < 4; ++c) found |= ((v[c] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+            if (i >= rows * 16) {
+            } else if (r >= left) {
+                *place(k) = make_uint4(0u, 0u, 0u, 0u);
+            } else if (found) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    if ((x[k].x & 0x7f80u) == 0x7f80u) x[k].x &= 0xffff0000u;
+                    if ((x[k].x & 0x7f800000u) == 0x7f800000u) x[k].x &= 0x0000ffffu;
+                    x[k] = make_uint4(x[k].y, x[k].z, x[k].w, x[k].x);
+                }
+                *place(k) = x[k];
                 const int node = node0 + r;
-                if (odd_one && node < 32 * words) atomicOr(odd, 1u << (node >> 5));     // the others nobody sees
+                if (node < 32 * words) atomicOr(odd, 1u << (node >> 5));        // the others nobody sees
             }
         }
     }
@@ -658,7 +661,7 @@ __device__ __forceinline__ float merged(uint32_t o, uint32_t o2, float fa, bool 
     const float x = __uint_as_float(o) * fa, y = fmaf(__uint_as_float(o2), fb, x);
     return lsum == 0.f ? 0.f : (b_too ? y : x) * inv;
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+__device__ __forceinline__ uint4 pack(const float *f) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
@@ -796,19 +799,22 @@ __device__ __forceinline__ bool softmax_piece(const TreeArgs &a, const volatile 
         if constexpr (R == 0) {
             uint4 *orow = out_row(row0);
 #pragma unroll 1
-            for (int d = d0; d < d1; d += 8) {
-                uint32_t o[8], o2[8];
-                tc::tmem_ld8((two ? tO : tmem + lane + 128) + d, o);
-                tc::tmem_ld8(tmem + lane + 384 + d, o2);
+            for (int d = d0; d < d1; d += 16) {
+                uint32_t o[16], o2[16];
+                tc::tmem_ld16((two ? tO : tmem + lane + 128) + d, o);
+                tc::tmem_ld16(tmem + lane + 384 + d, o2);
                 tc::tmem_ld_wait();
-                float y[8];
+                float y[16];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) y[c] = merged(o[c], o2[c], fa[0], b_too, fb[0], lsum[0], inv[0]);
-                if (rv[0] && whole) {
-                    orow[d / 8] = pack(y);
-                } else if (rv[0]) {
-                    po[(d / 4) * kPair + row0] = make_float4(y[0], y[1], y[2], y[3]);
-                    po[(d / 4 + 1) * kPair + row0] = make_float4(y[4], y[5], y[6], y[7]);
+                for (int c = 0; c < 16; ++c) y[c] = merged(o[c], o2[c], fa[0], b_too, fb[0], lsum[0], inv[0]);
+#pragma unroll
+                for (int c = 0; c < 16; c += 8) {
+                    if (rv[0] && whole) {
+                        orow[(d + c) / 8] = pack(y + c);
+                    } else if (rv[0]) {
+                        po[((d + c) / 4) * kPair + row0] = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
+                        po[((d + c) / 4 + 1) * kPair + row0] = make_float4(y[c + 4], y[c + 5], y[c + 6], y[c + 7]);
+                    }
                 }
             }
         } else {
@@ -822,18 +828,21 @@ __device__ __forceinline__ bool softmax_piece(const TreeArgs &a, const volatile 
                 prow[x] = reinterpret_cast<float2 *>(po + (pairs >> 1) * kPair + row0 + 8 * x) + (pairs & 1);
             }
 #pragma unroll 1
-            for (int d = 0; d < 64; d += 8) {
-                uint32_t o[4], o2[4];
-                tc::tmem_ld_16x256b_x1(tmem + lane + 128 + d0 + d, o);
-                tc::tmem_ld_16x256b_x1(tmem + lane + 384 + d0 + d, o2);
+            for (int d = 0; d < 64; d += 32) {
+                uint32_t o[16], o2[16];
+                tc::tmem_ld_16x256b_x4(tmem + lane + 128 + d0 + d, o);
+                tc::tmem_ld_16x256b_x4(tmem + lane + 384 + d0 + d, o2);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int x = 0; x < NR; ++x) {
-                    const float y0 = merged(o[2 * x], o2[2 * x], fa[x], b_too, fb[x], lsum[x], inv[x]);
-                    const float y1 = merged(o[2 * x + 1], o2[2 * x + 1], fa[x], b_too, fb[x], lsum[x], inv[x]);
-                    if (rv[x] && whole) orow[x][d / 2] = pack_bf16x2(y0, y1);
-                    else if (rv[x]) prow[x][d / 2 * kPair] = make_float2(y0, y1);
-                }
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int x = 0; x < NR; ++x) {
+                        const int i = 4 * k + 2 * x;
+                        const float y0 = merged(o[i], o2[i], fa[x], b_too, fb[x], lsum[x], inv[x]);
+                        const float y1 = merged(o[i + 1], o2[i + 1], fa[x], b_too, fb[x], lsum[x], inv[x]);
+                        if (rv[x] && whole) orow[x][(d + 8 * k) / 2] = pack_bf16x2(y0, y1);
+                        else if (rv[x]) prow[x][(d + 8 * k) / 2 * kPair] = make_float2(y0, y1);
+                    }
             }
         }
         const uint32_t odd = reaches_nodes(w, w.j1 - 1)
