@@ -12,7 +12,7 @@
 //
 // A unit is 256 query rows (two tiles of 128: 128 / G tokens x G heads, G = g rounded up
 // to a power of two) of one (sequence, KV head); its keys go in tiles of 128. The flat
-// space of all units' key tiles, and kUnitTiles places more a unit for what it costs
+// space of all units' key tiles, and kUnitPlaces places more a unit for what it costs
 // besides them, is cut into equal contiguous shares, one CTA per SM each, planned by
 // every CTA from the lengths and starts. A unit that one share holds whole is written
 // as it ends; one that several share leaves a part per share in fp32, and
@@ -63,8 +63,10 @@ constexpr int kThreads = kSoftmaxThreads + 3 * 32;
 constexpr int kWarpsAll = kThreads / 32;
 constexpr int kGroup = 16;                              // tokens per MMA of P V
 constexpr int kGroups = kKeys / kGroup;                 // 8
-constexpr int kUnitPlaces = 2;                          // places of a unit besides its tiles
-constexpr int kMinPlaces = 3;                           // fewest places of a share
+// Places of a unit besides its tiles, for its start and its end: at 2 a batch of 512 units
+// of 16 to 64 tiles takes 277 us, at 3 271, at 4 268, and 480 units of 1 to 8 tiles 45.6,
+// 45.5, 46.6.
+constexpr int kUnitPlaces = 3;
 constexpr uint32_t kQBytes = kRows * kRowBytes;         // 32 KB: 2 halves of [128][128 B]
 constexpr uint32_t kQHalf = kRows * 128;
 constexpr uint32_t kKVBytes = kKeys * kRowBytes;
@@ -171,6 +173,25 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
         return true;
     }
     return warp_wait_more(bar, parity, abort, spin);
+}
+// One lane's wait.
+__device__ __noinline__ bool lane_wait_more(uint32_t bar, uint32_t parity, volatile int *abort) {
+    const uint64_t t0 = tc::globaltimer_ns();
+#pragma unroll 1
+    for (uint32_t i = 1;; ++i) {
+        if (tc::mbar_test_wait(bar, parity)) return true;
+        if ((i & 255) == 0) {
+            if (*abort) return false;
+            if (tc::globaltimer_ns() - t0 > 2000000000ull) {
+                set_error(kErrTimeout);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return tc::mbar_test_wait(bar, parity) || lane_wait_more(bar, parity, abort);
 }
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
     __syncwarp();
@@ -306,7 +327,7 @@ __device__ __noinline__ bool plan_share(const TreeArgs &a, Walk *first, volatile
     // where all have the same number of pairs, the pairs are lanes
     const int lanes = most == least && (int)most <= a.workers ? most : 1;
     W = lanes > 1 ? one : all;
-    shares = max(1, min(W / kMinPlaces, a.workers / lanes));
+    shares = max(1, min(W, a.workers / lanes));
     const int w = blockIdx.x / lanes;
     if (w >= shares || W == 0) return false;
     const int T0 = share_begin(w, W, shares);
@@ -513,6 +534,39 @@ __device__ __forceinline__ float raise_max(float most, float sc, float &m, float
     lsum *= alpha;
     m = mt;
     return alpha;
+}
+
+// A tile of whose scores none passes a row's reference by more than the slack, as nearly all
+// do once a few tiles have set it: the weights against the reference as it is, and the
+// maximum beside them, in one reading. False, with nothing changed, when a row of the warp
+// has to raise it.
+__device__ __forceinline__ bool steady_tile(uint32_t tS, float sc, float m, float &lsum) {
+    if (__any_sync(0xffffffffu, m == -INFINITY)) return false;
+    float e[2] = {-INFINITY, -INFINITY};
+    uint32_t sr[2][32], pw[2][32];
+    const Two sc2{sc, sc}, mb2{-m, -m};
+    Two l2[2] = {};
+    tc::tmem_ld32(tS, sr[0]);
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+        tc::tmem_ld_wait();
+        if (ch < 3) tc::tmem_ld32(tS + 32 * (ch + 1), sr[(ch + 1) & 1]);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const Two s2{__uint_as_float(sr[ch & 1][2 * c]), __uint_as_float(sr[ch & 1][2 * c + 1])};
+            const Two x = fma2(s2, sc2, mb2);
+            const Two p{ex2(x.x), ex2(x.y)};
+            e[c & 1] = fmax3(e[c & 1], s2.x, s2.y);
+            l2[c & 1] = add(l2[c & 1], p);
+            pw[ch >> 1][16 * (ch & 1) + c] = pack_bf16x2(p.x, p.y);
+        }
+    }
+    if (__any_sync(0xffffffffu, fmaxf(e[0], e[1]) * sc > m + kRescaleSlack)) return false;
+    tc::tmem_st32(tS, pw[0]);
+    tc::tmem_st32(tS + 32, pw[1]);
+    lsum += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+    tc::tmem_st_wait();
+    return true;
 }
 
 // A thread per row: 128 scores of its TMEM lane, 32 at a time, once for the maximum and
@@ -723,8 +777,9 @@ __device__ __forceinline__ bool softmax_piece(const TreeArgs &a, const volatile 
         if (!warp_wait(bar(kBarSFull + wg), (st.gt + j) & 1, abort, any)) return false;
         tc::fence_after_sync();
         if (any) {
-            if constexpr (R == 0) wide_tile(tS, tO, sc, nodes, vis[0], m[0], lsum[0]);
-            else narrow_tile<R>(tS, tO, sc, nodes, vis, m, lsum);
+            if constexpr (R == 0) {
+                if (nodes || !steady_tile(tS, sc, m[0], lsum[0])) wide_tile(tS, tO, sc, nodes, vis[0], m[0], lsum[0]);
+            } else narrow_tile<R>(tS, tO, sc, nodes, vis, m, lsum);
         }
         // V has to be there to be cleaned; of two query tiles A's warps do it, whose product
         // is issued first
@@ -1025,7 +1080,7 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
                 const int2 at = box_next;
                 box_next = box_at(j + 1);
                 const int st = gt % nst;
-                if (!warp_wait(bar_empty + 8 * st, ((gt / nst) & 1) ^ 1, abort)) { ok = false; break; }
+                if (!warp_wait(bar_empty + 8 * st, ((gt / nst) & 1) ^ 1, abort, true)) { ok = false; break; }
                 const uint32_t full = bar_full + 8 * st;
                 const int n = __popc(__ballot_sync(0xffffffffu, at.x != INT_MIN));
                 if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)(n * box * 128));
@@ -1058,32 +1113,32 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
             const uint32_t qd = q_lo + b * (kQBytes >> 4);
             const uint32_t kd = k_lo + st * (kKVBytes >> 4);
             const uint32_t d = tmem + t * 256;
-            tc::fence_after_sync();
-            if (tc::elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kHeadDim / 16; ++kk)
-                    tc::mma_ss(d, desc(qd + (((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4)),
-                               desc(kd + (((kk >> 2) * kKVHalf + (kk & 3) * 32) >> 4)), idesc_s, kk > 0);
-                tc::commit(bar(kBarSFull + t));
-                if (release) tc::commit(release);
-            }
+            for (int kk = 0; kk < kHeadDim / 16; ++kk)
+                tc::mma_ss(d, desc(qd + (((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4)),
+                           desc(kd + (((kk >> 2) * kKVHalf + (kk & 3) * 32) >> 4)), idesc_s, kk > 0);
+            tc::commit(bar(kBarSFull + t));
+            if (release) tc::commit(release);
         };
         // over the first nv 16-key groups (the rest have P = 0 and no V)
         auto issue_pv = [&](int t, int st, bool acc, int nv, uint32_t release) {
             const uint32_t vd = v_lo + st * (kKVBytes >> 4);
             const uint32_t pa_ = tmem + t * 256;
             const uint32_t d = pa_ + 128;
-            tc::fence_after_sync();
-            if (tc::elect_one()) {
+            tc::mma_ts(d, pa_, desc(vd), kIdescPV, acc);
+            if (nv == kGroups) {
 #pragma unroll
-                for (int kk = 0; kk < kGroups; ++kk)
-                    if (kk < nv)
-                        tc::mma_ts(d, pa_ + kk * 8, desc(vd + ((kk * 2048) >> 4)), kIdescPV, acc || kk > 0);
-                tc::commit(bar(kBarPVDone + t));
-                if (release) tc::commit(release);
+                for (int kk = 1; kk < kGroups; ++kk)
+                    tc::mma_ts(d, pa_ + kk * 8, desc(vd + ((kk * 2048) >> 4)), kIdescPV, true);
+            } else {
+#pragma unroll 1
+                for (int kk = 1; kk < nv; ++kk)
+                    tc::mma_ts(d, pa_ + kk * 8, desc(vd + ((kk * 2048) >> 4)), kIdescPV, true);
             }
+            tc::commit(bar(kBarPVDone + t));
+            if (release) tc::commit(release);
         };
-        auto await = [&](uint32_t b, uint32_t parity) { return warp_wait(b, parity, abort, true); };
+        auto await = [&](uint32_t b, uint32_t parity) { return lane_wait(b, parity, abort); };
         static_assert(kVStages == 2, "V stages are counted on in turn");
         // Step i is of stream i % 2: of two query tiles over key tile i / 2, of halves over key
         // tile i. In turn: PV of step i once its P is in TMEM (and, for the first of a piece,
@@ -1104,42 +1159,43 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
             const int steps = nt << (two ? 1 : 0);
             const int tail = groups_used(w, w.j1 - 1);          // 16-key groups of the last tile
             const int b0 = qb.take(two);
-            ok = await(bar(kBarQFull + b0), (qb.uses(b0) - 1) & 1);
-            if (ok && two) ok = await(bar(kBarQFull + 1), (qb.uses(1) - 1) & 1);
+            if (tc::elect_one()) {
+                ok = await(bar(kBarQFull + b0), (qb.uses(b0) - 1) & 1);
+                if (ok && two) ok = await(bar(kBarQFull + 1), (qb.uses(1) - 1) & 1);
 #pragma unroll 1
-            for (int i = -2; ok && i < steps; ++i) {
-                const int t = i & 1;
-                const bool first = !two || t == 0, last = !two || t == 1;       // reader of its tiles
-                const bool more = i + 2 < steps;
-                if (first) {
-                    if (i >= 0) ok = await(bar(kBarVFull + vs), v_phase);
-                    if (ok && more) ok = await(bar(kBarKFull + ks), k_phase);
-                    if (ok && i == 0 && piece > 0) ok = await(bar(kBarOFree), (piece - 1) & 1);
-                }
-                if (ok && i >= 0) ok = await(bar(kBarPReady + t), p_phase >> t & 1);
-                if (!ok) break;
-                if (i >= 0) {
-                    issue_pv(t, vs, i > 1, i + (two ? 2 : 1) < steps ? kGroups : tail, last ? bar(kBarVEmpty + vs) : 0u);
-                    p_phase ^= 1u << t;
-                    if (last) {
-                        vs ^= 1;
-                        v_phase ^= vs == 0 ? 1u : 0u;
+                for (int i = -2; ok && i < steps; ++i) {
+                    const int t = i & 1;
+                    const bool first = !two || t == 0, last = !two || t == 1;       // reader of its tiles
+                    const bool more = i + 2 < steps;
+                    if (first) {
+                        if (i >= 0) ok = await(bar(kBarVFull + vs), v_phase);
+                        if (ok && more) ok = await(bar(kBarKFull + ks), k_phase);
+                        if (ok && i == 0 && piece > 0) ok = await(bar(kBarOFree), (piece - 1) & 1);
+                    }
+                    if (ok && i >= 0) ok = await(bar(kBarPReady + t), p_phase >> t & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (i >= 0) {
+                        issue_pv(t, vs, i > 1, i + (two ? 2 : 1) < steps ? kGroups : tail, last ? bar(kBarVEmpty + vs) : 0u);
+                        p_phase ^= 1u << t;
+                        if (last) {
+                            vs ^= 1;
+                            v_phase ^= vs == 0 ? 1u : 0u;
+                        }
+                    }
+                    if (more) {
+                        issue_s(t, two ? t : b0, ks, last ? bar(kBarKEmpty + ks) : 0u);
+                        if (last) {
+                            ks = ks == kKStages - 1 ? 0 : ks + 1;
+                            k_phase ^= ks == 0 ? 1u : 0u;
+                        }
                     }
                 }
-                if (more) {
-                    issue_s(t, two ? t : b0, ks, last ? bar(kBarKEmpty + ks) : 0u);
-                    if (last) {
-                        ks = ks == kKStages - 1 ? 0 : ks + 1;
-                        k_phase ^= ks == 0 ? 1u : 0u;
-                    }
-                }
+                // the queries' buffers are free once this piece's MMAs are done
+                if (ok) tc::commit(bar(kBarQEmpty + b0));
+                if (ok && two) tc::commit(bar(kBarQEmpty + 1));
             }
-            // the queries' buffers are free once this piece's MMAs are done
-            if (ok && tc::elect_one()) {
-                tc::commit(bar(kBarQEmpty + b0));
-                if (two) tc::commit(bar(kBarQEmpty + 1));
-            }
-            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
             ++piece;
         } while (ok && walk_next<G>(w, a));
         if (tc::elect_one()) tc::commit(bar(kBarDrain));
