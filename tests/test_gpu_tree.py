@@ -293,6 +293,21 @@ def test_large_scores_and_equal_ones():
     b.check()
 
 
+# Scores of powers of two from key tile to key tile, up to about 400 (of 2): rows whose maximum
+# grows by more than the exponent's range, by a little, or falls. 400 units of 2^-24, and what
+# 128 products add, are a few 1e-5 of a weight: inside element_bound's tenth.
+@pytest.mark.parametrize("down", [False, True])
+@pytest.mark.parametrize("nodes,Hq,Hkv", [(40, 16, 2), (20, 16, 2), (6, 16, 2), (3, 16, 2)])
+def test_maxima_that_rise_and_fall(nodes, Hq, Hkv, down):
+    b = Batch([1000, 130, 700], [nodes, nodes, 1], Hq, Hkv)
+    for s in range(3):
+        for j in range(-(-int(b.lens[s]) // b.bs)):
+            e = j * b.bs // 128 - 3
+            b.k[b.tables[s, j].long()] *= 2.0 ** (1 - e if down else e)
+    b.q *= 2.0 ** torch.randint(-4, 3, b.q.shape[:2], device="cuda", generator=torch.Generator("cuda").manual_seed(9))[..., None]
+    b.check()
+
+
 def test_bad_blocks_read_as_zeros():
     b = Batch([200, 50], [9, 40], 8, 2)
     b.tables[0, 3] = b.k.shape[0]

@@ -44,6 +44,8 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     (dict(mb=0), pa.PA_ERR_INVALID_ARG),
     (dict(NB=0), pa.PA_ERR_INVALID_ARG),
     (dict(NB=1 << 27), pa.PA_ERR_UNSUPPORTED),
+    (dict(S=40, mb=1 << 26), pa.PA_ERR_UNSUPPORTED),    # 40 x 8 units of 2^23 key tiles
+    (dict(T=1 << 17, S=1, mb=1 << 22), pa.PA_ERR_UNSUPPORTED),  # 8 x 1024 units of 2^19
     (dict(S=0, q=None, sl=None), pa.PA_OK),
     (dict(T=0, q=None, mask=None), pa.PA_OK),
 ])
