@@ -813,7 +813,7 @@ pa_status_t pa_decode_tree(const void *q, const void *k_cache, const void *v_cac
     // a scale of 0 stands for the smallest number: scores are then 0 to fp32, and a masked
     // one's infinity stays one
     if (a.scale_log2 == 0.f) a.scale_log2 = 1.4e-45f;
-    a.workers = sms;
+    a.workers = std::min(sms, pa::kTreeMaxWorkers);
     pa::tree_carve_workspace(a, workspace);
     const cudaError_t e = pa::launch_decode_tree(a, pa::decode_group_pad(a.group), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -63,6 +63,7 @@ constexpr int kThreads = kSoftmaxThreads + 3 * 32;
 constexpr int kWarpsAll = kThreads / 32;
 constexpr int kGroup = 16;                              // tokens per MMA of P V
 constexpr int kGroups = kKeys / kGroup;                 // 8
+constexpr int kCombineRows = 8;                         // rows merged at a time
 // Places of a unit besides its tiles, for its start and its end: at 2 a batch of 512 units
 // of 16 to 64 tiles takes 277 us, at 3 271, at 4 268, and 480 units of 1 to 8 tiles 45.6,
 // 45.5, 46.6.
@@ -1053,7 +1054,8 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
                 // a unit that begins here and ends in another share: the combine's task
                 if (lane == 0 && w.j0 == 0 && w.j1 < w.q.nt) {
                     const int parts = share_of(w.T + w.q.nt - 1, W, shares) - w_id / w.lanes + 1;
-                    a.tasks[w_id] = make_int4(w.s, w.kvh, w.pair, parts | w.lanes << 16);
+                    const int tokens = min(w.q.n - w.pair * (kPair / G), kPair / G);
+                    a.tasks[w_id] = make_int4(w.q.q0 + w.pair * (kPair / G), w.kvh, tokens, parts | w.lanes << 8);
                 }
                 __syncwarp();
             }
@@ -1212,55 +1214,90 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
     }
 }
 
-// Merge of the parts of the unit that worker blockIdx.x began and others ended: 8 rows
-// x 32 words of 4 dims a CTA. A part's words are [dim / 4][row].
-constexpr int kCombineRows = 8;
+// Merge of the parts of the units that one worker began and others ended, 8 rows x 32 words
+// of 4 dims at a time. A part's words are [dim / 4][row]. Every CTA counts the groups of 8
+// rows of all such units and takes every gridDim.x-th: few units of many parts then have as
+// many CTAs as many of few. (A CTA for each group that there could be, 32 a worker, takes
+// 4 us where no unit has parts; 4 a worker for its own unit's alone take 15 us more for 10
+// units of 15 parts.)
+constexpr int kCombineCtas = 4;              // per worker
 constexpr int kCombineBatch = 4;             // parts whose loads are in flight together
+constexpr int kCombineThreads = kCombineRows * 32;
+static_assert(kTreeMaxWorkers <= kCombineThreads, "a thread for each worker");
 
 template <int G>
-__global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const TreeArgs a) {
+    __shared__ int sums[kCombineThreads / 32];
+    __shared__ int4 unit;                   // of the group at hand
+    __shared__ int unit_w, unit_group;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    const int w = blockIdx.x, r = blockIdx.y * kCombineRows + (threadIdx.x & 7), c = threadIdx.x >> 3;
-    const int4 task = a.tasks[w];
-    if (task.x < 0) return;
-    // share by share of the lane; what is read lies in the workspace
-    const int parts = task.w & 0xffff, lanes = task.w >> 16;
-    if (w + (parts - 1) * lanes >= a.workers) return;
-    const Seq q = load_seq<G>(a, task.x);
-    const int tok = task.z * (kPair / G) + r / G, head = r % G;
-    if (tok >= q.n || head >= a.group) return;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < parts; i0 += kCombineBatch) {
-        float2 e[kCombineBatch];
-        float4 x[kCombineBatch];
+    const int tid = threadIdx.x, c = tid >> 3;
+    // thread i has worker i's task; what a task leads to lies in the workspace
+    const int4 mine = tid < a.workers ? a.tasks[tid] : make_int4(-1, 0, 0, 0);
+    const int parts_mine = mine.w & 0xff, lanes_mine = mine.w >> 8;
+    const bool there = mine.x >= 0 && tid + (parts_mine - 1) * lanes_mine < a.workers;
+    const int groups = there ? (mine.z * G + kCombineRows - 1) / kCombineRows : 0;
+    int end = groups;
 #pragma unroll
-        for (int k = 0; k < kCombineBatch; ++k) {
-            const int i = i0 + k;
-            if (i < parts) {
-                const int64_t slot = i == 0 ? 2 * w + 1 : 2 * (w + i * lanes);
-                e[k] = a.part_ml[slot * kPair + r];
-                x[k] = a.part_o[(slot * 32 + c) * kPair + r];
+    for (int off = 1; off < 32; off <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, end, off);
+        if ((tid & 31) >= off) end += n;
+    }
+    if ((tid & 31) == 31) sums[tid >> 5] = end;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int k = 0; k < kCombineThreads / 32; ++k) {
+        if (k < tid >> 5) end += sums[k];
+        total += sums[k];
+    }
+#pragma unroll 1
+    for (int item = blockIdx.x; item < total; item += gridDim.x) {
+        if (item < end && item >= end - groups) {
+            unit = mine;
+            unit_w = tid;
+            unit_group = item - (end - groups);
+        }
+        __syncthreads();
+        const int4 task = unit;
+        const int w = unit_w, r = unit_group * kCombineRows + (tid & 7);
+        __syncthreads();
+        const int parts = task.w & 0xff, lanes = task.w >> 8;
+        const int tok = r / G, head = r % G;
+        if (tok >= task.z || head >= a.group) continue;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < parts; i0 += kCombineBatch) {
+            float2 e[kCombineBatch];
+            float4 x[kCombineBatch];
+#pragma unroll
+            for (int k = 0; k < kCombineBatch; ++k) {
+                const int i = i0 + k;
+                if (i < parts) {
+                    const int64_t slot = i == 0 ? 2 * w + 1 : 2 * (w + i * lanes);
+                    e[k] = a.part_ml[slot * kPair + r];
+                    x[k] = a.part_o[(slot * 32 + c) * kPair + r];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kCombineBatch; ++k) {
+                if (i0 + k >= parts || e[k].y == 0.f) continue;         // no token seen in the part
+                const float mn = fmaxf(m, e[k].x);
+                const float al = ex2(m - mn), be = ex2(e[k].x - mn);
+                l = l * al + e[k].y * be;
+                o.x = o.x * al + x[k].x * be;
+                o.y = o.y * al + x[k].y * be;
+                o.z = o.z * al + x[k].z * be;
+                o.w = o.w * al + x[k].w * be;
+                m = mn;
             }
         }
-#pragma unroll
-        for (int k = 0; k < kCombineBatch; ++k) {
-            if (i0 + k >= parts || e[k].y == 0.f) continue;         // no token seen in the part
-            const float mn = fmaxf(m, e[k].x);
-            const float al = ex2(m - mn), be = ex2(e[k].x - mn);
-            l = l * al + e[k].y * be;
-            o.x = o.x * al + x[k].x * be;
-            o.y = o.y * al + x[k].y * be;
-            o.z = o.z * al + x[k].z * be;
-            o.w = o.w * al + x[k].w * be;
-            m = mn;
-        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t row = ((int64_t)task.x + tok) * a.num_q_heads + (int64_t)task.y * a.group + head;
+        reinterpret_cast<uint2 *>(a.out)[row * 32 + c] =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t row = ((int64_t)q.q0 + tok) * a.num_q_heads + (int64_t)task.y * a.group + head;
-    reinterpret_cast<uint2 *>(a.out)[row * 32 + c] =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
 // q [total_q, Hq, 128] as (128, Hq, total_q) with boxes of 64 dims x G heads x
@@ -1308,10 +1345,8 @@ cudaError_t launch_g(const TreeArgs &a, cudaStream_t st) {
     e = launch_dependent(reinterpret_cast<const void *>(&tree_kernel<G>), dim3((unsigned)a.workers), kThreads,
                          kSmemBytes, args, st);
     if (e != cudaSuccess) return e;
-    const int64_t rows = (int64_t)a.total_q * G < kPair ? (int64_t)a.total_q * G : kPair;   // of a unit, at most
     return launch_dependent(reinterpret_cast<const void *>(&tree_combine_kernel<G>),
-                            dim3((unsigned)a.workers, (unsigned)((rows + kCombineRows - 1) / kCombineRows)),
-                            kCombineRows * 32, 0, args, st);
+                            dim3((unsigned)(a.workers * kCombineCtas)), kCombineThreads, 0, args, st);
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }

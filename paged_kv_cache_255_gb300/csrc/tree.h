@@ -33,10 +33,14 @@ struct TreeArgs {
     float scale_log2;
     int workers;                    // CTAs the work is shared among
     // in the workspace
-    int4 *tasks;                    // [workers] the unit that a worker's share leaves unfinished
+    int4 *tasks;                    // [workers] the unit that a share leaves unfinished: first query row (-1: none), KV
+                                    // head, query rows, parts and (from bit 8) the workers between them
     float4 *part_o;                 // [2 workers][32][256] parts of units that several workers share
     float2 *part_ml;                // [2 workers][256] (running max in log2 units, sum)
 };
+
+// A task packs counts of workers into bytes, and the merge has a thread for each worker.
+constexpr int kTreeMaxWorkers = 255;
 
 size_t tree_workspace_bytes(int workers);
 void tree_carve_workspace(TreeArgs &a, void *workspace);
