@@ -16,7 +16,10 @@
  *     Key highlights: paged attention for decoding).
  *
  * pagedattn/blocks.h declares the operations on the pools' blocks (copy, fork,
- * free, compact), pagedattn/decode_shared.h decode over shared prefixes.
+ * free, compact), pagedattn/decode_shared.h decode over shared prefixes,
+ * pagedattn/rotary.h rotary positions and norms of heads, alone and on the way
+ * into the cache, pagedattn/decode_tree.h decode over trees of drafted tokens
+ * and keeping the accepted ones.
  *
  * Layouts (all row-major, contiguous, bf16 = IEEE bfloat16):
  *   q            [num_seqs, num_q_heads, head_dim]                 bf16
@@ -346,25 +349,27 @@ PA_API pa_status_t pa_prefill_layout(const void *q, const void *k_cache, const v
 /*
  * Device-side error record. The kernels do not fault or hang on their inputs:
  * an index outside its range is handled in a defined way, and every mbarrier
- * wait is bounded (the hand-offs between the warps of the prefill kernel and of
- * the one that computes shared prefixes, about 2 s; a decode warp's wait for its
+ * wait is bounded (the hand-offs between the warps of the prefill kernel, of the
+ * one that computes shared prefixes and of decode over trees, about 2 s; a decode warp's wait for its
  * own tile copies, about 1 s). Each such
  * event is recorded on the device, the first code of each kernel kind kept,
  * without any synchronization in the calls themselves.
  * This call synchronizes `stream`, stores the smallest recorded code in *code
  * and clears every record:
  *   0  none;
- *   1  pa_prefill / pa_decode_shared: shared memory not 1024-byte aligned; the
+ *   1  pa_prefill / pa_decode_shared / pa_decode_tree: shared memory not 1024-byte aligned; the
  *      launch's outputs are undefined;
  *   2  pa_prefill, or any decode call: a bounded wait ran out; the launch's
  *      outputs are undefined;
- *   3  pa_store_kvcache: a slot outside [-1, num_blocks * block_size) was
- *      skipped; nothing is written for that row;
- *   4  pa_decode / pa_decode_multi / pa_decode_shared / pa_prefill: a block-table
- *      entry that covers context tokens lies outside [0, num_blocks); its rows
- *      are read as zeros, so each of those keys scores 0 and adds a zero value;
+ *   3  pa_store_kvcache, pa_append_kvcache: a slot outside
+ *      [-1, num_blocks * block_size) was skipped; nothing is written for that row;
+ *   4  pa_decode / pa_decode_multi / pa_decode_shared / pa_decode_tree /
+ *      pa_prefill: a block-table entry that covers context tokens lies outside
+ *      [0, num_blocks); its rows are read as zeros, so each of those keys scores 0
+ *      and adds a zero value;
  *   5  a block operation: a row or block id out of range, or an owned entry
  *      whose block had count 0; that item was skipped (fork: passed on);
+ *      pa_keep_tokens: the same, or an accepted path that is not one;
  *   6  pa_fork_blocks: a fork was refused (its child row was not empty or was
  *      listed before, or no block was free).
  * Entries past a sequence's last block are never read and never reported.
@@ -373,11 +378,12 @@ PA_API pa_status_t pa_take_device_error(int32_t *code, void *stream);
 
 /*
  * Test hook for the error path above, off by default: with mode 1, later
- * pa_prefill / pa_prefill_layout launches (tcgen05 kernel), and the kernel that
- * computes the prefixes of later pa_decode_shared calls, hold back one barrier
- * arrival of their V producer, so that a wait runs out after about 2 s and the
- * launch records code 2 and returns, its outputs undefined; mode 0 restores
- * normal launches. Process-wide; for tests only.
+ * pa_prefill / pa_prefill_layout launches (tcgen05 kernel), the kernel that
+ * computes the prefixes of later pa_decode_shared calls, and that of later
+ * pa_decode_tree calls hold back one barrier arrival of their V producer, so
+ * that a wait runs out after about 2 s and the launch records code 2 and
+ * returns, its outputs undefined; mode 0 restores normal launches.
+ * Process-wide; for tests only.
  */
 PA_API pa_status_t pa_debug_prefill_fault(int mode);
 

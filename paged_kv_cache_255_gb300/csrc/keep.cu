@@ -12,6 +12,11 @@
 //                  look the rows up once
 //   finish_kernel  a warp per sequence: the new length, and the blocks given back; a
 //                  programmatic dependent, as the moves read both
+//
+// Bound by latency: list, table entry and row are three loads that wait for one another,
+// and then the second launch: one layer of 4 sequences 6 us, 16 layers of 64 sequences (32
+// pools, 21 MB read and written, 6.2 us of bytes) 14, the copy of the tables that the
+// measurement needs included.
 #include "common.cuh"
 #include "tree.h"
 

@@ -16,7 +16,14 @@
 // 16-byte chunks (neighbours when interleaved, rot_dim / 2 dims apart otherwise), so
 // a pair never leaves its lane; a warp works on four rows at a time. The 64 sines
 // and cosines of a token are computed once per warp, two pairs a lane, handed round
-// by shuffles, and used for all heads the warp takes.
+// by shuffles, and used for all heads the warp takes. Four quads of rows per warp are on
+// their way into shared memory, so that loads wait for no arithmetic, which is two lanes'
+// floats an instruction.
+//
+// Bound by memory: 16384 tokens of 40 heads, normed and rotated, 52.2 us (6.43 TB/s read
+// and written, 0.95 of a copy), of 80 heads with K and V on their way into the cache 102.8
+// (6.53 TB/s, 0.96); 1024 tokens of 48 heads (7.4 us of bytes) 14.5, where a warp has a
+// handful of quads; 4 tokens 2.4, a launch.
 #include <algorithm>
 #include <climits>
 #include <cmath>

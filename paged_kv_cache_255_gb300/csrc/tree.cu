@@ -33,6 +33,17 @@
 //   warps 8, 9       K and V producers: TMA boxes of a block's tokens (16 .. 128) x 64
 //                    dims; the V warp also loads the queries
 //   warp 10          issues S = Q K^T and O += P V as their inputs arrive
+// Measured (calls in a graph, both kernels): 8 contexts of 32k to 131k tokens, up to 128 rows
+// a unit, 406 - 418 us, 6.4 - 6.6 TB/s of 6.79: bound by memory. 512 units of 192 to 256 rows
+// over 16 to 64 key tiles 271 - 290 us, 1070 - 1150 TFLOP/s of 1939: the tensor pipe is busy for
+// 59 % of the cycles. A step's products take 2 x (512 + 512) cycles alone, about 1400 a query
+// tile beside the other stream's TMEM traffic and the tiles' arrival (a product from shared memory
+// reads 128 B a cycle, all there is), and a stream's chain P -> PV -> S -> P is 2700. 480 units of
+// 1 to 8 tiles 42.4 us, where the floor is 21: 3 us until the plan is made, then 5 per unit
+// of dependent steps (tiles, S, softmax, PV, result), and 3 for the merge. A softmax with a
+// polynomial for a part of its powers of two is slower (a quarter of them: 319 us against 304):
+// the XU pipe is busy for 28 %.
+//
 // Hand-offs are mbarriers; every wait is bounded (about 2 s), and a wait that ran out
 // makes every role skip to its end. A role ends when what it has in flight has landed
 // (or 0.1 s later); then the CTA frees its TMEM.
@@ -420,8 +431,8 @@ __device__ __forceinline__ bool reaches_nodes(const volatile Walk &w, int j) {
 
 // A V tile in shared memory whose keys reach the nodes: rows past the last token become
 // zero, and so do the elements of nodes' rows that are not finite; the words of 32 nodes
-// that had some are marked in `odd`. By the 128 threads of a stream. The 16-byte chunks of a row are permuted within it (128-byte
-// swizzle), which does not matter here.
+// that had some are marked in `odd`. By the 128 threads of a stream. The 16-byte chunks of a
+// row are permuted within it (128-byte swizzle), which does not matter here.
 __device__ __noinline__ void clean_v(const volatile Walk &w, int j, uint8_t *vtile, uint32_t *odd, int words,
                                         int thread) {
     const int node0 = j * kKeys - (w.q.L - w.q.n);              // node of the tile's first key
@@ -432,7 +443,8 @@ __device__ __noinline__ void clean_v(const volatile Walk &w, int j, uint8_t *vti
         uint4 x[kBatch];
         auto place = [&](int k) {
             const int i = i0 + kRows * k;
-            return reinterpret_cast<uint4 *>(vtile + ((i >> 3) & 1) * kKVHalf + (first + (i >> 4)) * 128 + (i & 7) * 16);
+            return reinterpret_cast<uint4 *>(vtile + ((i >> 3) & 1) * kKVHalf + (first + (i >> 4)) * 128 +
+                                             (i & 7) * 16);
         };
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
@@ -1147,8 +1159,11 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
         // the previous piece's results have been read), then S of step i + 2. The tiles they
         // need have been waited for before, off the chain from P to S. A stage is released
         // after its last reader.
-        // (A wait costs 130 cycles also where nothing is to wait for, and a step's products take
-        // 1024: a second reader does not wait for its tiles, and the rings' places are counted on.)
+        // (One lane does all of it: an elected lane a product had the warp part and meet four
+        // times a step, 304 us against 298. A wait costs 50 to 100 cycles also where nothing is to
+        // wait for: a second reader does not wait for its tiles, and the rings' places are
+        // counted on. Tiles seen by a softmax warp, so that P alone is waited for here, made it
+        // 289 against 277: what looks like waiting for V is the queue of products.)
         int vs = 0, ks = 0;                     // next V and K stage, and their phases
         uint32_t v_phase = 0, k_phase = 0, p_phase = 0;         // (p_phase: bit t, of stream t)
         int piece = 0;

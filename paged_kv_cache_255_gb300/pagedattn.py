@@ -872,7 +872,7 @@ def take_device_error(stream=None, device=None) -> int:
     """Synchronize the stream and return (and clear) the smallest device-side
     error code recorded so far: 0 none, 1 shared memory misaligned, 2 a wait
     ran out, 3 a bad slot, 4 a bad block id, 5 a bad row or block in a block
-    operation, 6 a fork refused."""
+    operation (or a path that is none in keep_tokens), 6 a fork refused."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     code = ctypes.c_int32(0)
     with torch.cuda.device(dev):
@@ -882,9 +882,9 @@ def take_device_error(stream=None, device=None) -> int:
 
 
 def debug_prefill_fault(mode: int) -> None:
-    """Test hook (off by default): mode 1 makes later prefill launches, and the
-    prefix kernel of later decode_shared calls, hold back one barrier arrival so
-    that a bounded wait runs out and code 2 is recorded; mode 0 turns it off."""
+    """Test hook (off by default): mode 1 makes later prefill launches, the
+    prefix kernel of later decode_shared calls and the kernel of later
+    decode_tree calls hold back one barrier arrival so that a bounded wait runs out and code 2 is recorded; mode 0 turns it off."""
     _check("pa_debug_prefill_fault", lib().pa_debug_prefill_fault(int(mode)))
 
 
