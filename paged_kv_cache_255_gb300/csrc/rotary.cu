@@ -22,7 +22,7 @@
 //
 // Bound by memory: 16384 tokens of 40 heads, normed and rotated, 52.2 us (6.43 TB/s read
 // and written, 0.95 of a copy), of 80 heads with K and V on their way into the cache 102.8
-// (6.53 TB/s, 0.96); 1024 tokens of 48 heads (7.4 us of bytes) 14.5, where a warp has a
+// (6.53 TB/s, 0.96); 2047 tokens of 48 heads (7.4 us of bytes) 14.5, where a warp has a
 // handful of quads; 4 tokens 2.4, a launch.
 #include <algorithm>
 #include <climits>
