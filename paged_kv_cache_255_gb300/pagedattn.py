@@ -757,6 +757,14 @@ class Rotary:
             self._addr, int(rot_dim), int(bool(interleaved)), float(base), self.SCALINGS.index(scaling),
             float(factor), float(original_context), low, high, 0.0 if amplitude is None else float(amplitude)))
 
+    # a copy has a struct of its own, and its address
+    def __getstate__(self):
+        return bytes(self._struct)
+
+    def __setstate__(self, state):
+        self._struct = _RotaryStruct.from_buffer_copy(state)
+        self._addr = ctypes.addressof(self._struct)
+
     rot_dim = property(lambda self: self._struct.rot_dim)
     interleaved = property(lambda self: bool(self._struct.interleaved))
     amplitude = property(lambda self: self._struct.amplitude)

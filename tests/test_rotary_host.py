@@ -1,8 +1,10 @@
 """Rotation of heads and appends with it, CPU side: frequencies, refusals before
 any CUDA call, the header from strict C99, the NVTX ranges."""
+import copy
 import ctypes
 import math
 import os
+import pickle
 import re
 import shutil
 import subprocess
@@ -31,6 +33,13 @@ def test_frequencies(pa_lib, scaling, rot_dim, base, factor, original):
         assert abs(got / 2 ** 64 * 2 * math.pi - theta) <= 1e-12 * theta + 2 * math.pi * 2 ** -64
     assert R.rot_dim == rot_dim and not R.interleaved
     assert list(R._struct.turns)[rot_dim // 2:] == [0] * (64 - rot_dim // 2)
+
+
+def test_copies_do_not_share_memory(pa_lib):
+    R = pa.Rotary(64, interleaved=True, scaling="yarn", factor=4.0, original_context=4096)
+    for C in (copy.copy(R), copy.deepcopy(R), pickle.loads(pickle.dumps(R))):
+        assert bytes(C._struct) == bytes(R._struct) and (C.rot_dim, C.interleaved) == (64, True)
+        assert C._addr == ctypes.addressof(C._struct) != R._addr
 
 
 def test_frequencies_of_more_than_a_turn_and_negative(pa_lib):
