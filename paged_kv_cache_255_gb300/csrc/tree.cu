@@ -75,9 +75,9 @@ constexpr int kWarpsAll = kThreads / 32;
 constexpr int kGroup = 16;                              // tokens per MMA of P V
 constexpr int kGroups = kKeys / kGroup;                 // 8
 constexpr int kCombineRows = 8;                         // rows merged at a time
-// Places of a unit besides its tiles, for its start and its end: at 2 a batch of 512 units
-// of 16 to 64 tiles takes 277 us, at 3 271, at 4 268, and 480 units of 1 to 8 tiles 45.6,
-// 45.5, 46.6.
+// Places of a unit besides its tiles, for its start and its end: at 0, 1, 2, 3 a batch of 512
+// units of 16 to 64 tiles takes 297, 285, 282, 274 us, and 480 units of 1 to 8 tiles 55.4,
+// 47.3, 42.3, 42.6; at 4 the first gains 3 more and the second loses 1.
 constexpr int kUnitPlaces = 3;
 constexpr uint32_t kQBytes = kRows * kRowBytes;         // 32 KB: 2 halves of [128][128 B]
 constexpr uint32_t kQHalf = kRows * 128;
