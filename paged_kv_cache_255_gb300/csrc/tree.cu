@@ -103,9 +103,9 @@ constexpr uint32_t kNumBars = kBarDrain + 1;
 constexpr uint32_t kOffTmemSlot = kOffCtl + 8 * kNumBars;
 constexpr uint32_t kOffAbort = kOffTmemSlot + 4;
 constexpr uint32_t kWalkBytes = 56;
-constexpr uint32_t kOffWalk = (kOffAbort + 4 + 15) & ~15u;        // one Walk per warp
+constexpr uint32_t kOffWalk = (kOffAbort + 4 + 15) & ~15u;        // one Walk per warp, and the plan's
 constexpr int kOddSets = 4;                                       // of the pieces in flight: bit i, nodes 32 i ..
-constexpr uint32_t kOffOdd = kOffWalk + kWalkBytes * kWarpsAll;   // 32 i + 31 have V that is not finite
+constexpr uint32_t kOffOdd = kOffWalk + kWalkBytes * (kWarpsAll + 1);   // 32 i + 31 have V that is not finite
 constexpr uint32_t kOffHalves = kOffOdd + 4 * kOddSets;           // [2][128] float2; before that the plan's sums
 constexpr uint32_t kSmemBytes = kOffHalves + 2 * kRows * 8;
 static_assert(kSmemBytes <= 232448, "shared memory");
@@ -234,9 +234,9 @@ __device__ __noinline__ Seq load_seq(const TreeArgs &a, int s) {
     return r;
 }
 
-// Places of a sequence's units in one of `lanes` lanes. (The host has ruled out 2^31 places.)
-__device__ __forceinline__ int seq_places(const Seq &q, int num_kv_heads, int lanes) {
-    return q.pairs / lanes * num_kv_heads * (q.nt + kUnitPlaces);
+// Places of a sequence's units. (The host has ruled out 2^31 places.)
+__device__ __forceinline__ int seq_places(const Seq &q, int num_kv_heads) {
+    return q.pairs * num_kv_heads * (q.nt + kUnitPlaces);
 }
 
 // A share's walk over the flat space of its lane, sequence by sequence, KV head, pair, key
@@ -285,10 +285,12 @@ __device__ __noinline__ bool walk_next(volatile Walk &place, const TreeArgs &a) 
     return more;
 }
 
-// Where share i of `shares` begins among W places: floor(i W / shares).
+// Where share i of `shares` begins among W places: floor(i W / shares). Both factors of the
+// second term are below 256: half a unit, 1 / 512 of a share, is more than its quotient in
+// fp32 is off by.
 __device__ __forceinline__ int share_begin(int i, int W, int shares) {
     const int each = W / shares;
-    return i * each + i * (W - each * shares) / shares;
+    return i * each + (int)__fdividef((float)(i * (W - each * shares)) + 0.5f, (float)shares);
 }
 
 // The share that place T is in: a guess, which is off by one at most.
@@ -299,83 +301,124 @@ __device__ __forceinline__ int share_of(int T, int W, int shares) {
     return i;
 }
 
+// Sum of a thread's number over the threads before it in its warp, and its own.
+__device__ __forceinline__ int warp_scan(int v, int lane) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += n;
+    }
+    return v;
+}
+
 // The places of a lane, its shares, and this CTA's first piece (in `first`, shared memory);
-// false when it has none. All threads call it; `sums` is scratch.
+// false when it has none. All threads call it; `sums` is scratch. A chain of dependent steps
+// that every CTA goes through before its first tile: of up to kThreads sequences thread i
+// has the i-th, which is scanned and summed at once, and there are no divisions but those
+// that a batch needs: 4100 to 5800 cycles, of which 2000 wait for the lengths (with two
+// scans and every division 1100 more).
 template <int G>
 __device__ __noinline__ bool plan_share(const TreeArgs &a, Walk *first, volatile int *sums, int &W, int &shares) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = a.num_seqs, Hkv = a.num_kv_heads;
     Seq mine{};
-    unsigned all = 0, one = 0;                  // places of all pairs, and of one pair a unit
+    int own = 0;                                // places of this thread's sequence of the first kThreads
+    unsigned later = 0;                         // of those after them
     unsigned most = 0, least = INT_MAX;         // pairs of a sequence
 #pragma unroll 1
     for (int s = tid; s < S; s += kThreads) {
         const Seq q = load_seq<G>(a, s);
-        if (s == tid) mine = q;
+        const int places = seq_places(q, Hkv);
+        if (s == tid) {
+            mine = q;
+            own = places;
+        } else {
+            later += places;
+        }
         if (q.pairs == 0) continue;
-        all += seq_places(q, Hkv, 1);
-        one += seq_places(q, Hkv, q.pairs);
         most = max(most, q.pairs);
         least = min(least, q.pairs);
     }
-    all = __reduce_add_sync(0xffffffffu, all);
-    one = __reduce_add_sync(0xffffffffu, one);
+    int scan = warp_scan(own, lane);
     most = __reduce_max_sync(0xffffffffu, most);
     least = __reduce_min_sync(0xffffffffu, least);
-    if (lane == 0) {
-        sums[warp] = all;
-        sums[32 + warp] = one;
-        sums[64 + warp] = most;
-        sums[96 + warp] = least;
+    if (S > kThreads) later = __reduce_add_sync(0xffffffffu, later);
+    if (lane == 31) {
+        sums[warp] = scan;
+        sums[32 + warp] = most;
+        sums[64 + warp] = least;
+        sums[96 + warp] = later;
     }
     if (tid == 0) first->T1 = -1;               // nothing found yet
     __syncthreads();
     // every warp adds up all warps' sums
-    const bool mine_too = lane < kWarpsAll;
-    all = __reduce_add_sync(0xffffffffu, mine_too ? sums[lane] : 0);
-    one = __reduce_add_sync(0xffffffffu, mine_too ? sums[32 + lane] : 0);
-    most = __reduce_max_sync(0xffffffffu, mine_too ? sums[64 + lane] : 0);
-    least = __reduce_min_sync(0xffffffffu, mine_too ? sums[96 + lane] : INT_MAX);
+    const bool there = lane < kWarpsAll;
+    const int x = there ? sums[lane] : 0;
+    most = __reduce_max_sync(0xffffffffu, there ? sums[32 + lane] : 0);
+    least = __reduce_min_sync(0xffffffffu, there ? sums[64 + lane] : INT_MAX);
+    int chunk = (int)__reduce_add_sync(0xffffffffu, (unsigned)x);
+    int excl = scan - own + (int)__reduce_add_sync(0xffffffffu, (unsigned)(lane < warp ? x : 0));
+    W = chunk;
+    if (S > kThreads) W += (int)__reduce_add_sync(0xffffffffu, there ? (unsigned)sums[96 + lane] : 0u);
     // where all have the same number of pairs, the pairs are lanes
-    const int lanes = most == least && (int)most <= a.workers ? most : 1;
-    W = lanes > 1 ? one : all;
-    shares = max(1, min(W, a.workers / lanes));
-    const int w = blockIdx.x / lanes;
+    const int lanes = most == least && (int)most <= a.workers ? (int)most : 1;
+    const bool side = lanes > 1;
+    shares = a.workers;
+    int w = blockIdx.x, my_lane = 0;
+    if (side) {
+        W /= lanes;
+        shares /= lanes;
+        w /= lanes;
+        my_lane = blockIdx.x - w * lanes;
+    }
+    shares = max(1, min(W, shares));
     if (w >= shares || W == 0) return false;
-    const int T0 = share_begin(w, W, shares);
+    const int T0 = share_begin(w, W, shares), T1 = share_begin(w + 1, W, shares);
     int base = 0;
 #pragma unroll 1
-    for (int c0 = 0; c0 < S && base <= T0; c0 += kThreads) {
-        const int s = c0 + tid;
-        if (c0 > 0 && s < S) mine = load_seq<G>(a, s);
-        const int own = s < S ? seq_places(mine, Hkv, lanes) : 0;
-        int v = own;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int n = __shfl_up_sync(0xffffffffu, v, off);
-            if (lane >= off) v += n;
+    for (int c0 = 0;;) {
+        if (side) {
+            own /= lanes;
+            excl /= lanes;
+            chunk /= lanes;
         }
-        __syncthreads();                        // the sums before have been read
-        if (lane == 31) sums[warp] = v;
-        __syncthreads();
-        const int x = mine_too ? sums[lane] : 0;
-        const int excl = base + v - own + __reduce_add_sync(0xffffffffu, (unsigned)(lane < warp ? x : 0));
+        excl += base;
         if (own > 0 && T0 >= excl && T0 < excl + own) {
-            const int rem = T0 - excl, places = mine.nt + kUnitPlaces, per_head = mine.pairs / lanes;
+            const int rem = T0 - excl, places = mine.nt + kUnitPlaces;
             const int unit = rem / places;
+            int kvh = unit, pair = 0;
+            if (mine.pairs > lanes) {
+                const int per_head = side ? mine.pairs / lanes : mine.pairs;
+                kvh = unit / per_head;
+                pair = unit - kvh * per_head;
+            }
             first->T = T0;
-            first->T1 = share_begin(w + 1, W, shares);
+            first->T1 = T1;
             first->q = mine;
-            first->s = s;
-            first->lane = blockIdx.x % lanes;
+            first->s = c0 + tid;
+            first->lane = my_lane;
             first->lanes = lanes;
-            first->kvh = unit / per_head;
-            first->pair = first->lane + lanes * (unit % per_head);
+            first->kvh = kvh;
+            first->pair = my_lane + lanes * pair;
             first->j0 = rem - unit * places;
             if (first->j0 < mine.nt) piece_end(*first);
             else if (!next_unit<G>(*first, a)) first->T1 = -1;      // past the unit's tiles
         }
-        base += __reduce_add_sync(0xffffffffu, (unsigned)x);
+        base += chunk;
+        c0 += kThreads;
+        if (c0 >= S || base > T0) break;
+        own = 0;
+        if (c0 + tid < S) {
+            mine = load_seq<G>(a, c0 + tid);
+            own = seq_places(mine, Hkv);
+        }
+        scan = warp_scan(own, lane);
+        __syncthreads();                        // the sums before have been read
+        if (lane == 31) sums[warp] = scan;
+        __syncthreads();
+        const int y = there ? sums[lane] : 0;
+        chunk = (int)__reduce_add_sync(0xffffffffu, (unsigned)y);
+        excl = scan - own + (int)__reduce_add_sync(0xffffffffu, (unsigned)(lane < warp ? y : 0));
     }
     __syncthreads();
     return first->T1 >= 0;
@@ -999,14 +1042,12 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     int W, shares;
     Walk *walks = reinterpret_cast<Walk *>(smem + kOffWalk);
-    const bool works = plan_share<G>(a, walks, reinterpret_cast<volatile int *>(smem + kOffHalves), W, shares);
+    const bool works = plan_share<G>(a, walks + kWarpsAll, reinterpret_cast<volatile int *>(smem + kOffHalves), W, shares);
     // the place of the first piece, for each warp its own
-    {
-        const Walk first = walks[0];
-        __syncthreads();
-        if ((tid & 31) == 0) walks[warp] = first;
-        __syncwarp();
-    }
+    if ((tid & 31) < kWalkBytes / 4)
+        reinterpret_cast<volatile int *>(walks + warp)[tid & 31] =
+            reinterpret_cast<volatile int *>(walks + kWarpsAll)[tid & 31];
+    __syncwarp();
     volatile Walk &w = walks[warp];
     const int w_id = blockIdx.x;
     if (warp == kVWarp && (tid & 31) == 0) a.tasks[w_id] = make_int4(-1, 0, 0, 0);
