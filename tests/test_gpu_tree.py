@@ -204,6 +204,19 @@ def test_runs_of_sequences_without_nodes():
     Batch(base, nodes, 4, 2).check()
 
 
+# every tree of the same number of units: they are shared side by side, in few and many
+# sequences, some without nodes or context; and more of them than SMs
+@pytest.mark.parametrize("S,lo,hi,Hq,Hkv", [(1, 97, 128, 8, 1), (7, 65, 128, 8, 2), (5, 129, 192, 12, 3), (400, 65, 128, 8, 2),
+                                            (800, 33, 64, 16, 2), (1, 5000, 5000, 8, 1)])
+def test_units_side_by_side(S, lo, hi, Hq, Hkv):
+    rng = np.random.default_rng(S + lo)
+    base, nodes = rng.integers(0, 500, S), rng.integers(lo, hi + 1, S)
+    if S > 1:
+        nodes[rng.permutation(S)[:S // 5]] = 0
+    same = int(rng.integers(1, 1 << 40)) | 1
+    Batch(base, nodes, Hq, Hkv, masks=lambda r, n: [same & (1 << n) - 1] * n, mask_words=3).check()
+
+
 # one unit over all SMs, units cut into two or three, more units than SMs
 @pytest.mark.parametrize("base,nodes,Hq,Hkv", [
     ([40000], [5], 4, 1), ([20000], [60], 8, 1), ([9000, 5], [100, 3], 4, 1), ([3000] * 5, [33] * 5, 16, 8),
