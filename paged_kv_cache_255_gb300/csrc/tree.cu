@@ -767,9 +767,9 @@ __device__ __forceinline__ void narrow_tile(uint32_t tS, uint32_t tO, float sc, 
 
 // An element of a result from those of both streams; a row that saw nothing outputs zero,
 // whatever its O. (A second O that is not there may be anything.)
-__device__ __forceinline__ float merged(uint32_t o, uint32_t o2, float fa, bool b_too, float fb, float lsum, float inv) {
+__device__ __forceinline__ float merged(uint32_t o, uint32_t o2, float fa, bool b_too, float fb, bool none) {
     const float x = __uint_as_float(o) * fa, y = fmaf(__uint_as_float(o2), fb, x);
-    return lsum == 0.f ? 0.f : (b_too ? y : x) * inv;
+    return none ? 0.f : (b_too ? y : x);
 }
 __device__ __forceinline__ uint4 pack(const float *f) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
@@ -900,32 +900,51 @@ __device__ __forceinline__ bool softmax_piece(const TreeArgs &a, const volatile 
         const int slot = 2 * (int)blockIdx.x + (w.j0 == 0 ? 1 : 0);
         float4 *po = a.part_o + (int64_t)slot * 32 * kPair + tile * kRows;
         const int d0 = two ? 0 : 64 * wg, d1 = two ? kHeadDim : d0 + 64;
-        float inv[NR];
+        bool none[NR];
 #pragma unroll
         for (int x = 0; x < NR; ++x) {
-            inv[x] = whole ? 1.f / lsum[x] : 1.f;
+            const float inv = whole ? 1.f / lsum[x] : 1.f;
+            none[x] = lsum[x] == 0.f;
+            fa[x] *= inv;
+            fb[x] *= inv;
             if (!whole && rv[x] && first && (two || wg == 0))
                 a.part_ml[(int64_t)slot * kPair + tile * kRows + row0 + 8 * x] = make_float2(m[x], lsum[x]);
         }
         if constexpr (R == 0) {
             uint4 *orow = out_row(row0);
+            // 8 dims of the row
+            auto put = [&](int d, const float *y) {
+                if (rv[0] && whole) {
+                    orow[d / 8] = pack(y);
+                } else if (rv[0]) {
+                    po[(d / 4) * kPair + row0] = make_float4(y[0], y[1], y[2], y[3]);
+                    po[(d / 4 + 1) * kPair + row0] = make_float4(y[4], y[5], y[6], y[7]);
+                }
+            };
+            if (two) {
 #pragma unroll 1
-            for (int d = d0; d < d1; d += 16) {
-                uint32_t o[16], o2[16];
-                tc::tmem_ld16((two ? tO : tmem + lane + 128) + d, o);
-                tc::tmem_ld16(tmem + lane + 384 + d, o2);
-                tc::tmem_ld_wait();
-                float y[16];
+                for (int d = 0; d < kHeadDim; d += 32) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(tO + d, o);
+                    tc::tmem_ld_wait();
+                    float y[32];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) y[c] = merged(o[c], o2[c], fa[0], b_too, fb[0], lsum[0], inv[0]);
+                    for (int c = 0; c < 32; ++c) y[c] = none[0] ? 0.f : __uint_as_float(o[c]) * fa[0];
 #pragma unroll
-                for (int c = 0; c < 16; c += 8) {
-                    if (rv[0] && whole) {
-                        orow[(d + c) / 8] = pack(y + c);
-                    } else if (rv[0]) {
-                        po[((d + c) / 4) * kPair + row0] = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
-                        po[((d + c) / 4 + 1) * kPair + row0] = make_float4(y[c + 4], y[c + 5], y[c + 6], y[c + 7]);
-                    }
+                    for (int c = 0; c < 32; c += 8) put(d + c, y + c);
+                }
+            } else {
+#pragma unroll 1
+                for (int d = 64 * wg; d < 64 * wg + 64; d += 16) {
+                    uint32_t o[16], o2[16];
+                    tc::tmem_ld16(tmem + lane + 128 + d, o);
+                    tc::tmem_ld16(tmem + lane + 384 + d, o2);
+                    tc::tmem_ld_wait();
+                    float y[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) y[c] = merged(o[c], o2[c], fa[0], b_too, fb[0], none[0]);
+#pragma unroll
+                    for (int c = 0; c < 16; c += 8) put(d + c, y + c);
                 }
             }
         } else {
@@ -949,8 +968,8 @@ __device__ __forceinline__ bool softmax_piece(const TreeArgs &a, const volatile 
 #pragma unroll
                     for (int x = 0; x < NR; ++x) {
                         const int i = 4 * k + 2 * x;
-                        const float y0 = merged(o[i], o2[i], fa[x], b_too, fb[x], lsum[x], inv[x]);
-                        const float y1 = merged(o[i + 1], o2[i + 1], fa[x], b_too, fb[x], lsum[x], inv[x]);
+                        const float y0 = merged(o[i], o2[i], fa[x], b_too, fb[x], none[x]);
+                        const float y1 = merged(o[i + 1], o2[i + 1], fa[x], b_too, fb[x], none[x]);
                         if (rv[x] && whole) orow[x][(d + 8 * k) / 2] = pack_bf16x2(y0, y1);
                         else if (rv[x]) prow[x][(d + 8 * k) / 2 * kPair] = make_float2(y0, y1);
                     }
