@@ -1266,11 +1266,13 @@ tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensor
                             ks = ks == kKStages - 1 ? 0 : ks + 1;
                             k_phase ^= ks == 0 ? 1u : 0u;
                         }
+                        // the queries' buffers are free once the piece's last scores are there
+                        if (i + 3 == steps) {
+                            tc::commit(bar(kBarQEmpty + b0));
+                            if (two) tc::commit(bar(kBarQEmpty + 1));
+                        }
                     }
                 }
-                // the queries' buffers are free once this piece's MMAs are done
-                if (ok) tc::commit(bar(kBarQEmpty + b0));
-                if (ok && two) tc::commit(bar(kBarQEmpty + 1));
             }
             ok = __all_sync(0xffffffffu, ok);
             ++piece;
