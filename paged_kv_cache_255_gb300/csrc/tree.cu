@@ -775,6 +775,27 @@ __device__ __forceinline__ uint4 pack(const float *f) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
+// Lane i of a quad gives its 16 bytes k to lane k, as that one's i-th: a store of 32 lanes then
+// covers 64 bytes of 8 rows instead of 16 of 32.
+__device__ __forceinline__ void quad_transpose(uint4 (&x)[4], int lane) {
+#pragma unroll
+    for (int m = 1; m <= 2; m <<= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k & m) continue;
+            uint4 &lo = x[k], &hi = x[k | m];
+            uint4 v = up ? lo : hi;
+            v.x = __shfl_xor_sync(0xffffffffu, v.x, m);
+            v.y = __shfl_xor_sync(0xffffffffu, v.y, m);
+            v.z = __shfl_xor_sync(0xffffffffu, v.z, m);
+            v.w = __shfl_xor_sync(0xffffffffu, v.w, m);
+            if (up) lo = v;
+            else hi = v;
+        }
+    }
+}
+
 // What a softmax warp counts over its pieces.
 struct Streams {
     uint32_t gt = 0, ga = 0;    // key tiles before this piece, of this stream and of all
@@ -911,17 +932,10 @@ __device__ __forceinline__ bool softmax_piece(const TreeArgs &a, const volatile 
                 a.part_ml[(int64_t)slot * kPair + tile * kRows + row0 + 8 * x] = make_float2(m[x], lsum[x]);
         }
         if constexpr (R == 0) {
-            uint4 *orow = out_row(row0);
-            // 8 dims of the row
-            auto put = [&](int d, const float *y) {
-                if (rv[0] && whole) {
-                    orow[d / 8] = pack(y);
-                } else if (rv[0]) {
-                    po[(d / 4) * kPair + row0] = make_float4(y[0], y[1], y[2], y[3]);
-                    po[(d / 4 + 1) * kPair + row0] = make_float4(y[4], y[5], y[6], y[7]);
-                }
-            };
             if (two) {
+                // the rows of a quad of lanes are written together
+                uint4 *const quad = out_row(row0 & ~3) + (tid & 3);
+                const unsigned valid = __ballot_sync(0xffffffffu, rv[0]) >> (tid & 28);
 #pragma unroll 1
                 for (int d = 0; d < kHeadDim; d += 32) {
                     uint32_t o[32];
@@ -930,12 +944,24 @@ __device__ __forceinline__ bool softmax_piece(const TreeArgs &a, const volatile 
                     float y[32];
 #pragma unroll
                     for (int c = 0; c < 32; ++c) y[c] = none[0] ? 0.f : __uint_as_float(o[c]) * fa[0];
+                    if (whole) {
+                        uint4 x[4];
 #pragma unroll
-                    for (int c = 0; c < 32; c += 8) put(d + c, y + c);
+                        for (int c = 0; c < 4; ++c) x[c] = pack(y + 8 * c);
+                        quad_transpose(x, tid);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (valid >> k & 1) quad[(k / G * a.num_q_heads + k % G) * (kHeadDim / 8) + d / 8] = x[k];
+                    } else if (rv[0]) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            po[((d + c) / 4) * kPair + row0] = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
+                    }
                 }
             } else {
+                uint4 *const orow = out_row(row0);
 #pragma unroll 1
-                for (int d = 64 * wg; d < 64 * wg + 64; d += 16) {
+                for (int d = d0; d < d1; d += 16) {
                     uint32_t o[16], o2[16];
                     tc::tmem_ld16(tmem + lane + 128 + d, o);
                     tc::tmem_ld16(tmem + lane + 384 + d, o2);
@@ -944,7 +970,14 @@ __device__ __forceinline__ bool softmax_piece(const TreeArgs &a, const volatile 
 #pragma unroll
                     for (int c = 0; c < 16; ++c) y[c] = merged(o[c], o2[c], fa[0], b_too, fb[0], none[0]);
 #pragma unroll
-                    for (int c = 0; c < 16; c += 8) put(d + c, y + c);
+                    for (int c = 0; c < 16; c += 8) {
+                        if (rv[0] && whole) {
+                            orow[(d + c) / 8] = pack(y + c);
+                        } else if (rv[0]) {
+                            po[((d + c) / 4) * kPair + row0] = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
+                            po[((d + c) / 4 + 1) * kPair + row0] = make_float4(y[c + 4], y[c + 5], y[c + 6], y[c + 7]);
+                        }
+                    }
                 }
             }
         } else {
