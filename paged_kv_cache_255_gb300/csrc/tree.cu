@@ -481,39 +481,40 @@ __device__ __noinline__ void clean_v(const volatile Walk &w, int j, uint8_t *vti
     const int node0 = j * kKeys - (w.q.L - w.q.n);              // node of the tile's first key
     const int first = node0 < 0 ? -node0 : 0, left = w.q.L - j * kKeys;
     const int rows = groups_used(w, j) * kGroup - first;
+    auto place = [&](int i) {
+        return reinterpret_cast<uint4 *>(vtile + ((i >> 3) & 1) * kKVHalf + (first + (i >> 4)) * 128 + (i & 7) * 16);
+    };
     constexpr int kBatch = 4;                                   // chunks a thread has in flight
+#pragma unroll 1
     for (int i0 = thread; i0 < rows * 16; i0 += kRows * kBatch) {
         uint4 x[kBatch];
-        auto place = [&](int k) {
-            const int i = i0 + kRows * k;
-            return reinterpret_cast<uint4 *>(vtile + ((i >> 3) & 1) * kKVHalf + (first + (i >> 4)) * 128 +
-                                             (i & 7) * 16);
-        };
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            x[k] = i0 + kRows * k < rows * 16 ? *place(k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int i = i0 + kRows * k, r = first + (i >> 4);
-            uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            // an exponent of all ones is an infinity or NaN: one more carries into the sign's place
-            uint32_t found = 0;
+            const int i = i0 + kRows * k;
+            const bool real = first + (i >> 4) < left;
+            x[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < rows * 16 && real) x[k] = *place(i);
+            if (i < rows * 16 && !real) *place(i) = x[k];
+        }
+        // an exponent of all ones is an infinity or NaN: one more carries into the sign's place
+        uint32_t found = 0;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) found |= ((v[c] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-            if (i >= rows * 16) {
-            } else if (r >= left) {
-                *place(k) = make_uint4(0u, 0u, 0u, 0u);
-            } else if (found) {
+        for (int k = 0; k < kBatch; ++k)
+            for (uint32_t v : {x[k].x, x[k].y, x[k].z, x[k].w}) found |= (v & 0x7f807f80u) + 0x00800080u;
+        if (!(found & 0x80008000u)) continue;                   // as nearly all
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    if ((x[k].x & 0x7f80u) == 0x7f80u) x[k].x &= 0xffff0000u;
-                    if ((x[k].x & 0x7f800000u) == 0x7f800000u) x[k].x &= 0x0000ffffu;
-                    x[k] = make_uint4(x[k].y, x[k].z, x[k].w, x[k].x);
-                }
-                *place(k) = x[k];
-                const int node = node0 + r;
-                if (node < 32 * words) atomicOr(odd, 1u << (node >> 5));        // the others nobody sees
+        for (int i = i0; i < min(i0 + kRows * kBatch, min(left - first, rows) * 16); i += kRows) {
+            uint4 v = *place(i);
+            bool odd_one = false;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                const bool lo = (v.x & 0x7f80u) == 0x7f80u, hi = (v.x & 0x7f800000u) == 0x7f800000u;
+                odd_one |= lo || hi;
+                v = make_uint4(v.y, v.z, v.w, v.x & (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u));
             }
+            *place(i) = v;
+            const int node = node0 + first + (i >> 4);
+            if (odd_one && node < 32 * words) atomicOr(odd, 1u << (node >> 5));     // the others nobody sees
         }
     }
 }
