@@ -35,11 +35,11 @@
 //   warp 10          issues S = Q K^T and O += P V as their inputs arrive
 // Measured (calls in a graph, both kernels): 8 contexts of 32k to 131k tokens, up to 128 rows
 // a unit, 406 - 425 us, 6.4 - 6.6 TB/s of 6.79: bound by memory. 512 units of 192 to 256 rows
-// over 16 to 64 key tiles 263 - 281 us, 1110 - 1180 TFLOP/s of 1939: the tensor pipe is busy for
+// over 16 to 64 key tiles 258 - 281 us, 1110 - 1200 TFLOP/s of 1939: the tensor pipe is busy for
 // 61 % of the cycles. A step's products take 2 x (512 + 512) cycles alone, about 1400 a query
 // tile beside the other stream's TMEM traffic and the tiles' arrival (a product from shared memory
 // reads 128 B a cycle, all there is), and a stream's chain P -> PV -> S -> P is 2700. 480 units of
-// 1 to 8 tiles 42.7 us, where the floor is 21: 3 us until the plan is made, then 5 per unit
+// 1 to 8 tiles 42.1 us, where the floor is 21: 3 us until the plan is made, then 5 per unit
 // of dependent steps (tiles, S, softmax, PV, result), and 3 for the merge. A softmax with a
 // polynomial for a part of its powers of two is slower (a quarter of them: 319 us against 304):
 // the XU pipe is busy for 28 %.
@@ -636,18 +636,21 @@ __device__ __forceinline__ void wide_tile(uint32_t tS, uint32_t tO, float sc, bo
     if (nodes) {
         uint32_t v0 = vis[0], v1 = vis[1], v2 = vis[2], v3 = vis[3];
 #pragma unroll 1
-        for (int ch = 0; ch < 4; ++ch) {
-            tc::tmem_ld32(tS + 32 * ch, sr[0]);
-            tc::tmem_ld_wait();
+        for (int ch = 0; ch < 4; ch += 2) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                if (!(v0 >> c & 1)) sr[0][c] = kMasked;
-                e[c & 1] = fmaxf(e[c & 1], __uint_as_float(sr[0][c]));
+            for (int h = 0; h < 2; ++h) {
+                tc::tmem_ld_wait();
+                if (ch + h < 3) tc::tmem_ld32(tS + 32 * (ch + h + 1), sr[h ^ 1]);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    if (!(v0 >> c & 1)) sr[h][c] = kMasked;
+                    e[c & 1] = fmaxf(e[c & 1], __uint_as_float(sr[h][c]));
+                }
+                tc::tmem_st32(tS + 32 * (ch + h), sr[h]);
+                v0 = v1;
+                v1 = v2;
+                v2 = v3;
             }
-            tc::tmem_st32(tS + 32 * ch, sr[0]);
-            v0 = v1;
-            v1 = v2;
-            v2 = v3;
         }
         tc::tmem_st_wait();
     } else {
