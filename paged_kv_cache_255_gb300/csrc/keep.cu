@@ -18,6 +18,7 @@
 // pools, 21 MB read and written, 6.2 us of bytes) 14, the copy of the tables that the
 // measurement needs included.
 #include "common.cuh"
+#include "keep_path.h"
 #include "tree.h"
 
 #include "../../include/pagedattn/decode_tree.h"
@@ -53,10 +54,7 @@ __device__ __forceinline__ Draft load_draft(const KeepArgs &a, int s) {
 }
 // Whether entry i of a list continues it; `bad` when it is no -1 either.
 __device__ __forceinline__ bool continues(const int32_t *list, int i, int n, bool &bad) {
-    const int k = __ldg(list + i);
-    const bool ok = k >= 0 && k < n && (i == 0 || k > __ldg(list + i - 1));
-    bad = !ok && k != -1;
-    return ok;
+    return path_continues(__ldg(list + i), i == 0 ? 0 : __ldg(list + i - 1), i, n, bad);
 }
 
 __global__ void __launch_bounds__(kThreads) keep_kernel(const KeepArgs a, const PoolSet pools) {
@@ -77,7 +75,8 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const KeepArgs a, const 
             atomicMin(&s_count, i);
             continue;
         }
-        // rows by token, or (head-major) by block, head 0, token
+        // Rows by token, or (head-major) by block, head 0, token. (An entry behind the list's end
+        // that looks like one of a path is looked up too: its places are the draft's.)
         const int32_t *table = a.block_tables + (int64_t)s * a.max_blocks;
         auto row = [&](int t) -> int64_t {
             const int b = __ldg(table + (t >> lb));
