@@ -42,9 +42,9 @@ extern "C" {
  *
  * Rows of out outside [query_start_loc[0], query_start_loc[num_seqs]) (the
  * padding of a batch of fixed size) are not written, and nothing of them enters a
- * result. Values of query_start_loc are clamped to [0, total_q]; one that decreases
- * gives unspecified results within the buffers. With n above L, tokens before the
- * first do not exist. The call plans on the device, so a captured call follows the
+ * result. Values of query_start_loc are clamped to [0, total_q]; where one decreases,
+ * results are unspecified, or not written, and stay within the buffers. With n above L,
+ * tokens before the first do not exist. The call plans on the device, so a captured call follows the
  * contents of its arrays; results do not depend on timing.
  *
  * Requirements: pa_decode's for heads, blocks, pools and alignment (either layout);

@@ -15,6 +15,7 @@
 #include "rotary.h"
 #include "shared.h"
 #include "tree.h"
+#include "tree_plan.h"
 
 namespace {
 
@@ -778,10 +779,10 @@ pa_status_t pa_decode_tree(const void *q, const void *k_cache, const void *v_cac
     if (num_seqs < 0) return PA_ERR_INVALID_ARG;
     if ((int64_t)total_q * num_q_heads > INT32_MAX) return PA_ERR_UNSUPPORTED;
     if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX - 127) return PA_ERR_UNSUPPORTED;
-    // the call counts key tiles of 128 and a few places more, of all units of 256 rows, in 32 bits
-    const int64_t units = (int64_t)total_q * pa::decode_group_pad(num_q_heads / num_kv_heads) / 256 + num_seqs;
-    const int64_t tiles = ((int64_t)max_blocks_per_seq * block_size + 127) / 128 + 8;
-    if (tiles * num_kv_heads > INT32_MAX || units > INT32_MAX / (tiles * num_kv_heads)) return PA_ERR_UNSUPPORTED;
+    // the call counts places of all units in 32 bits
+    if (!pa::tree_places_fit(total_q, pa::decode_group_pad(num_q_heads / num_kv_heads), num_seqs,
+                             (int64_t)max_blocks_per_seq * block_size, num_kv_heads))
+        return PA_ERR_UNSUPPORTED;
     if (nothing_to_do) return PA_OK;
     if (!query_start_loc || !tree_mask || (reinterpret_cast<uintptr_t>(tree_mask) & 7u)) return PA_ERR_INVALID_ARG;
     const int sms = current_sm_count();

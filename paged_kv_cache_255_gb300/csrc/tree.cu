@@ -54,6 +54,7 @@
 #include "shared.h"
 #include "tcgen05.cuh"
 #include "tree.h"
+#include "tree_plan.h"
 
 namespace pa {
 
@@ -63,7 +64,8 @@ namespace {
 
 constexpr int kRows = 128;                              // rows per query tile
 constexpr int kPair = 2 * kRows;
-constexpr int kKeys = 128;                              // keys per K/V tile
+constexpr int kKeys = kTreeKeys;                        // keys per K/V tile
+static_assert(kPair == kTreePairRows && kKeys == 128, "two tiles of 128 rows, tiles of 128 keys");
 constexpr int kKStages = 3;
 constexpr int kVStages = 2;
 constexpr int kSoftmaxThreads = 256;
@@ -78,7 +80,7 @@ constexpr int kCombineRows = 8;                         // rows merged at a time
 // Places of a unit besides its tiles, for its start and its end: at 0, 1, 2, 3 a batch of 512
 // units of 16 to 64 tiles takes 297, 285, 282, 274 us, and 480 units of 1 to 8 tiles 55.4,
 // 47.3, 42.3, 42.6; at 4 the first gains 3 more and the second loses 1.
-constexpr int kUnitPlaces = 3;
+constexpr int kUnitPlaces = kTreeUnitPlaces;
 constexpr uint32_t kQBytes = kRows * kRowBytes;         // 32 KB: 2 halves of [128][128 B]
 constexpr uint32_t kQHalf = kRows * 128;
 constexpr uint32_t kKVBytes = kKeys * kRowBytes;
@@ -108,6 +110,7 @@ constexpr int kOddSets = 4;                                       // of the piec
 constexpr uint32_t kOffOdd = kOffWalk + kWalkBytes * (kWarpsAll + 1);   // 32 i + 31 have V that is not finite
 constexpr uint32_t kOffHalves = kOffOdd + 4 * kOddSets;           // [2][128] float2; before that the plan's sums
 constexpr uint32_t kSmemBytes = kOffHalves + 2 * kRows * 8;
+static_assert(kOffHalves % 8 == 0, "pairs of floats, and a 64-bit count");
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdescS = tc::idesc_bf16(128, kKeys, false);
@@ -212,31 +215,12 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 
 // -- plan ------------------------------------------------------------------------
 
-// A sequence's part of the work.
-struct Seq {
-    int q0, n, L;       // first query row, query rows (nodes), tokens
-    int nt, pairs;      // key tiles; units of 256 query rows
-};
+using Seq = TreeSeq;
 
 template <int G>
 __device__ __noinline__ Seq load_seq(const TreeArgs &a, int s) {
     const int64_t max_len = (int64_t)a.max_blocks_per_seq << a.block_size_log2;     // below 2^31
-    const int64_t l = __ldg(a.context_lens + s);
-    int q0 = __ldg(a.starts + s), q1 = __ldg(a.starts + s + 1);
-    q0 = q0 < 0 ? 0 : (q0 > a.total_q ? a.total_q : q0);
-    q1 = q1 < q0 ? q0 : (q1 > a.total_q ? a.total_q : q1);
-    Seq r;
-    r.q0 = q0;
-    r.n = q1 - q0;
-    r.L = (int)(l < 0 ? 0 : (l > max_len ? max_len : l));
-    r.nt = r.L > 0 ? (r.L + kKeys - 1) / kKeys : 1;     // an empty sequence's zeros are written by one tile
-    r.pairs = (int)(((int64_t)r.n * G + kPair - 1) / kPair);
-    return r;
-}
-
-// Places of a sequence's units. (The host has ruled out 2^31 places.)
-__device__ __forceinline__ int seq_places(const Seq &q, int num_kv_heads) {
-    return q.pairs * num_kv_heads * (q.nt + kUnitPlaces);
+    return tree_seq(__ldg(a.starts + s), __ldg(a.starts + s + 1), __ldg(a.context_lens + s), a.total_q, max_len, G);
 }
 
 // A share's walk over the flat space of its lane, sequence by sequence, KV head, pair, key
@@ -311,6 +295,22 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {
     return v;
 }
 
+// Whether the places of all sequences are below 2^31. The host has seen to it for rows that
+// are one sequence's each; where a start is below the one before it, they may be several's and
+// their places many times as many, and what is counted in 32 bits would lead anywhere. All
+// threads call it. (Rare; `total` is scratch.)
+template <int G>
+__device__ __noinline__ bool places_fit(const TreeArgs &a, unsigned long long *total) {
+    if (threadIdx.x == 0) *total = 0;
+    __syncthreads();
+    unsigned long long mine = 0;
+#pragma unroll 1
+    for (int s = threadIdx.x; s < a.num_seqs; s += kThreads) mine += tree_seq_places(load_seq<G>(a, s), a.num_kv_heads);
+    atomicAdd(total, mine);
+    __syncthreads();
+    return *static_cast<volatile unsigned long long *>(total) <= INT_MAX;
+}
+
 // The places of a lane, its shares, and this CTA's first piece (in `first`, shared memory);
 // false when it has none. All threads call it; `sums` is scratch. A chain of dependent steps
 // that every CTA goes through before its first tile: of up to kThreads sequences thread i
@@ -325,10 +325,12 @@ __device__ __noinline__ bool plan_share(const TreeArgs &a, Walk *first, volatile
     int own = 0;                                // places of this thread's sequence of the first kThreads
     unsigned later = 0;                         // of those after them
     unsigned most = 0, least = INT_MAX;         // pairs of a sequence
+    bool falls = false;                         // a start is below the one before it
 #pragma unroll 1
     for (int s = tid; s < S; s += kThreads) {
         const Seq q = load_seq<G>(a, s);
-        const int places = seq_places(q, Hkv);
+        const int places = tree_seq_places(q, Hkv);
+        falls |= q.n < 0;
         if (s == tid) {
             mine = q;
             own = places;
@@ -350,7 +352,8 @@ __device__ __noinline__ bool plan_share(const TreeArgs &a, Walk *first, volatile
         sums[96 + warp] = later;
     }
     if (tid == 0) first->T1 = -1;               // nothing found yet
-    __syncthreads();
+    if (__syncthreads_or(falls) && !places_fit<G>(a, reinterpret_cast<unsigned long long *>(const_cast<int *>(sums + 128))))
+        return false;
     // every warp adds up all warps' sums
     const bool there = lane < kWarpsAll;
     const int x = there ? sums[lane] : 0;
@@ -410,7 +413,7 @@ __device__ __noinline__ bool plan_share(const TreeArgs &a, Walk *first, volatile
         own = 0;
         if (c0 + tid < S) {
             mine = load_seq<G>(a, c0 + tid);
-            own = seq_places(mine, Hkv);
+            own = tree_seq_places(mine, Hkv);
         }
         scan = warp_scan(own, lane);
         __syncthreads();                        // the sums before have been read
