@@ -67,12 +67,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if failed:
         raise RuntimeError("nvcc failed:\n" + "\n".join(f"{s}:\n{o}" for s, o in failed))
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    # the runtime that torch has loaded, not a second one of our own: its launches and torch's
-    # allocations then share their state (2 us of an 18 us call that allocates); -ldl: NVTX
+    # with the CUDA runtime inside, so that a program needs this file and a driver alone; -ldl: NVTX
     # loads a tool by dlopen
-    libs = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "lib64")
-    subprocess.run([nvcc, *ARCH, "-shared", "--cudart=shared", "-o", tmp, *objs, "-ldl", "-Xlinker",
-                    f"-rpath,{libs}"], check=True)
+    subprocess.run([nvcc, *ARCH, "-shared", "--cudart=static", "-o", tmp, *objs, "-ldl"], check=True)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 
