@@ -20,9 +20,11 @@ extern "C" {
  * rot_dim / 2 pairs, the others pass. Pair i is dims (2 i, 2 i + 1) when
  * interleaved, dims (i, i + rot_dim / 2) otherwise; at position p
  *   (a, b) -> amplitude * (a cos x - b sin x, b cos x + a sin x),  x = p * frequency of pair i.
- * turns[i] is that frequency in turns per token, modulo one turn, in units of
- * 2^-64: the angle of any 32-bit position is exact to 2^-32 turns. Host memory,
- * filled by one of the two calls below and read during the calls that take it.
+ * turns[i] is that frequency, a double in radians per token, in turns modulo one
+ * turn, in units of 2^-64 and to half a unit: its product with a 32-bit position is
+ * the angle modulo one turn to 2^-34 turns. Sine and cosine are taken in fp32, of the
+ * angle rounded to 24 bits (2^-26 turns at most). Host memory, filled by one of the two
+ * calls below and read during the calls that take it.
  */
 typedef struct {
     int32_t rot_dim;

@@ -6,11 +6,12 @@
 //
 //   y = x w / sqrt(mean(x^2) + eps);  (a, b) -> A (a cos px - b sin px, b cos px + a sin px)
 //
-// The angle: pair i turns F_i 2^-64 of a circle per token, F_i a 64-bit whole
-// number, so the low 64 bits of p F_i are the angle modulo one turn for any 32-bit
-// position p, with an error of p 2^-64 turns (the frequency in fp32 would be off by
-// a tenth of a radian at p = 2^20). Its upper 32 bits as a signed fraction go to
-// sincospif, whose argument then needs no reduction.
+// The angle: pair i turns F_i 2^-64 of a circle per token, F_i a 64-bit whole number that
+// is its frequency (a double) to half a unit, so the low 64 bits of p F_i are the angle
+// modulo one turn for any 32-bit position p to |p| 2^-65 turns (the frequency in fp32
+// would be off by a tenth of a radian at p = 2^20). The upper 32 bits as a signed fraction,
+// rounded to fp32 (2^-26 of a turn at most), go to sincospif, whose argument then needs no
+// reduction.
 //
 // One row of 256 bytes is 8 lanes' work: a lane holds 8 pairs, which are two
 // 16-byte chunks (neighbours when interleaved, rot_dim / 2 dims apart otherwise), so
@@ -248,16 +249,35 @@ cudaError_t launch(const RotateArgs &a, unsigned grid, cudaStream_t stream) {
 
 }  // namespace
 
+namespace {
+
+// radians / 2 pi in units of 2^-64 of a turn, modulo one turn, to the nearest: the 53 bits of a
+// double times 1 / 2 pi to 128 bits behind the point, in whole numbers. (In doubles the
+// quotient is off by 2^-54 of itself and more: at position 2^31 a frequency of 1 by 2^-25 turns,
+// one of 2^20 by 2^-5.)
+uint64_t turns_of(double radians) {
+    constexpr uint64_t kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;    // 2^128 / 2 pi
+    int e;
+    const uint64_t m = (uint64_t)std::ldexp(std::frexp(std::fabs(radians), &e), 53);    // |radians| = m 2^(e - 53)
+    const unsigned __int128 lo = (unsigned __int128)m * kLo, hi = (unsigned __int128)m * kHi + (uint64_t)(lo >> 64);
+    const uint64_t product[3] = {(uint64_t)lo, (uint64_t)hi, (uint64_t)(hi >> 64)};     // below 2^179
+    auto word = [&](int i) { return i < 3 ? product[i] : 0; };
+    const int shift = 53 + 128 - 64 - e;        // 96 and up: frequencies are 2^20 at most
+    auto from_bit = [&](int b) {                // 64 bits of the product
+        return word(b / 64) >> b % 64 | (b % 64 ? word(b / 64 + 1) << (64 - b % 64) : 0);
+    };
+    const uint64_t turns = from_bit(shift) + (from_bit(shift - 1) & 1);
+    return radians < 0 ? 0 - turns : turns;
+}
+
+}  // namespace
+
 void rotary_fill(pa_rotary_t *r, int rot_dim, int interleaved, const double *radians, double amplitude) {
     std::memset(r, 0, sizeof(*r));
     r->rot_dim = rot_dim;
     r->interleaved = interleaved ? 1 : 0;
     r->amplitude = (float)amplitude;
-    for (int i = 0; i < rot_dim / 2; ++i) {
-        double turns = radians[i] / (2 * 3.14159265358979323846);
-        turns -= std::floor(turns);             // of one turn; 1.0 where it rounds up to a whole one
-        r->turns[i] = turns < 1.0 ? (uint64_t)std::ldexp(turns, 64) : 0;
-    }
+    for (int i = 0; i < rot_dim / 2; ++i) r->turns[i] = turns_of(radians[i]);
 }
 
 void rotary_scaled(double *radians, int rot_dim, double base, pa_rotary_scaling_t scaling, double factor,
