@@ -26,13 +26,13 @@
 // (6.53 TB/s, 0.96); 2047 tokens of 48 heads (7.4 us of bytes) 14.5, where a warp has a
 // handful of quads; 4 tokens 2.4, a launch.
 #include <algorithm>
-#include <climits>
 #include <cmath>
 #include <cstring>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "rotary.h"
+#include "rotary_split.h"
 
 namespace pa {
 
@@ -311,16 +311,9 @@ cudaError_t take_rotary_error(cudaStream_t stream, int *code) {
 
 cudaError_t launch_rotate(RotateArgs a, bool append, bool interleaved, int sm_count, cudaStream_t stream) {
     const int rows = a.num_q_heads + a.num_kv_heads * (append ? 2 : 1);
-    const int all = (rows + 3) / 4;             // quads of a token
-    // A warp takes as many of a token's quads as leave the GPU full of warps: the sines are
-    // then computed once for all of them. (One wave of 24 warps an SM, each going from token
-    // to token, instead of CTAs in turn: 16384 tokens of 40 heads 58.9 us against 52.5, of
-    // 2047 x 48 19.1 against 14.5.)
-    const int64_t quads = a.num_tokens * all / ((int64_t)sm_count * 32);
-    a.quads = (int)(quads < 1 ? 1 : (quads > all ? all : quads));
-    a.slices = (all + a.quads - 1) / a.quads;
-    while (a.num_tokens * a.slices > INT32_MAX) --a.slices;     // items are counted in 32 bits
-    a.quads = (all + a.slices - 1) / a.slices;      // alike
+    const RotarySplit split = rotary_split(a.num_tokens, rows, sm_count);
+    a.quads = split.quads;
+    a.slices = split.slices;
     int64_t grid = (a.num_tokens * a.slices + kWarps - 1) / kWarps;
     if (grid > (int64_t)sm_count * kCtasPerSm * 3) grid = (int64_t)sm_count * kCtasPerSm * 3;
     if (append)
