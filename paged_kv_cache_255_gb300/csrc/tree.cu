@@ -13,8 +13,9 @@
 // A unit is 256 query rows (two tiles of 128: 128 / G tokens x G heads, G = g rounded up
 // to a power of two) of one (sequence, KV head); its keys go in tiles of 128. The flat
 // space of all units' key tiles, and kUnitPlaces places more a unit for what it costs
-// besides them, is cut into equal contiguous shares, one CTA per SM each, planned by
-// every CTA from the lengths and starts. A unit that one share holds whole is written
+// besides them, is cut into equal contiguous shares, one CTA per SM each (but for what
+// side by side lanes leave over: tree_lanes), planned by every CTA from the lengths and
+// starts. A unit that one share holds whole is written
 // as it ends; one that several share leaves a part per share in fp32, and
 // tree_combine_kernel merges them by their running maxima and sums.
 //
@@ -364,7 +365,7 @@ __device__ __noinline__ bool plan_share(const TreeArgs &a, Walk *first, volatile
     W = chunk;
     if (S > kThreads) W += (int)__reduce_add_sync(0xffffffffu, there ? (unsigned)sums[96 + lane] : 0u);
     // where all have the same number of pairs, the pairs are lanes
-    const int lanes = most == least && (int)most <= a.workers ? (int)most : 1;
+    const int lanes = tree_lanes((int)most, (int)least, a.workers);
     const bool side = lanes > 1;
     shares = a.workers;
     int w = blockIdx.x, my_lane = 0;
@@ -390,10 +391,9 @@ __device__ __noinline__ bool plan_share(const TreeArgs &a, Walk *first, volatile
             const int rem = T0 - excl, places = mine.nt + kUnitPlaces;
             const int unit = rem / places;
             int kvh = unit, pair = 0;
-            if (mine.pairs > lanes) {
-                const int per_head = side ? mine.pairs / lanes : mine.pairs;
-                kvh = unit / per_head;
-                pair = unit - kvh * per_head;
+            if (mine.pairs > lanes) {           // (not side by side)
+                kvh = unit / mine.pairs;
+                pair = unit - kvh * mine.pairs;
             }
             first->T = T0;
             first->T1 = T1;

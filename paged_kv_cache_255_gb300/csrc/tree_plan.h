@@ -44,6 +44,17 @@ PA_TREE_FN int tree_seq_places(const TreeSeq &q, int num_kv_heads) {
     return q.pairs * num_kv_heads * (q.nt + kTreeUnitPlaces);
 }
 
+// Lanes that units are shared in: where all sequences with units have the same number of
+// them a KV head, these go side by side and read the same keys together, each lane over
+// workers / lanes CTAs, as long as the CTAs left over, workers modulo lanes, are an eighth at
+// most. Otherwise there is one lane, whose shares take every CTA. Of 152 CTAs, us side by side
+// and in one lane: 8 units a KV head over 100000 tokens, 8 heads, 545 and 591; 13 (9 CTAs left
+// over) 942 and 1066; 17 (16) 645 and 740; one head over 16000 tokens 22 (20) 48.9 and 48.4,
+// 32 (24) 67 and 64, 52 (48) 125 and 99, 77 (75) 231 and 143.
+PA_TREE_FN int tree_lanes(int most, int least, int workers) {
+    return most > 1 && most == least && most <= workers && workers % most <= workers / 8 ? most : 1;
+}
+
 // Whether the places of all sequences of a call, whatever its lengths, are below 2^31, as
 // long as no start is below the one before it: the rows of two sequences are then not the
 // same, and there are total_q of them in all. The kernel counts again where one is.

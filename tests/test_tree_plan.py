@@ -73,3 +73,32 @@ int main()
 def test_places_fit_unless_the_starts_fall(tmp_path):
     rc, out, log = run(tmp_path, COUNTS)
     assert rc == 0 and out == "taken 1 bad 0 past 1", log
+
+
+LANES = r"""
+#include <cstdio>
+#include "tree_plan.h"
+int main()
+{
+    long bad = 0, side = 0;
+    for (int workers = 1; workers <= 255; ++workers)
+        for (int pairs = 1; pairs <= 600; ++pairs) {
+            const int lanes = pa::tree_lanes(pairs, pairs, workers);
+            side += lanes > 1;
+            bad += lanes != 1 && lanes != pairs;                // a unit of each sequence and head to a lane
+            const int busy = workers / lanes * lanes;
+            bad += busy < 1 || (workers - busy) * 8 > workers;  // CTAs that no share is for
+            bad += pairs > 1 && pa::tree_lanes(pairs, pairs - 1, workers) != 1;
+        }
+    bad += pa::tree_lanes(0, INT_MAX, 152) != 1;                // no units at all
+    const int good[] = {2, 3, 8, 17, 76, 152};
+    for (int pairs : good) bad += pa::tree_lanes(pairs, pairs, 152) != pairs;
+    std::printf("side %d bad %ld\n", side > 0, bad);
+    return bad != 0;
+}
+"""
+
+
+def test_lanes_leave_few_ctas_without_a_share(tmp_path):
+    rc, out, log = run(tmp_path, LANES)
+    assert rc == 0 and out == "side 1 bad 0", log
