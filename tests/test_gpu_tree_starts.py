@@ -65,3 +65,29 @@ def test_padded_starts_are_empty_sequences():
     out = torch.full_like(b.q, 77.0)
     b.run(out=out)
     assert pa.take_device_error() == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("starts", [[0, 7, 3, 18], [18, 3, 0, -4], [-5, 3, 7, 900], [5, 5, 5, 5], [0, 18, 0, 18],
+                                    [2 ** 31 - 1, -(2 ** 31), 2 ** 31 - 1, 0]])
+@pytest.mark.parametrize("Hq,Hkv,hm", [(8, 2, False), (33, 3, True)])
+def test_starts_of_any_kind_change_nothing_around_the_buffers(starts, Hq, Hkv, hm):
+    b = Batch([30, 300, 20], [5, 9, 4], Hq, Hkv, hm=hm)
+    out, out_same = guarded(b.q.numel(), torch.bfloat16, 77.0)
+    ws, ws_same = guarded(pa.decode_tree_workspace_size(Hq, Hkv), torch.uint8, 255)
+    inputs = [x.clone() for x in (b.tables, b.lens, b.mask)]
+    kv = [x.view(torch.int16).clone() for x in (b.q, b.k, b.v)]
+    b.starts.copy_(torch.tensor(starts, dtype=torch.int32))
+    for _ in range(2):      # also over what a call has left in the workspace
+        b.run(out=out.view(b.q.shape), workspace=ws)
+        assert pa.take_device_error() in (0, 4)
+        assert out_same() and ws_same()
+    assert all(torch.equal(x, y) for x, y in zip((b.tables, b.lens, b.mask), inputs))
+    assert all(torch.equal(x.view(torch.int16), y) for x, y in zip((b.q, b.k, b.v), kv))
+
+
+@pytest.mark.parametrize("hm", [False, True])
+def test_a_chain_is_prefill(hm):
+    """A chain's rows see what a prompt's last rows see."""
+    b = Batch([300, 1, 64, 0], [4, 20, 130, 33], 16, 8, hm=hm, masks=lambda r, n: [(2 << i) - 1 for i in range(n)])
+    b.check()
+    b.check(pa.prefill(b.q, b.k, b.v, b.tables, b.lens, b.starts, b.scale, head_major=hm))
