@@ -88,8 +88,10 @@ PA_API pa_status_t pa_rotary_init_frequencies(pa_rotary_t *rotary, int rot_dim, 
  * and strides); other overlaps give unspecified results.
  *
  * Requirements: head_dim == 128; addresses 16-byte aligned; strides not negative
- * and multiples of 8, those of outputs such that no two rows overlap; eps finite,
- * not negative; heads of both together at most 2^20; num_tokens below 2^31.
+ * and multiples of 8; of an output's two strides one is 128 or more and the other
+ * steps over all rows that the first one leads to (heads inside tokens or tokens
+ * inside heads; rows in turn from both are refused, also where none overlap); eps
+ * finite, not negative; heads of both together at most 2^20; num_tokens below 2^31.
  */
 PA_API pa_status_t pa_rotate(const void *q, int64_t q_token_stride, int64_t q_head_stride,
                              void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,

@@ -277,7 +277,7 @@ bool rows_ok(const void *p, int64_t tokens, int64_t token, int heads, int64_t he
     return p && aligned16(p) && ok(tokens, token) && ok(heads, head);
 }
 
-// Whether no two rows of an output overlap.
+// Whether an output's rows lie apart: heads inside tokens, or tokens inside heads.
 bool rows_apart(int64_t tokens, int64_t token, int heads, int64_t head) {
     const int64_t D = pa::kHeadDimPublic;
     if (tokens <= 1) return heads <= 1 || head >= D;

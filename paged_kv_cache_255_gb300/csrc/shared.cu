@@ -650,7 +650,7 @@ shared_prefix_kernel(const DecodeArgs a, const SharedArgs sh,
                 }
                 const float mb = m == -INFINITY ? 0.f : m;
                 // P = 2^(S sc - m), rounded to bf16 for the second product: its
-                // error of 2^-9 per weight averages out over the keys, and the
+                // error of up to 2^-8 of a weight averages out over the keys, and the
                 // output is rounded to bf16 as well
                 float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

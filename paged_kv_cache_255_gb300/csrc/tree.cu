@@ -78,9 +78,10 @@ constexpr int kWarpsAll = kThreads / 32;
 constexpr int kGroup = 16;                              // tokens per MMA of P V
 constexpr int kGroups = kKeys / kGroup;                 // 8
 constexpr int kCombineRows = 8;                         // rows merged at a time
-// Places of a unit besides its tiles, for its start and its end: at 0, 1, 2, 3 a batch of 512
-// units of 16 to 64 tiles takes 297, 285, 282, 274 us, and 480 units of 1 to 8 tiles 55.4,
-// 47.3, 42.3, 42.6; at 4 the first gains 3 more and the second loses 1.
+// Places of a unit besides its tiles, for its start and its end: at 0, 1, 2, 3, 4 a batch of 512
+// units of 16 to 64 tiles takes 275, 270, 267, 261, 261 us, 480 units of 1 to 8 tiles 53.3,
+// 45.3, 41.8, 42.1, 43.2, a few small units 10.85, 11.0, 10.9, 10.8, 11.1, and 64 units of 256 to
+// 1024 tiles 413 at each.
 constexpr int kUnitPlaces = kTreeUnitPlaces;
 constexpr uint32_t kQBytes = kRows * kRowBytes;         // 32 KB: 2 halves of [128][128 B]
 constexpr uint32_t kQHalf = kRows * 128;
@@ -581,9 +582,10 @@ struct QBuffers {
 // Scores S from TMEM (of -Q, where the scale is negative, so that sc is positive), the masked
 // ones -infinity; the running max m (log2 units) is raised
 // only when the tile exceeds it by 2^8: weights stay below 2^8, far inside fp32 and bf16
-// range, and O is rescaled rarely. P = 2^(S sc - m), rounded to bf16 for the second product:
-// its error of 2^-9 per weight averages out over the keys, and the output is rounded
-// to bf16 as well. The sum is of the exact weights.
+// range, and O is rescaled rarely. P = 2^(S sc - m), rounded to bf16 for the second product,
+// whose operands have to be: its error of up to 2^-8 of a weight averages out over the keys
+// (0.0019 to 0.0024 of a result's length against 64 bits, where rounding the result itself is
+// 0.0017). The sum is of the exact weights.
 
 // The new max for a tile whose largest raw score is `most` (-infinity: all masked); the
 // factor on what was summed before (1 when the max stays).
